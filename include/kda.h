@@ -367,6 +367,120 @@ kda_status kda_prologue(const void *q_raw, const void *k_raw, const void *v_raw,
                         void *conv_final, void *stream);
 
 /*
+ * Linear attention with one decay per head -- the recurrence above without the delta rule, and
+ * with a scalar decay (the state-space row of the mapping table in Kimi K3 -- Architecture
+ * Notes, section 1.2, is a decay of this kind). Per sequence and value head h, with the query /
+ * key head h / (H / H_k):
+ *
+ *     S_t = e^{g_t} S_{t-1} + k_t v_t^T ,    o_t = scale * S_t^T q_t
+ *
+ * kda_linear_prefill runs packed variable-length sequences, kda_linear_decode one token for B
+ * sequences. Layouts, alignment, aliasing and error rules are those of kda_prefill and
+ * kda_decode; the differences:
+ *
+ *   H, H_k       value heads and query / key heads; H a multiple of H_k
+ *   q, k         [total_tokens, H_k, d_k] (decode: [B, H_k, d_k])   in_dtype
+ *   log_decay    g, fp32: [total_tokens, H] (decode: [B, H]) with decay_per_token = 1, or one
+ *                constant per head [H] with decay_per_token = 0. Any value up to 0 including
+ *                -infinity (the state is forgotten); a positive g grows the state and is computed
+ *                while e^g and the state stay finite. NaN propagates. No clamp is applied.
+ *   workspace    (prefill) as in kda_prefill, of kda_linear_prefill_workspace_size() bytes: with
+ *                it, sequences longer than a CTA's share of the call are cut into segments that
+ *                run side by side; with less, every (sequence, head) runs from end to end. It may
+ *                not be shared by calls that run at the same time (two captured graphs that may
+ *                replay together need one each).
+ *   force_recurrent (prefill) nonzero runs the fp32 token-recurrent kernel
+ *
+ * Sizes: 1 <= d_k, d_v <= 128, H, H_k >= 1; decode needs B >= 1. Results are accumulated in fp32
+ * and states are fp32.
+ */
+typedef struct kda_linear_prefill_params {
+  uint32_t struct_size;       /* sizeof the struct; any other value is KDA_ERR_INVALID_ARG   */
+  kda_dtype in_dtype, out_dtype;
+  int32_t num_seqs, H, H_k, d_k, d_v;
+  int32_t decay_per_token;    /* 1: log_decay [total_tokens, H], 0: [H]                      */
+  int32_t force_recurrent;
+  int64_t total_tokens;
+  const void *q, *k;          /* [total_tokens, H_k, d_k]                                    */
+  const void *v;              /* [total_tokens, H, d_v]                                      */
+  const float *log_decay;
+  const int32_t *cu_seqlens;  /* [num_seqs + 1]                                              */
+  const float *init_state;    /* [num_seqs, H, d_k, d_v] or NULL                             */
+  void *out;                  /* [total_tokens, H, d_v], out_dtype                           */
+  float *final_state;         /* [num_seqs, H, d_k, d_v] or NULL; may equal init_state       */
+  void *workspace;            /* device scratch or NULL                                      */
+  size_t workspace_bytes;
+  float scale;
+} kda_linear_prefill_params;
+
+typedef struct kda_linear_decode_params {
+  uint32_t struct_size;
+  kda_dtype in_dtype, out_dtype;
+  int32_t B, H, H_k, d_k, d_v;
+  int32_t decay_per_token;    /* 1: log_decay [B, H], 0: [H]                                 */
+  float scale;
+  const void *q, *k;          /* [B, H_k, d_k]                                               */
+  const void *v;              /* [B, H, d_v]                                                 */
+  const float *log_decay;
+  float *state;               /* [B, H, d_k, d_v], updated in place                          */
+  void *out;                  /* [B, H, d_v], out_dtype                                      */
+} kda_linear_decode_params;
+
+kda_status kda_linear_prefill(const kda_linear_prefill_params *params, void *stream);
+kda_status kda_linear_decode(const kda_linear_decode_params *params, void *stream);
+
+/*
+ * Bytes of workspace kda_linear_prefill can use for these sizes (0: none). Pure host function, no
+ * CUDA call; the same arguments always give the same answer.
+ */
+size_t kda_linear_prefill_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t H,
+                                         int32_t d_k, int32_t d_v, kda_dtype in_dtype,
+                                         kda_dtype out_dtype, int32_t force_recurrent);
+
+/*
+ * kda_block_norm -- between two blocks of a residual stream x: the norm after the block that
+ * wrote y, its gate and residual scale, and the norm before the next block, in one pass. Per row
+ * of D channels:
+ *
+ *     n  = post_weight (*) y / sqrt(mean(y^2) + post_eps)     post_norm = 1
+ *     n  = y                                                  post_norm = 0
+ *     x' = x + scale * channel_scale (*) Sigmoid(gate) (*) n
+ *     h  = pre_weight (*) x' / sqrt(mean(x'^2) + pre_eps)
+ *
+ *   x            [rows, D] x_dtype: the residual stream
+ *   y            [rows, D] y_dtype: the block's output, or NULL (x' = x: only the norm before)
+ *   gate         gate logits in y_dtype: [rows, D] with KDA_GATE_CHANNEL, [rows] with
+ *                KDA_GATE_ROW, NULL with KDA_GATE_NONE (factor 1)
+ *   post_weight, channel_scale, pre_weight   [D] fp32, or NULL for ones
+ *   residual_out [rows, D] x_dtype, written with x', or NULL; may equal x
+ *   out          [rows, D] out_dtype, written with h, or NULL (not both NULL). h is formed from
+ *                x' in fp32, before x' is rounded to x_dtype
+ *
+ * Without y there is no gate, post_weight or channel_scale (NULL) and post_norm is 0; post_weight
+ * needs post_norm = 1; pre_weight needs out. Outputs overlap no input and not each other
+ * (residual_out == x excepted). x, y, gate and the outputs are 16-byte aligned, the weights too.
+ * Sizes: rows >= 0, 1 <= D <= 16384. eps finite and >= 0; a row of zeros with eps = 0 gives NaN,
+ * as the formula does. Reads and writes each tensor once.
+ */
+typedef enum { KDA_GATE_NONE = 0, KDA_GATE_CHANNEL = 1, KDA_GATE_ROW = 2 } kda_gate_form;
+
+typedef struct kda_block_norm_params {
+  uint32_t struct_size;
+  kda_dtype x_dtype, y_dtype, out_dtype;
+  kda_gate_form gate_form;
+  int32_t post_norm;
+  int32_t D;
+  float scale;
+  int64_t rows;
+  const void *x, *y, *gate;
+  const float *post_weight, *channel_scale, *pre_weight;
+  void *residual_out, *out;
+  float post_eps, pre_eps;
+} kda_block_norm_params;
+
+kda_status kda_block_norm(const kda_block_norm_params *params, void *stream);
+
+/*
  * kda_check_device_error -- reads and clears the library's device error word in
  * one atomic exchange, enqueued on `stream` behind the work already there, then
  * synchronises `stream` and returns what the word held: KDA_OK, KDA_ERR_TIMEOUT

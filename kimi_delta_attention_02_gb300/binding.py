@@ -55,6 +55,40 @@ class DecodeParams(ctypes.Structure):
                 ("l2_eps", ctypes.c_float)]
 
 
+class LinearPrefillParams(ctypes.Structure):
+    """``kda_linear_prefill_params`` of include/kda.h, field for field."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("H", ctypes.c_int32), ("H_k", ctypes.c_int32), ("d_k", ctypes.c_int32),
+                ("d_v", ctypes.c_int32), ("decay_per_token", ctypes.c_int32), ("force_recurrent", ctypes.c_int32),
+                ("total_tokens", ctypes.c_int64), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("log_decay", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p),
+                ("init_state", ctypes.c_void_p), ("out", ctypes.c_void_p), ("final_state", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("scale", ctypes.c_float)]
+
+
+class LinearDecodeParams(ctypes.Structure):
+    """``kda_linear_decode_params`` of include/kda.h, field for field."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("H_k", ctypes.c_int32), ("d_k", ctypes.c_int32),
+                ("d_v", ctypes.c_int32), ("decay_per_token", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("log_decay", ctypes.c_void_p), ("state", ctypes.c_void_p), ("out", ctypes.c_void_p)]
+
+
+KDA_GATE_NONE, KDA_GATE_CHANNEL, KDA_GATE_ROW = 0, 1, 2
+
+
+class BlockNormParams(ctypes.Structure):
+    """``kda_block_norm_params`` of include/kda.h, field for field."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("x_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("gate_form", ctypes.c_int32), ("post_norm", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("scale", ctypes.c_float), ("rows", ctypes.c_int64), ("x", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("post_weight", ctypes.c_void_p),
+                ("channel_scale", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("residual_out", ctypes.c_void_p), ("out", ctypes.c_void_p), ("post_eps", ctypes.c_float),
+                ("pre_eps", ctypes.c_float)]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -88,6 +122,14 @@ def _declare(lib):
     lib.kda_decode_ex.restype = i32
     lib.kda_prologue.argtypes = [vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, i32, vp, f32, vp, vp, vp, vp, vp]
     lib.kda_prologue.restype = i32
+    lib.kda_linear_prefill.argtypes = [ctypes.POINTER(LinearPrefillParams), vp]
+    lib.kda_linear_prefill.restype = i32
+    lib.kda_linear_decode.argtypes = [ctypes.POINTER(LinearDecodeParams), vp]
+    lib.kda_linear_decode.restype = i32
+    lib.kda_linear_prefill_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32, i32, i32]
+    lib.kda_linear_prefill_workspace_size.restype = sz
+    lib.kda_block_norm.argtypes = [ctypes.POINTER(BlockNormParams), vp]
+    lib.kda_block_norm.restype = i32
     lib.kda_check_device_error.argtypes = [vp]
     lib.kda_check_device_error.restype = i32
     lib.kda_status_string.argtypes = [i32]
@@ -416,6 +458,200 @@ def decode(q, k, v, log_alpha, beta, state, *, out=None, out_dtype=torch.float32
     if st != KDA_OK:
         raise KdaError(st, "kda_decode")
     return out
+
+
+def _check_linear(q, k, v, log_decay, rows_name):
+    """Shapes and dtypes shared by linear_prefill and linear_decode; (rows, H_k, H, d_k, d_v, per_token)."""
+    if q.ndim != 3 or v.ndim != 3 or k.shape != q.shape or v.shape[0] != q.shape[0]:
+        raise ValueError(f"q and k must be [{rows_name}, H_k, d_k] and v [{rows_name}, H, d_v]")
+    rows, H_k, d_k = q.shape
+    _, H, d_v = v.shape
+    if H_k < 1 or H % H_k:
+        raise ValueError("the value heads must be a multiple of the query / key heads")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must share one dtype")
+    if log_decay.dtype != torch.float32:
+        raise TypeError("log_decay must be float32")
+    if log_decay.shape != (rows, H) and log_decay.shape != (H,):
+        raise ValueError(f"log_decay must be [{rows_name}, H] or [H]")
+    return rows, H_k, H, d_k, d_v, int(log_decay.ndim == 2)
+
+
+def _check_out(name, t, shape, dtype=None):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+
+
+def _check_one_device(*tensors):
+    """All given tensors contiguous and on one CUDA device, which is returned."""
+    _check_cuda(*tensors)
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError("KDA tensors must be on one CUDA device")
+    return devices.pop()
+
+
+def _used_on(stream, *tensors):
+    """Tensors allocated here for the caller's stream: the allocator must not hand their memory
+    to another stream's work before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def linear_workspace_size(total_tokens: int, num_seqs: int, H: int, d_k: int = 128, d_v: int = 128,
+                          dtype=torch.bfloat16, out_dtype=torch.float32, recurrent: bool = False) -> int:
+    """Bytes of device scratch ``linear_prefill`` can use (``kda_linear_prefill_workspace_size``)."""
+    return int(lib().kda_linear_prefill_workspace_size(int(total_tokens), int(num_seqs), int(H), int(d_k), int(d_v),
+                                                       _io_dtype(dtype), _io_dtype(out_dtype), int(bool(recurrent))))
+
+
+def linear_prefill(q, k, v, log_decay, cu_seqlens, init_state=None, *, out=None, final_state=None,
+                   out_dtype=torch.float32, scale: float = 1.0, stream=None, recurrent: bool = False,
+                   want_final: bool = True, workspace="auto"):
+    """Linear attention with one decay per head over packed variable-length sequences
+    (``kda_linear_prefill``): S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
+
+    q, k [T, H_k, d_k], v [T, H, d_v] (bf16 or fp32, one dtype; value head h reads query / key head
+    h // (H // H_k)); log_decay g [T, H] or, constant, [H] float32; cu_seqlens [N+1] int32 (device);
+    init_state [N, H, d_k, d_v] float32 or None. Returns (out [T, H, d_v] in ``out_dtype`` (or
+    out's dtype), final_state [N, H, d_k, d_v] or None). ``recurrent=True`` forces the fp32
+    token-recurrent kernel. ``workspace``: ``"auto"`` allocates what ``linear_workspace_size``
+    asks for, ``None`` passes none, a uint8 CUDA tensor is passed as given."""
+    T, H_k, H, d_k, d_v, per_token = _check_linear(q, k, v, log_decay, "T")
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.ndim != 1 or cu_seqlens.shape[0] < 1:
+        raise TypeError("cu_seqlens must be int32 [N + 1]")
+    N = cu_seqlens.shape[0] - 1
+    device = _check_one_device(q, k, v, log_decay, cu_seqlens, init_state, out, final_state)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out=out, final_state=final_state,
+                                  out_dtype=out_dtype, scale=scale, stream=stream, recurrent=recurrent,
+                                  want_final=want_final, workspace=workspace)
+    state_shape = (N, H, d_k, d_v)
+    if init_state is not None:
+        _check_out("init_state", init_state, state_shape, torch.float32)
+    if out is None:
+        out = torch.empty((T, H, d_v), dtype=out_dtype, device=device)
+        _used_on(stream, out)
+    else:
+        _check_out("out", out, (T, H, d_v))
+    if final_state is not None:
+        _check_out("final_state", final_state, state_shape, torch.float32)
+    elif want_final:
+        final_state = torch.empty(state_shape, dtype=torch.float32, device=device)
+        _used_on(stream, final_state)
+    dt, odt = _io_dtype(q.dtype), _io_dtype(out.dtype)
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError("workspace must be 'auto', None or a uint8 CUDA tensor")
+        n = lib().kda_linear_prefill_workspace_size(T, N, H, d_k, d_v, dt, odt, int(bool(recurrent)))
+        workspace = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+        _used_on(stream, workspace)
+    elif workspace is not None and _check_one_device(workspace) != device:
+        raise ValueError("KDA tensors must be on one CUDA device")
+    p = LinearPrefillParams(ctypes.sizeof(LinearPrefillParams), dt, odt, N, H, H_k, d_k, d_v, per_token,
+                            int(bool(recurrent)), T, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                            cu_seqlens.data_ptr(), None if init_state is None else init_state.data_ptr(),
+                            out.data_ptr(), None if final_state is None else final_state.data_ptr(),
+                            None if workspace is None else workspace.data_ptr(),
+                            0 if workspace is None else workspace.numel() * workspace.element_size(), scale)
+    st = lib().kda_linear_prefill(ctypes.byref(p), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_prefill")
+    return out, final_state
+
+
+def linear_decode(q, k, v, log_decay, state, *, out=None, out_dtype=torch.float32, scale: float = 1.0, stream=None):
+    """One token of linear attention with one decay per head for B sequences
+    (``kda_linear_decode``); ``state`` [B, H, d_k, d_v] float32 is updated in place.
+    q, k [B, H_k, d_k], v [B, H, d_v], log_decay [B, H] or [H]. Returns out [B, H, d_v]."""
+    B, H_k, H, d_k, d_v, per_token = _check_linear(q, k, v, log_decay, "B")
+    device = _check_one_device(q, k, v, log_decay, state, out)
+    _check_out("state", state, (B, H, d_k, d_v), torch.float32)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return linear_decode(q, k, v, log_decay, state, out=out, out_dtype=out_dtype, scale=scale, stream=stream)
+    if out is None:
+        out = torch.empty((B, H, d_v), dtype=out_dtype, device=device)
+        _used_on(stream, out)
+    else:
+        _check_out("out", out, (B, H, d_v))
+    p = LinearDecodeParams(ctypes.sizeof(LinearDecodeParams), _io_dtype(q.dtype), _io_dtype(out.dtype), B, H, H_k, d_k,
+                           d_v, per_token, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                           state.data_ptr(), out.data_ptr())
+    st = lib().kda_linear_decode(ctypes.byref(p), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_linear_decode")
+    return out
+
+
+def block_norm(x, y=None, *, gate=None, post_norm: bool = False, post_weight=None, scale: float = 1.0,
+               channel_scale=None, pre_weight=None, eps: float = 1e-6, post_eps=None, residual_out=None, out=None,
+               out_dtype=None, want_out: bool = True, want_residual: bool = True, stream=None):
+    """The norm after a block, its gate and residual scale, and the norm before the next block
+    (``kda_block_norm``), per row of D channels:
+
+        n  = post_weight * y / sqrt(mean(y^2) + post_eps) with ``post_norm``, else y
+        x' = x + scale * channel_scale * Sigmoid(gate) * n
+        h  = pre_weight * x' / sqrt(mean(x'^2) + eps)
+
+    x [rows, D] and y [rows, D] or None (x' = x), each bf16 or fp32; gate logits in the dtype of y,
+    [rows, D] or [rows], or None (factor 1); weights [D] float32 or None (ones); post_eps defaults
+    to eps. Returns (x' in x's dtype, h in ``out_dtype`` (x's dtype by default) or out's dtype);
+    either is None when not wanted. ``residual_out`` may be x itself. Without y, x' is x and is not
+    written unless ``residual_out`` is given."""
+    if x.ndim != 2 or (y is not None and y.shape != x.shape):
+        raise ValueError("x and y must be [rows, D]")
+    rows, D = x.shape
+    form = KDA_GATE_NONE
+    if y is None:
+        if gate is not None or post_norm or post_weight is not None or channel_scale is not None:
+            raise ValueError("gate, post_norm, post_weight and channel_scale belong to y")
+    elif gate is not None:
+        if gate.dtype != y.dtype:
+            raise TypeError("gate must have the dtype of y")
+        if gate.shape == x.shape:
+            form = KDA_GATE_CHANNEL
+        elif gate.shape == (rows,):
+            form = KDA_GATE_ROW
+        else:
+            raise ValueError("gate must be [rows, D] or [rows]")
+    for w in (post_weight, channel_scale, pre_weight):
+        if w is not None:
+            _check_out("a weight", w, (D,), torch.float32)
+    device = _check_one_device(x, y, gate, post_weight, channel_scale, pre_weight, residual_out, out)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return block_norm(x, y, gate=gate, post_norm=post_norm, post_weight=post_weight, scale=scale,
+                              channel_scale=channel_scale, pre_weight=pre_weight, eps=eps, post_eps=post_eps,
+                              residual_out=residual_out, out=out, out_dtype=out_dtype, want_out=want_out,
+                              want_residual=want_residual, stream=stream)
+    if residual_out is not None:
+        _check_out("residual_out", residual_out, (rows, D), x.dtype)
+    elif want_residual and y is not None:
+        residual_out = torch.empty_like(x)
+        _used_on(stream, residual_out)
+    if out is not None:
+        _check_out("out", out, (rows, D))
+    elif want_out:
+        out = torch.empty((rows, D), dtype=x.dtype if out_dtype is None else out_dtype, device=device)
+        _used_on(stream, out)
+    p = BlockNormParams(ctypes.sizeof(BlockNormParams), _io_dtype(x.dtype), KDA_F32 if y is None else _io_dtype(y.dtype),
+                        KDA_F32 if out is None else _io_dtype(out.dtype), form, int(bool(post_norm)), D, scale, rows,
+                        x.data_ptr(), None if y is None else y.data_ptr(), None if gate is None else gate.data_ptr(),
+                        None if post_weight is None else post_weight.data_ptr(),
+                        None if channel_scale is None else channel_scale.data_ptr(),
+                        None if pre_weight is None else pre_weight.data_ptr(),
+                        None if residual_out is None else residual_out.data_ptr(),
+                        None if out is None else out.data_ptr(), eps if post_eps is None else post_eps, eps)
+    st = lib().kda_block_norm(ctypes.byref(p), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_block_norm")
+    return (x if y is None and residual_out is None and want_residual else residual_out), out
 
 
 def check_device_error(stream=None):

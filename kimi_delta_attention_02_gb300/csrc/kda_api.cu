@@ -3,7 +3,9 @@
 #include <cmath>
 #include <cstdint>
 
+#include "kda_block_norm.h"
 #include "kda_common.cuh"
+#include "kda_linear.cuh"
 
 #include <atomic>
 #include <mutex>
@@ -96,6 +98,9 @@ kda_status launch_chunked(const void *q, const void *k, const void *v, const voi
                           int64_t total_tokens, int H, bool out_bf16, float lb, float scale, const float *init_state,
                           const void *out_gate, const float *norm_weight, float norm_eps, void *out,
                           float *final_state, void *workspace, size_t workspace_bytes, cudaStream_t stream);
+cudaError_t launch_linear_decode(const void *q, const void *k, const void *v, const float *log_decay, bool per_token,
+                                 float *state, void *out, int B, int H, int H_k, int d_k, int d_v, bool in_bf16,
+                                 bool out_bf16, float scale, cudaStream_t stream);
 
 namespace {
 
@@ -278,6 +283,33 @@ kda_status check_decay_form(kda_decay_form form, const float *A_log, float bound
   return KDA_ERR_INVALID_ARG;
 }
 
+bool valid_dtype(kda_dtype d) { return d == KDA_F32 || d == KDA_BF16; }
+
+// Sizes of a linear-attention call: rows of q, k, v (tokens, or decode's B) and states.
+kda_status check_linear_sizes(int64_t rows, int64_t states, int32_t H, int32_t H_k, int32_t d_k, int32_t d_v,
+                              int32_t per_token, kda_dtype in_dtype, kda_dtype out_dtype) {
+  if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return KDA_ERR_INVALID_ARG;
+  if (rows < 0 || states < 0 || H < 1 || H_k < 1 || d_k < 1 || d_v < 1) return KDA_ERR_INVALID_ARG;
+  if (H % H_k != 0 || (per_token != 0 && per_token != 1)) return KDA_ERR_INVALID_ARG;
+  if (d_k > 128 || d_v > 128 || rows > INT32_MAX || states * H > INT32_MAX / 4) return KDA_ERR_UNSUPPORTED;
+  return KDA_OK;
+}
+
+// A byte range of a tensor argument (null: none). No output may overlap an input or another output.
+struct Range {
+  const void *p;
+  size_t bytes;
+};
+bool outputs_clear(const Range *outs, int n_out, const Range *ins, int n_in) {
+  for (int o = 0; o < n_out; ++o) {
+    for (int i = 0; i < n_in; ++i)
+      if (overlaps(outs[o].p, outs[o].bytes, ins[i].p, ins[i].bytes)) return false;
+    for (int o2 = o + 1; o2 < n_out; ++o2)
+      if (overlaps(outs[o].p, outs[o].bytes, outs[o2].p, outs[o2].bytes)) return false;
+  }
+  return true;
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -420,6 +452,121 @@ kda_status kda_prologue(const void *q_raw, const void *k_raw, const void *v_raw,
   const cudaError_t err = launch_prologue(q_raw, k_raw, v_raw, conv_weight, cu_seqlens, num_seqs, total_tokens, H,
                                           d_k, d_v, dtype == KDA_BF16, conv_init, l2_eps, q, k, v, conv_final,
                                           static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_linear_prefill_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t d_k, int32_t d_v,
+                                         kda_dtype in_dtype, kda_dtype out_dtype, int32_t force_recurrent) {
+  if (check_linear_sizes(total_tokens, num_seqs, H, H, d_k, d_v, 1, in_dtype, out_dtype) != KDA_OK) return 0;
+  if (total_tokens == 0 || num_seqs == 0) return 0;
+  return linear_plan(total_tokens, num_seqs, H, d_k, d_v, in_dtype == KDA_BF16, out_dtype == KDA_BF16,
+                     force_recurrent != 0)
+      .bytes;
+}
+
+kda_status kda_linear_prefill(const kda_linear_prefill_params *p, void *stream) {
+  if (p == nullptr || p->struct_size != sizeof(kda_linear_prefill_params)) return KDA_ERR_INVALID_ARG;
+  const kda_status st = check_linear_sizes(p->total_tokens, p->num_seqs, p->H, p->H_k, p->d_k, p->d_v,
+                                           p->decay_per_token, p->in_dtype, p->out_dtype);
+  if (st != KDA_OK) return st;
+  const int64_t T = p->total_tokens;
+  if (T > 0 && p->num_seqs == 0) return KDA_ERR_INVALID_ARG;
+  if (p->cu_seqlens == nullptr || !aligned4(p->cu_seqlens)) return KDA_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (!p->q || !p->k || !p->v || !p->log_decay || !p->out) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(p->q) || !aligned16(p->k) || !aligned16(p->v) || !aligned16(p->out) || !aligned4(p->log_decay))
+      return KDA_ERR_INVALID_ARG;
+  }
+  if (!aligned16(p->init_state) || !aligned16(p->final_state)) return KDA_ERR_INVALID_ARG;
+  if ((p->workspace == nullptr) != (p->workspace_bytes == 0) || !aligned16(p->workspace)) return KDA_ERR_INVALID_ARG;
+  const size_t es = p->in_dtype == KDA_BF16 ? 2 : 4, eo = p->out_dtype == KDA_BF16 ? 2 : 4;
+  const size_t nk = size_t(T) * p->H_k * p->d_k * es, nv = size_t(T) * p->H * p->d_v;
+  const size_t ns = size_t(p->num_seqs) * p->H * p->d_k * p->d_v * 4;
+  const bool in_place = p->final_state != nullptr && p->final_state == p->init_state;
+  const Range ins[6] = {{p->q, nk}, {p->k, nk}, {p->v, nv * es},
+                        {p->log_decay, size_t(p->decay_per_token ? T : 1) * p->H * 4},
+                        {p->cu_seqlens, (size_t(p->num_seqs) + 1) * 4}, {in_place ? nullptr : p->init_state, ns}};
+  const Range outs[3] = {{p->out, nv * eo}, {p->final_state, ns}, {p->workspace, p->workspace_bytes}};
+  if (!outputs_clear(outs, 3, ins, 6)) return KDA_ERR_INVALID_ARG;
+  if (p->num_seqs == 0) return KDA_OK;
+  if (T == 0 && p->final_state == nullptr) return KDA_OK;
+
+  LinearArgs a{};
+  a.q = p->q, a.k = p->k, a.v = p->v, a.log_decay = p->log_decay, a.cu = p->cu_seqlens;
+  a.init_state = p->init_state, a.out = p->out, a.final_state = p->final_state;
+  a.num_seqs = p->num_seqs, a.H = p->H, a.H_k = p->H_k, a.d_k = p->d_k, a.d_v = p->d_v;
+  a.per_token = p->decay_per_token, a.total = T, a.scale = p->scale;
+  const bool in_bf16 = p->in_dtype == KDA_BF16, out_bf16 = p->out_dtype == KDA_BF16;
+  a.plan = linear_plan(T, p->num_seqs, p->H, p->d_k, p->d_v, in_bf16, out_bf16, p->force_recurrent != 0);
+  if (p->workspace_bytes < a.plan.bytes) {  // every sequence from end to end
+    a.plan.seg_len = 0;
+    a.plan.slots = p->num_seqs;
+  } else if (a.plan.bytes != 0) {
+    a.seg_states = static_cast<float *>(p->workspace);
+    a.seg_decay = reinterpret_cast<float *>(static_cast<uint8_t *>(p->workspace) + a.plan.state_bytes);
+  }
+  const cudaError_t err = launch_linear_recurrent(a, in_bf16, out_bf16, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_linear_decode(const kda_linear_decode_params *p, void *stream) {
+  if (p == nullptr || p->struct_size != sizeof(kda_linear_decode_params)) return KDA_ERR_INVALID_ARG;
+  if (p->B < 1) return KDA_ERR_INVALID_ARG;
+  const kda_status st =
+      check_linear_sizes(p->B, p->B, p->H, p->H_k, p->d_k, p->d_v, p->decay_per_token, p->in_dtype, p->out_dtype);
+  if (st != KDA_OK) return st;
+  if (!p->q || !p->k || !p->v || !p->log_decay || !p->state || !p->out) return KDA_ERR_INVALID_ARG;
+  if (!aligned16(p->q) || !aligned16(p->k) || !aligned16(p->v) || !aligned16(p->state) || !aligned16(p->out) ||
+      !aligned4(p->log_decay))
+    return KDA_ERR_INVALID_ARG;
+  const size_t es = p->in_dtype == KDA_BF16 ? 2 : 4, eo = p->out_dtype == KDA_BF16 ? 2 : 4;
+  const size_t nk = size_t(p->B) * p->H_k * p->d_k * es, nv = size_t(p->B) * p->H * p->d_v;
+  const Range ins[4] = {{p->q, nk}, {p->k, nk}, {p->v, nv * es},
+                        {p->log_decay, size_t(p->decay_per_token ? p->B : 1) * p->H * 4}};
+  const Range outs[2] = {{p->out, nv * eo}, {p->state, nv * p->d_k * 4}};
+  if (!outputs_clear(outs, 2, ins, 4)) return KDA_ERR_INVALID_ARG;
+  const cudaError_t err = launch_linear_decode(p->q, p->k, p->v, p->log_decay, p->decay_per_token != 0, p->state,
+                                               p->out, p->B, p->H, p->H_k, p->d_k, p->d_v, p->in_dtype == KDA_BF16,
+                                               p->out_dtype == KDA_BF16, p->scale, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_block_norm(const kda_block_norm_params *p, void *stream) {
+  if (p == nullptr || p->struct_size != sizeof(kda_block_norm_params)) return KDA_ERR_INVALID_ARG;
+  if (!valid_dtype(p->x_dtype) || !valid_dtype(p->y_dtype) || !valid_dtype(p->out_dtype)) return KDA_ERR_INVALID_ARG;
+  if (p->rows < 0 || p->D < 1) return KDA_ERR_INVALID_ARG;
+  if (p->D > kBlockNormMaxD || p->rows > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if (p->gate_form != KDA_GATE_NONE && p->gate_form != KDA_GATE_CHANNEL && p->gate_form != KDA_GATE_ROW)
+    return KDA_ERR_INVALID_ARG;
+  if (p->post_norm != 0 && p->post_norm != 1) return KDA_ERR_INVALID_ARG;
+  if (!finite_nonneg(p->pre_eps) || !finite_nonneg(p->post_eps)) return KDA_ERR_INVALID_ARG;
+  if (p->rows > 0) {
+    if (p->x == nullptr || (p->residual_out == nullptr && p->out == nullptr)) return KDA_ERR_INVALID_ARG;
+    if ((p->gate_form != KDA_GATE_NONE) != (p->gate != nullptr)) return KDA_ERR_INVALID_ARG;
+    if (p->y == nullptr && (p->gate || p->post_weight || p->channel_scale || p->post_norm)) return KDA_ERR_INVALID_ARG;
+    if ((p->post_weight != nullptr && p->post_norm == 0) || (p->pre_weight != nullptr && p->out == nullptr))
+      return KDA_ERR_INVALID_ARG;
+  }
+  const void *all[8] = {p->x, p->y, p->gate, p->post_weight, p->channel_scale, p->pre_weight, p->residual_out, p->out};
+  for (const void *q : all)
+    if (!aligned16(q)) return KDA_ERR_INVALID_ARG;
+  const size_t ex = p->x_dtype == KDA_BF16 ? 2 : 4, ey = p->y_dtype == KDA_BF16 ? 2 : 4;
+  const size_t n = size_t(p->rows) * p->D, w = size_t(p->D) * 4;
+  const bool in_place = p->residual_out != nullptr && p->residual_out == p->x;
+  const Range ins[6] = {{in_place ? nullptr : p->x, n * ex}, {p->y, n * ey},
+                        {p->gate, (p->gate_form == KDA_GATE_ROW ? size_t(p->rows) : n) * ey},
+                        {p->post_weight, w}, {p->channel_scale, w}, {p->pre_weight, w}};
+  const Range outs[2] = {{p->residual_out, n * ex}, {p->out, n * (p->out_dtype == KDA_BF16 ? 2 : 4)}};
+  if (!outputs_clear(outs, 2, ins, 6)) return KDA_ERR_INVALID_ARG;
+  if (p->rows == 0) return KDA_OK;
+  BlockNormArgs a{};
+  a.x = p->x, a.y = p->y, a.gate = p->gate;
+  a.post_weight = p->post_weight, a.channel_scale = p->channel_scale, a.pre_weight = p->pre_weight;
+  a.residual_out = p->residual_out, a.out = p->out, a.rows = p->rows, a.D = p->D;
+  a.gate_form = int(p->gate_form), a.post_norm = p->post_norm;
+  a.scale = p->scale, a.post_eps = p->post_eps, a.pre_eps = p->pre_eps;
+  const cudaError_t err = launch_block_norm(a, p->x_dtype == KDA_BF16, p->y_dtype == KDA_BF16,
+                                            p->out_dtype == KDA_BF16, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
