@@ -505,7 +505,9 @@ kda_status kda_linear_prefill(const kda_linear_prefill_params *p, void *stream) 
     a.seg_states = static_cast<float *>(p->workspace);
     a.seg_decay = reinterpret_cast<float *>(static_cast<uint8_t *>(p->workspace) + a.plan.state_bytes);
   }
-  const cudaError_t err = launch_linear_recurrent(a, in_bf16, out_bf16, static_cast<cudaStream_t>(stream));
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const cudaError_t err = a.plan.tensor && T > 0 ? launch_linear_chunked(a, out_bf16, cs)
+                                                 : launch_linear_recurrent(a, in_bf16, out_bf16, cs);
   return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -81,6 +81,8 @@ struct LinearArgs {
 LinearPlan linear_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool in_bf16, bool out_bf16,
                        bool recurrent);
 cudaError_t launch_linear_recurrent(const LinearArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream);
+bool linear_chunked_supported(int d_k, int d_v, bool in_bf16);
+cudaError_t launch_linear_chunked(const LinearArgs &a, bool out_bf16, cudaStream_t stream);
 cudaError_t launch_linear_scan(const LinearArgs &a, cudaStream_t stream);
 
 }  // namespace kda

@@ -1,0 +1,601 @@
+// kda_linear_chunked.cu -- linear attention with one decay per head on the tensor cores (bf16
+// inputs, head sizes that are multiples of 8): S_t = e^{g_t} S_{t-1} + k_t v_t^T,
+// o_t = scale S_t^T q_t, in chunks of 128 tokens.
+//
+// With G the cumulative log-decay inside a chunk and S the state that enters it,
+//     O  = (D (*) Q K^T) V + diag(e^G) Q S,      D_ij = e^{G_i - G_j} for j <= i, else 0,
+//     S <- e^{G_C} S + K^T V',                   V'_j = e^{G_C - G_j} v_j .
+// All four products are tcgen05 MMAs with fp32 accumulators in tensor memory; the state itself
+// stays in fp32 registers. One CTA owns one segment of one (sequence, head) and kDV value columns.
+//
+// Roundings. P = D (*) Q K^T and the state enter their products as bf16 (each off by at most 2^-8
+// of the value, like the bf16 output they end in); with an fp32 output they enter as a bf16 pair
+// hi + lo (2^-16). V' is always such a pair, because the fp32 state adds it up over the whole sequence.
+//
+// Decays. A chunk has four blocks of 32 tokens. a_i is the sum of g from its block's start to i,
+// s_j from behind j to its block's end, t_B a whole block's (log2 units). Then e^{G_i - G_j} is
+// 2^{a_i - a_j} within a block and 2^{a_i + t_{J+1} + ... + t_{I-1}} 2^{s_j} across: no factor is
+// the difference of two long sums, none exceeds one while g <= 0, and only the diagonal blocks
+// take an exponential per entry. A decay below 2^-127 per token counts as 2^-127, which leaves
+// nothing in fp32 either, so g = -infinity needs no case of its own.
+//
+// Warps (16): 0 loads (TMA), 1 issues the MMAs, 2 makes the decay tables, 4-7 form P (one query row
+// per thread, in place in tensor memory: P is the A operand of its product), 8-15 convert V to V' in
+// quarters of 32 tokens, keep the state (one key row and half the columns per thread) and write
+// the output. Per chunk the tensor pipe runs Q K^T, K^T V' (hi, lo), P V, Q S: 2560 cycles for
+// 128 value columns; everything else runs beside it.
+#include "kda_linear.cuh"
+#include "kda_tma_host.h"
+
+namespace kda {
+namespace {
+
+constexpr int kC = 128;            // tokens per chunk
+constexpr int kThreads = 512;
+constexpr uint32_t kTileQK = 32768;  // 128 tokens x 128 channels bf16, two 64-channel blocks
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kMinLog2 = -127.f;
+
+template <int kDV, bool kOutBF16, bool kStateOnly>
+struct Cfg {
+  static constexpr bool kPair = !kOutBF16 && !kStateOnly;  // P and S as hi + lo
+  static constexpr int kNK = kDV == 128 && !kStateOnly ? 1 : 2, kNQ = kStateOnly ? 0 : 2, kNV = 2;
+  static constexpr uint32_t kTileV = 256u * kDV;
+  static constexpr uint32_t kTileS = kStateOnly ? 0 : 256u * kDV;   // 128 key rows x kDV bf16
+  static constexpr uint32_t kTileVP = 64u * kDV;                    // a quarter of V': 32 tokens
+  static constexpr uint32_t oK = 0, oQ = oK + kNK * kTileQK, oV = oQ + kNQ * kTileQK, oS = oV + kNV * kTileV,
+                            oVP = oS + (kPair ? 2 : 1) * kTileS, oTab = oVP + 4 * kTileVP;
+};
+
+struct Table {  // decays of one chunk, log2 units unless said otherwise
+  float a[kC];   // from the block's start to the token, itself included
+  float es[kC];  // 2^(from behind the token to the block's end)
+  float t[4];    // blocks
+  float after[4];  // 2^(everything behind block B)
+  float e1;      // e^{G_C} - 1
+  float pad[3];
+};
+
+struct Control {
+  uint64_t k_full[2], k_free[2], q_full[2], q_free[2], v_full[2], v_free[2];
+  uint64_t vp_full[2], vp_free[2], tab_full[2], tab_free[2];
+  uint64_t qk_done, p_full, d_done, s_full, pv_done, qs_done, drain;
+  uint32_t tmem;
+  volatile uint32_t abort;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// D[tmem] (+)= A[tmem] x B[smem], bf16: A's row m in lane m, two elements of K per 32-bit column.
+__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// K-major tile (128-byte rows of 64 elements, 8-row atoms); MN-major tile with `lbo` between its
+// 64-element blocks.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) { return umma_desc(addr, 16, 1024, kSwizzle128B); }
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
+  return umma_desc(addr, lbo, 1024, kSwizzle128B);
+}
+
+template <int kDV, bool kOutBF16, bool kStateOnly>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_chunked_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                          const __grid_constant__ CUtensorMap mv, const LinearArgs a, uint32_t *err_word) {
+  using F = Cfg<kDV, kOutBF16, kStateOnly>;
+  constexpr bool kPair = F::kPair;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Table *tab = reinterpret_cast<Table *>(smem + F::oTab);
+  Control *ctl = reinterpret_cast<Control *>(smem + F::oTab + 2 * sizeof(Table));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H, hk = h / (a.H / a.H_k);
+  const int col0 = blockIdx.y * kDV;
+
+  LinearSlot s;
+  if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, slot, s)) return;
+  if (kStateOnly && s.last) return;
+  const int len = int(s.t1 - s.t0), chunks = (len + kC - 1) / kC;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_free[i], 1);
+      mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->q_free[i], 1);
+      mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_free[i], 1);
+      mbar_init(&ctl->vp_full[i], 8), mbar_init(&ctl->vp_free[i], 1);
+      mbar_init(&ctl->tab_full[i], 1), mbar_init(&ctl->tab_free[i], kStateOnly ? 8 : 12);
+    }
+    mbar_init(&ctl->qk_done, 1), mbar_init(&ctl->p_full, 4), mbar_init(&ctl->d_done, 1);
+    mbar_init(&ctl->s_full, 8), mbar_init(&ctl->pv_done, 1), mbar_init(&ctl->qs_done, 1);
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) tmem_alloc(&ctl->tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+  const uint32_t tQK = tmem, tOI = tmem + 128, tOX = tOI + kDV, tD = tOX + kDV, tPL = tD + kDV;  // tPL: low half of P
+
+  // A bounded wait; false once any role has given up, so that all leave together. `wait` is for
+  // the single-lane roles, `wait_warp` gives all lanes of a warp one answer.
+  auto wait = [&](uint64_t &bar, uint32_t parity, uint32_t code) -> bool {
+    for (uint32_t i = 0; i < kSpinLimit; ++i) {
+      if (mbar_try_wait(&bar, parity & 1)) return true;
+      if ((i & 63) == 63 && ctl->abort != 0) return false;
+    }
+    ctl->abort = 1;
+    raise_device_error(err_word, code);
+    return false;
+  };
+  auto wait_warp = [&](uint64_t &bar, uint32_t parity, uint32_t code) -> bool {
+    return __all_sync(0xffffffffu, wait(bar, parity, code)) != 0;
+  };
+
+  if (warp == 0) {
+    // ---- loads: chunk n's V, Q and K, each when its buffer is free (K last: with one buffer it
+    // waits for the chunk before); chunk n + 1's tiles go to L2 meanwhile
+    if (lane == 0) {
+      int issued = 0;
+      for (int n = 0; n < chunks; ++n) {
+        const int32_t t = int32_t(s.t0) + n * kC;
+        const int sk = n % F::kNK, s2 = n & 1;
+        if (!wait(ctl->v_free[s2], (n >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) break;
+        mbar_arrive_expect_tx(&ctl->v_full[s2], F::kTileV);
+#pragma unroll
+        for (int b = 0; b < kDV / 64; ++b)
+          tma_load_3d(smem + F::oV + s2 * F::kTileV + b * 16384, &mv, &ctl->v_full[s2], col0 + 64 * b, h, t);
+        issued = 3 * n + 1;
+        if constexpr (!kStateOnly) {
+          if (!wait(ctl->q_free[s2], (n >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) break;
+          mbar_arrive_expect_tx(&ctl->q_full[s2], kTileQK);
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            tma_load_3d(smem + F::oQ + s2 * kTileQK + b * 16384, &mq, &ctl->q_full[s2], 64 * b, hk, t);
+        }
+        issued = 3 * n + 2;
+        if (!wait(ctl->k_free[sk], (n / F::kNK) ^ 1, DEVERR_MMA_TIMEOUT)) break;
+        mbar_arrive_expect_tx(&ctl->k_full[sk], kTileQK);
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+          tma_load_3d(smem + F::oK + sk * kTileQK + b * 16384, &mk, &ctl->k_full[sk], 64 * b, hk, t);
+        issued = 3 * n + 3;
+        if (n + 1 < chunks) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            tma_prefetch_l2_3d(&mk, 64 * b, hk, t + kC);
+            if constexpr (!kStateOnly) tma_prefetch_l2_3d(&mq, 64 * b, hk, t + kC);
+          }
+#pragma unroll
+          for (int b = 0; b < kDV / 64; ++b) tma_prefetch_l2_3d(&mv, col0 + 64 * b, h, t + kC);
+        }
+      }
+      // every load issued has landed before the CTA may end
+      const int nv = (issued + 2) / 3, nq = (issued + 1) / 3, nk = issued / 3;
+      for (int n = nk > F::kNK ? nk - F::kNK : 0; n < nk; ++n)
+        mbar_wait(&ctl->k_full[n % F::kNK], (n / F::kNK) & 1, err_word, DEVERR_TMA_TIMEOUT);
+      if constexpr (!kStateOnly)
+        for (int n = nq > 2 ? nq - 2 : 0; n < nq; ++n)
+          mbar_wait(&ctl->q_full[n & 1], (n >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
+      for (int n = nv > 2 ? nv - 2 : 0; n < nv; ++n)
+        mbar_wait(&ctl->v_full[n & 1], (n >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
+    }
+  } else if (warp == 1) {
+    // ---- MMAs
+    if (lane == 0) {
+      constexpr uint32_t iQK = umma_idesc_bf16(128, 128, false, false, false);
+      constexpr uint32_t iD = umma_idesc_bf16(128, kDV, true, true, false);
+      constexpr uint32_t iPV = umma_idesc_bf16(128, kDV, false, true, false);  // P V and Q S
+      const uint32_t base = smem_u32(smem);
+      for (int n = 0; n < chunks; ++n) {
+        const uint32_t K = base + F::oK + (n % F::kNK) * kTileQK, Q = base + F::oQ + (n & 1) * kTileQK,
+                       V = base + F::oV + (n & 1) * F::kTileV;
+        if (!wait(ctl->k_full[n % F::kNK], n / F::kNK, DEVERR_TMA_TIMEOUT)) break;
+        if constexpr (!kStateOnly) {
+          if (!wait(ctl->q_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
+          // P of chunk n - 1 has been read out of the columns Q K^T goes to
+          if (n > 0 && !wait(ctl->pv_done, n - 1, DEVERR_MMA_TIMEOUT)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint32_t o = (ks >> 2) * 16384 + (ks & 3) * 32;
+            umma_f16(tQK, desc_k(Q + o), desc_k(K + o), iQK, ks > 0);
+          }
+          umma_commit(&ctl->qk_done);
+        }
+        bool ok = true;
+        for (int q = 0; q < 4; ++q) {  // K^T V', 32 tokens at a time
+          const int u = 4 * n + q;
+          ok = wait(ctl->vp_full[u & 1], u >> 1, DEVERR_MMA_TIMEOUT);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t hi = base + F::oVP + (u & 1) * 2 * F::kTileVP;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {  // hi, lo
+            const uint32_t kk = (ks & 1) * 2048;
+            umma_f16(tD, desc_mn(K + q * 4096 + kk, 16384), desc_mn(hi + (ks >> 1) * F::kTileVP + kk, 4096), iD,
+                     q > 0 || ks > 0);
+          }
+          umma_commit(&ctl->vp_free[u & 1]);
+        }
+        if (!ok) break;
+        umma_commit(&ctl->d_done);
+        umma_commit(&ctl->k_free[n % F::kNK]);
+        if constexpr (kStateOnly) {
+          umma_commit(&ctl->v_free[n & 1]);
+        } else {
+          if (!wait(ctl->p_full, n, DEVERR_MMA_TIMEOUT)) break;
+          if (!wait(ctl->s_full, n, DEVERR_MMA_TIMEOUT)) break;  // and O of chunk n - 1 is read out
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < (kPair ? 16 : 8); ++ks)
+            umma_f16_ta(tOI, (ks < 8 ? tQK : tPL) + 8 * (ks & 7), desc_mn(V + (ks & 7) * 2048, 16384), iPV, ks > 0);
+          umma_commit(&ctl->pv_done);
+          umma_commit(&ctl->v_free[n & 1]);
+#pragma unroll
+          for (int ks = 0; ks < (kPair ? 16 : 8); ++ks) {
+            const uint32_t o = ((ks & 7) >> 2) * 16384 + (ks & 3) * 32;
+            umma_f16(tOX, desc_k(Q + o), desc_mn(base + F::oS + (ks >> 3) * F::kTileS + (ks & 7) * 2048, 16384), iPV,
+                     ks > 0);
+          }
+          umma_commit(&ctl->q_free[n & 1]);
+          umma_commit(&ctl->qs_done);
+        }
+      }
+      // no MMA is in flight when tensor memory is freed
+      umma_commit(&ctl->drain);
+      mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
+    }
+  } else if (warp == 2) {
+    // ---- decay tables
+    double total = 0.;
+    const bool per_token = a.per_token != 0;
+    const float constant = per_token ? 0.f : a.log_decay[h];
+    float g[4];
+    auto fetch = [&](int n) {
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int i = n * kC + 32 * b + lane;
+        g[b] = i < len ? (per_token ? a.log_decay[(s.t0 + i) * a.H + h] : constant) : 0.f;
+      }
+    };
+    fetch(0);
+    for (int n = 0; n < chunks; ++n) {
+      float p[4], x[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const float v = g[b] * kLog2e;
+        p[b] = v < kMinLog2 ? kMinLog2 : v;  // a NaN stays
+        x[b] = __shfl_down_sync(0xffffffffu, p[b], 1);
+        if (lane == 31) x[b] = 0.f;  // from behind the token
+      }
+      if (n + 1 < chunks) fetch(n + 1);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const float up = __shfl_up_sync(0xffffffffu, p[b], o), down = __shfl_down_sync(0xffffffffu, x[b], o);
+          if (lane >= o) p[b] += up;
+          if (lane + o < 32) x[b] += down;
+        }
+      }
+      float t[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) t[b] = __shfl_sync(0xffffffffu, p[b], 31);
+      const float all = (t[0] + t[1]) + (t[2] + t[3]);
+      total += double(all);
+      Table &w = tab[n & 1];
+      if (!wait_warp(ctl->tab_free[n & 1], (n >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) break;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        w.a[32 * b + lane] = p[b];
+        w.es[32 * b + lane] = ex2(x[b]);
+      }
+      if (lane == 0) {
+        w.t[0] = t[0], w.t[1] = t[1], w.t[2] = t[2], w.t[3] = t[3];
+        w.after[0] = ex2(t[1] + t[2] + t[3]), w.after[1] = ex2(t[2] + t[3]), w.after[2] = ex2(t[3]), w.after[3] = 1.f;
+        w.e1 = expm1f(all * kLn2);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->tab_full[n & 1]);
+    }
+    if (kStateOnly && lane == 0 && blockIdx.y == 0)
+      a.seg_decay[int64_t(slot) * a.H + h] = float(total * 0.6931471805599453);
+  } else if (warp >= 4 && warp < 8) {
+    // ---- P: row i of Q K^T in lane i; the decays, then bf16 in place
+    if constexpr (!kStateOnly) {
+      const int w = warp & 3;
+      const uint32_t row = uint32_t(32 * w) << 16;
+      for (int n = 0; n < chunks; ++n) {
+        const Table &tb = tab[n & 1];
+        if (!wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
+        const float ai = tb.a[32 * w + lane];
+        if (!wait_warp(ctl->qk_done, n, DEVERR_MMA_TIMEOUT)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int J = 0; J < 4; ++J) {
+          float hi[16], lo[16];
+          if (J <= w) {  // the whole warp alike
+            float x0[16], x1[16];
+            tmem_ld16(tQK + row + 32 * J, x0);
+            tmem_ld16(tQK + row + 32 * J + 16, x1);
+            float f[32];
+            if (J < w) {
+              float e = ai;
+#pragma unroll
+              for (int B = 1; B < 3; ++B)
+                if (B > J && B < w) e += tb.t[B];
+              e = ex2(e);
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 c = *reinterpret_cast<const float4 *>(&tb.es[32 * J + j]);
+                f[j] = c.x * e, f[j + 1] = c.y * e, f[j + 2] = c.z * e, f[j + 3] = c.w * e;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 c = *reinterpret_cast<const float4 *>(&tb.a[32 * J + j]);
+                f[j] = ex2(ai - c.x), f[j + 1] = ex2(ai - c.y), f[j + 2] = ex2(ai - c.z), f[j + 3] = ex2(ai - c.w);
+              }
+            }
+            tmem_ld_wait(x0, x1);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float p0 = (j < 16 ? x0[j & 15] : x1[j & 15]) * f[j];
+              float p1 = (j < 16 ? x0[(j + 1) & 15] : x1[(j + 1) & 15]) * f[j + 1];
+              if (J == w) {  // selected away, not multiplied: what lies above may be infinite
+                p0 = j <= lane ? p0 : 0.f;
+                p1 = j + 1 <= lane ? p1 : 0.f;
+              }
+              const uint32_t u = pack_bf16x2(p0, p1);
+              hi[j >> 1] = __uint_as_float(u);
+              if constexpr (kPair) {
+                const float2 b = unpack_bf16x2(u);
+                lo[j >> 1] = __uint_as_float(pack_bf16x2(p0 - b.x, p1 - b.y));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) hi[j] = lo[j] = 0.f;
+          }
+          tmem_st16(tQK + row + 16 * J, hi);  // over columns read already
+          if constexpr (kPair) tmem_st16(tPL + row + 16 * J, lo);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctl->p_full);
+          mbar_arrive(&ctl->tab_free[n & 1]);
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    // ---- V', the state and the output
+    constexpr int kHalf = kDV / 2;  // columns per thread
+    const int half = (warp - 8) >> 2, w = warp & 3, r = 32 * w + lane, wt = tid - 256;
+    const uint32_t row = uint32_t(32 * w) << 16;
+    const int cb = half * kHalf;  // first column within the tile
+    const int64_t dd = int64_t(a.d_k) * a.d_v;
+    float S[kHalf];
+    {
+      const float *src = nullptr;
+      if constexpr (!kStateOnly) {
+        if (a.plan.seg_len != 0) src = a.seg_states + (int64_t(slot) * a.H + h) * dd;
+        else if (a.init_state != nullptr) src = a.init_state + (int64_t(s.n) * a.H + h) * dd;
+      }
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 4) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int col = col0 + cb + c;
+        if (src != nullptr && r < a.d_k && col < a.d_v)  // d_v is a multiple of 8
+          x = *reinterpret_cast<const float4 *>(src + int64_t(r) * a.d_v + col);
+        S[c] = x.x, S[c + 1] = x.y, S[c + 2] = x.z, S[c + 3] = x.w;
+      }
+    }
+    auto write_state_tile = [&]() {  // the B operand of Q S: rows k, MN-major
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 8) {
+        uint32_t u[4], l[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          u[e] = pack_bf16x2(S[c + 2 * e], S[c + 2 * e + 1]);
+          if constexpr (kPair) {
+            const float2 b = unpack_bf16x2(u[e]);
+            l[e] = pack_bf16x2(S[c + 2 * e] - b.x, S[c + 2 * e + 1] - b.y);
+          }
+        }
+        const uint32_t o = sw128_chunk(r, ((cb + c) >> 3) & 7, (cb + c) >> 6, 128);
+        *reinterpret_cast<uint4 *>(smem + F::oS + o) = make_uint4(u[0], u[1], u[2], u[3]);
+        if constexpr (kPair)
+          *reinterpret_cast<uint4 *>(smem + F::oS + F::kTileS + o) = make_uint4(l[0], l[1], l[2], l[3]);
+      }
+    };
+    // quarter q of chunk n's V' (32 tokens) into its buffer
+    auto convert = [&](int n, int q) -> bool {
+      const int u = 4 * n + q;
+      const Table &tb = tab[n & 1];
+      uint8_t *V = smem + F::oV + (n & 1) * F::kTileV, *hi = smem + F::oVP + (u & 1) * 2 * F::kTileVP;
+      if (q == 0) {
+        if (!wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) return false;
+        if (!wait_warp(ctl->v_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) return false;
+      }
+      const bool partial = (n + 1) * kC > len;  // rows behind the segment hold another's tokens
+      if (partial && q == 0 && !wait_warp(ctl->k_full[n % F::kNK], n / F::kNK, DEVERR_TMA_TIMEOUT)) return false;
+      if (!wait_warp(ctl->vp_free[u & 1], (u >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) return false;
+      const float after = tb.after[q];
+#pragma unroll
+      for (int i = wt; i < 4 * kDV; i += 256) {  // pieces of 8 columns
+        const int t = i / (kDV / 8), j = i % (kDV / 8), tt = 32 * q + t;
+        uint4 *src = reinterpret_cast<uint4 *>(V + sw128_chunk(tt, j & 7, j >> 3, 128));
+        uint4 *dst = reinterpret_cast<uint4 *>(hi + sw128_chunk(t, j & 7, j >> 3, 32));
+        uint4 *dst_lo = reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(dst) + F::kTileVP);
+        if (partial && n * kC + tt >= len) {
+          // zero here and in K: a product of 0 with another sequence's infinity would not vanish
+          *src = *dst = *dst_lo = make_uint4(0, 0, 0, 0);
+          uint8_t *K = smem + F::oK + (n % F::kNK) * kTileQK;
+#pragma unroll
+          for (int b = 0; b < 128 / kDV; ++b)
+            *reinterpret_cast<uint4 *>(K + sw128_chunk(tt, j & 7, kDV == 128 ? j >> 3 : b, 128)) = make_uint4(0, 0, 0, 0);
+          continue;
+        }
+        const float f = tb.es[tt] * after;
+        const uint4 x = *src;
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+        uint32_t h4[4], l4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = f2_mul(unpack_bf16x2(xs[e]), make_float2(f, f));
+          h4[e] = pack_bf16x2(y.x, y.y);
+          const float2 b = unpack_bf16x2(h4[e]);
+          l4[e] = pack_bf16x2(y.x - b.x, y.y - b.y);
+        }
+        *dst = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+        *dst_lo = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->vp_full[u & 1]);
+      return true;
+    };
+    bool ok = true;
+    if constexpr (!kStateOnly) {
+      write_state_tile();
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->s_full);
+    }
+    if (chunks > 0) ok = convert(0, 0) && convert(0, 1);
+    for (int n = 0; ok && n < chunks; ++n) {
+      ok = convert(n, 2) && convert(n, 3);
+      if (!ok) break;
+      const Table &tb = tab[n & 1];
+      const float e1 = tb.e1;
+      float eG = 0.f;  // e^{G_r}, the decay of the entering state at token r
+      if constexpr (!kStateOnly) {
+        eG = tb.a[r];
+#pragma unroll
+        for (int B = 0; B < 3; ++B)
+          if (B < w) eG += tb.t[B];
+        eG = ex2(eG);
+      }
+      // the state: S <- e^{G_C} S + K^T V'
+      ok = wait_warp(ctl->d_done, n, DEVERR_MMA_TIMEOUT);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 16) {
+        float d[16];
+        tmem_ld16_wait(tD + row + cb + c, d);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) S[c + e] = decay_step(S[c + e], e1) + d[e];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->tab_free[n & 1]);
+      if (n + 1 < chunks) ok = convert(n + 1, 0) && convert(n + 1, 1);
+      if (!ok) break;
+      if constexpr (!kStateOnly) {
+        ok = wait_warp(ctl->qs_done, n, DEVERR_MMA_TIMEOUT);
+        if (!ok) break;
+        tc_fence_after();
+        const int64_t t = s.t0 + int64_t(n) * kC + r;
+#pragma unroll
+        for (int c = 0; c < kHalf; c += 16) {
+          float oi[16], ox[16];
+          tmem_ld16(tOI + row + cb + c, oi);
+          tmem_ld16(tOX + row + cb + c, ox);
+          tmem_ld_wait(oi, ox);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) oi[e] = a.scale * fmaf(eG, ox[e], oi[e]);
+          if (t < s.t1) {
+            const int col = col0 + cb + c;
+            const int64_t at = (t * a.H + h) * a.d_v + col;
+#pragma unroll
+            for (int e = 0; e < 16; e += 8) {
+              if (col + e >= a.d_v) continue;
+              if constexpr (kOutBF16) {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at + e) =
+                    make_uint4(pack_bf16x2(oi[e], oi[e + 1]), pack_bf16x2(oi[e + 2], oi[e + 3]),
+                               pack_bf16x2(oi[e + 4], oi[e + 5]), pack_bf16x2(oi[e + 6], oi[e + 7]));
+              } else {
+                float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at + e);
+                p[0] = make_float4(oi[e], oi[e + 1], oi[e + 2], oi[e + 3]);
+                p[1] = make_float4(oi[e + 4], oi[e + 5], oi[e + 6], oi[e + 7]);
+              }
+            }
+          }
+        }
+        if (n + 1 < chunks) write_state_tile();
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->s_full);
+      }
+    }
+    float *dst = kStateOnly ? a.seg_states + (int64_t(slot) * a.H + h) * dd
+                 : (s.last && a.final_state != nullptr) ? a.final_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
+    if (dst != nullptr && r < a.d_k) {
+#pragma unroll
+      for (int c = 0; c < kHalf; c += 4) {
+        const int col = col0 + cb + c;
+        if (col < a.d_v)
+          *reinterpret_cast<float4 *>(dst + int64_t(r) * a.d_v + col) = make_float4(S[c], S[c + 1], S[c + 2], S[c + 3]);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int kDV, bool kOutBF16, bool kStateOnly>
+cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const LinearArgs &a,
+                       cudaStream_t stream) {
+  using F = Cfg<kDV, kOutBF16, kStateOnly>;
+  constexpr uint32_t smem = F::oTab + 2 * sizeof(Table) + sizeof(Control);
+  static_assert(smem <= 232448, "shared memory of one CTA");
+  const auto kern = linear_chunked_kernel<kDV, kOutBF16, kStateOnly>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  const dim3 grid(unsigned(a.plan.slots) * unsigned(a.H), unsigned((a.d_v + kDV - 1) / kDV));
+  kern<<<grid, kThreads, smem, stream>>>(mq, mk, mv, a, device_error_word());
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool linear_chunked_supported(int d_k, int d_v, bool in_bf16) { return in_bf16 && d_k % 8 == 0 && d_v % 8 == 0; }
+
+cudaError_t launch_linear_chunked(const LinearArgs &a, bool out_bf16, cudaStream_t stream) {
+  CUtensorMap mq, mk, mv;
+  if (!tensor_map_3d(&mq, a.q, true, a.total, a.H_k, a.d_k, 64, kC, true) ||
+      !tensor_map_3d(&mk, a.k, true, a.total, a.H_k, a.d_k, 64, kC, true) ||
+      !tensor_map_3d(&mv, a.v, true, a.total, a.H, a.d_v, 64, kC, true))
+    return cudaErrorInvalidValue;
+  const bool wide = a.plan.col_tile == 128;
+  if (a.plan.seg_len != 0) {
+    cudaError_t e = wide ? launch_one<128, true, true>(mq, mk, mv, a, stream)
+                         : launch_one<64, true, true>(mq, mk, mv, a, stream);
+    if (e == cudaSuccess) e = launch_linear_scan(a, stream);
+    if (e != cudaSuccess) return e;
+  }
+  if (wide) return launch_one<128, true, false>(mq, mk, mv, a, stream);
+  return out_bf16 ? launch_one<64, true, false>(mq, mk, mv, a, stream)
+                  : launch_one<64, false, false>(mq, mk, mv, a, stream);
+}
+
+}  // namespace kda

@@ -1,0 +1,176 @@
+"""kda_linear_prefill on the tensor-core kernel (bf16, head sizes that are multiples of 8), its
+segments and its pass of state sums, against the fp64 oracle.
+
+Bounds, relative to the magnitude (the same sums over absolute values). The state: its terms'
+decayed values enter as bf16 pairs, off by at most 2^-16; the decay of a term is 2 to a sum of at
+most 32 log-decays per factor, each sum at most 32 x 5 x 1.45 = 231 in these tests and so off by
+231 x 2^-24 x ln 2 < 2^-16; fp32 accumulation as in linear_cases.fp32_factor over a chunk (128
+tokens) and two roundings per chunk. An fp32 output is made of the same (P and the state enter as
+pairs). A bf16 output has P and the state rounded to bf16, 2^-8, and its own half step, 2^-8."""
+
+import numpy as np
+import pytest
+import torch
+
+from kimi_delta_attention_02_gb300 import binding
+from linear_cases import check, fp32_factor, make, reference, run
+
+pytestmark = pytest.mark.gpu
+B16, F32 = torch.bfloat16, torch.float32
+
+
+def _check(c, lens, scale=1.0, out_dtype=B16, **kw):
+    out, fin = run(c, scale=scale, out_dtype=out_dtype, **kw)
+    o, f, mo, mf = reference(c, scale)
+    fine = 2.0 ** -15 + fp32_factor(128 + max(lens) // 64, c["q"].shape[2])
+    if out_dtype == B16:
+        check(out, o, mo * (2.0 ** -8 + fine) + 2.0 ** -8 * np.abs(o), 1.0, "out")
+    else:
+        check(out, o, mo, fine, "out")
+    if fin is not None:
+        check(fin, f, mf, fine, "final")
+    return out, fin
+
+
+@pytest.mark.parametrize("out_dtype", [B16, F32])
+@pytest.mark.parametrize("lens", [[128], [1], [127], [129], [256], [31, 32, 33], [0, 300, 0, 5], [640]])
+def test_lengths(lens, out_dtype):
+    _check(make(lens, H=2, seed=sum(lens)), lens, out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("out_dtype", [B16, F32])
+@pytest.mark.parametrize("d_k,d_v", [(128, 64), (64, 128), (64, 64), (8, 8), (16, 128), (120, 72), (128, 8), (72, 104)])
+def test_head_sizes(d_k, d_v, out_dtype):
+    lens = [150, 40]
+    _check(make(lens, H=3, d_k=d_k, d_v=d_v, seed=d_k + d_v), lens, scale=0.25, out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("H,H_k", [(6, 1), (6, 3), (8, 2)])
+@pytest.mark.parametrize("per_token", [True, False])
+def test_shared_heads(H, H_k, per_token):
+    lens = [70, 200]
+    for out_dtype in (B16, F32):
+        _check(make(lens, H=H, H_k=H_k, d_v=64, per_token=per_token, seed=H), lens, out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("decay", [0.0, 1e-3, 0.3, 3.0])
+@pytest.mark.parametrize("out_dtype", [B16, F32])
+def test_decays(decay, out_dtype):
+    lens = [400]
+    _check(make(lens, decay=decay, seed=7), lens, out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("lens", [[3000], [1500, 0, 1, 2600, 511, 512, 513, 1025]])
+@pytest.mark.parametrize("d_v,out_dtype", [(128, B16), (64, B16), (128, F32)])
+def test_segments_join(lens, d_v, out_dtype):
+    c = make(lens, H=2, d_v=d_v, decay=0.01, seed=11)
+    assert binding.linear_workspace_size(sum(lens), len(lens), 2, 128, d_v, B16, out_dtype) > 0
+    _check(c, lens, out_dtype=out_dtype)
+    _check(c, lens, out_dtype=out_dtype, workspace=None)
+
+
+def test_states():
+    lens = [200, 0, 60]
+    _check(make(lens, init=False), lens)
+    c = make(lens)
+    o, f, mo, mf = reference(c)
+    state = c["init_state"]
+    out, fin = run(c, final_state=state)
+    assert fin is state
+    check(fin, f, mf, 2.0 ** -15 + fp32_factor(130, 128), "in place")
+    assert run(make(lens), want_final=False)[1] is None
+
+
+def test_forgetting_and_nan():
+    lens = [300]
+    c = make(lens, H=2, seed=3)
+    for t in (5, 6, 31, 32, 127, 128, 200, 201, 202):
+        c["log_decay"][t, 0] = -float("inf")
+    _check(c, lens, out_dtype=F32)
+    c["log_decay"][150, 1] = float("nan")
+    out, fin = run(c, out_dtype=F32)
+    nan = torch.isnan(out)
+    assert nan[150:, 1].all() and not nan[:150].any() and not nan[:, 0].any()
+    assert torch.isnan(fin[0, 1]).all() and not torch.isnan(fin[0, 0]).any()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_other_sequences_infinities_stay_there(bad):
+    """Tiles reach into the next sequence and behind the last one: nothing of theirs may arrive."""
+    lens = [100, 90, 70]
+    c = make(lens, H=2, seed=4)
+    o, f, mo, mf = reference(c)
+    for n in ("q", "k", "v"):
+        c[n][100:190] = bad
+    pad = {n: torch.cat([c[n], torch.full_like(c[n][:40], bad)]) for n in ("q", "k", "v", "log_decay")}
+    out = torch.full((300, 2, 128), 7.0, device="cuda", dtype=F32)
+    _, fin = binding.linear_prefill(pad["q"], pad["k"], pad["v"], pad["log_decay"], c["cu_seqlens"], c["init_state"],
+                                    out=out)
+    binding.check_device_error()
+    keep = np.r_[0:100, 190:260]
+    fine = 2.0 ** -15 + fp32_factor(130, 128)
+    check(out[:260][keep], o[keep], mo[keep], fine, "out")
+    check(fin[[0, 2]], f[[0, 2]], mf[[0, 2]], fine, "final")
+    assert (out[260:] == 7.0).all()
+
+
+def test_agrees_with_the_token_kernel_on_a_long_memory():
+    lens = [5000]
+    c = make(lens, H=4, H_k=1, decay=1e-3, per_token=False, seed=8)
+    o, f = run(c, recurrent=True)
+    _, _, mo, mf = reference(c)
+    out, fin = run(c, out_dtype=F32)
+    fine = 2.0 ** -15 + 2 * fp32_factor(5000, 128)
+    check(out, o.double().cpu().numpy(), mo, fine, "out")
+    check(fin, f.double().cpu().numpy(), mf, fine, "final")
+
+
+def test_prompt_of_the_packed_layer_then_block_norm_and_tokens():
+    """The operators together: a packed prompt, its output through the block norm, then tokens."""
+    lens = [130, 61]
+    c = make(lens, H=4, H_k=2, d_v=64, seed=12)
+    out, state = run(c, out_dtype=B16)
+    x = torch.randn(sum(lens), 4 * 64, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+    x2, h = binding.block_norm(x, out.reshape(sum(lens), -1), post_norm=True, scale=0.5, out_dtype=B16)
+    want = x.double() + 0.5 * out.reshape(sum(lens), -1).double() * torch.rsqrt(
+        out.reshape(sum(lens), -1).double().square().mean(-1, keepdim=True) + 1e-6)
+    assert torch.allclose(x2.double(), want, rtol=1e-5, atol=1e-5)
+    n = make([1, 1], H=4, H_k=2, d_v=64, seed=13)
+    n["init_state"] = state.clone()
+    o, f, mo, mf = reference(n)
+    tok = binding.linear_decode(n["q"], n["k"], n["v"], n["log_decay"], state)
+    check(tok, o, mo, fp32_factor(1, 128), "token")
+    check(state, f, mf, fp32_factor(1, 128), "state")
+
+
+def test_captured_prefill_replays_on_new_inputs_beside_another():
+    """Two captured graphs with a workspace each, replayed on two streams at once."""
+    lens = [2600]
+    graphs, cases, results = [], [], []
+    for i in range(2):
+        c = make(lens, H=2, seed=20 + i)
+        ws = torch.empty(binding.linear_workspace_size(2600, 1, 2, 128, 128, B16, F32), dtype=torch.uint8, device="cuda")
+        out, fin = torch.empty(2600, 2, 128, device="cuda"), torch.empty(1, 2, 128, 128, device="cuda")
+        run(c, out=out, final_state=fin, workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            binding.linear_prefill(**c, out=out, final_state=fin, workspace=ws)
+        graphs.append(g), cases.append((c, ws)), results.append((out, fin))
+    refs = []
+    for i in range(2):
+        new = make(lens, H=2, seed=30 + i)
+        for n in ("q", "k", "v", "log_decay", "init_state"):
+            cases[i][0][n].copy_(new[n])
+        refs.append(reference(new))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    binding.check_device_error()
+    fine = 2.0 ** -15 + fp32_factor(128 + 40, 128)
+    for (out, fin), (o, f, mo, mf) in zip(results, refs):
+        check(out, o, mo, fine, "out")
+        check(fin, f, mf, fine, "final")
