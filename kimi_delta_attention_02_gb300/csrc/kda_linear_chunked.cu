@@ -19,11 +19,11 @@
 // take an exponential per entry. A decay below 2^-127 per token counts as 2^-127, which leaves
 // nothing in fp32 either, so g = -infinity needs no case of its own.
 //
-// Warps (16): 0 loads (TMA), 1 issues the MMAs, 2 makes the decay tables, 4-7 form P (one query row
-// per thread, in place in tensor memory: P is the A operand of its product), 8-15 convert V to V' in
-// quarters of 32 tokens, keep the state (one key row and half the columns per thread) and write
-// the output. Per chunk the tensor pipe runs Q K^T, K^T V' (hi, lo), P V, Q S: 2560 cycles for
-// 128 value columns; everything else runs beside it.
+// Warps (20): 0 loads (TMA), 1 issues the MMAs, 2 makes the decay tables, 3 stores the output tiles
+// (TMA), 4-7 form P (one query row per thread, in place in tensor memory: P is the A operand of
+// its product), 8-11 convert V to V' in quarters of 32 tokens, 12-19 keep the state (one key row
+// and half the columns per thread) and read out the output. Per chunk the tensor pipe runs
+// Q K^T, K^T V' (hi, lo), P V, Q S: 2560 cycles for 128 value columns; everything else runs beside.
 #include "kda_linear.cuh"
 #include "kda_tma_host.h"
 
@@ -31,7 +31,7 @@ namespace kda {
 namespace {
 
 constexpr int kC = 128;            // tokens per chunk
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr uint32_t kTileQK = 32768;  // 128 tokens x 128 channels bf16, two 64-channel blocks
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMinLog2 = -127.f;
@@ -48,18 +48,18 @@ struct Cfg {
 };
 
 struct Table {  // decays of one chunk, log2 units unless said otherwise
-  float a[kC];   // from the block's start to the token, itself included
-  float es[kC];  // 2^(from behind the token to the block's end)
-  float t[4];    // blocks
-  float after[4];  // 2^(everything behind block B)
-  float e1;      // e^{G_C} - 1
-  float pad[3];
+  float a[kC];       // from the block's start to the token, itself included
+  float es[96];      // 2^(from behind the token to the block's end), blocks 0 .. 2
+  uint32_t f[kC];    // e^{G_C - G_j} as a pair: the nearest bf16 (low half), what is left
+  float t[3];        // blocks 0 .. 2
+  float e1;          // e^{G_C} - 1
 };
 
+template <int kNK>
 struct Control {
-  uint64_t k_full[2], k_free[2], q_full[2], q_free[2], v_full[2], v_free[2];
+  uint64_t k_full[kNK], k_free[kNK], q_full[2], q_free[2], v_full[2], v_free[2];
   uint64_t vp_full[2], vp_free[2], tab_full[2], tab_free[2];
-  uint64_t qk_done, p_full, d_done, s_full, pv_done, qs_done, drain;
+  uint64_t qk_done, p_full, d_done, d_free, s_full, pv_done, qs_done, o_full, drain;
   uint32_t tmem;
   volatile uint32_t abort;
 };
@@ -70,13 +70,43 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// D[tmem] (+)= A[tmem] x B[smem], bf16: A's row m in lane m, two elements of K per 32-bit column.
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// bf16 pairs: a b and a b + c, rounded to nearest-even
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
+// The MMA warp runs as a whole, so that descriptors stay in uniform registers (a lone lane has to
+// move each one there), and its leader lane alone issues.
+//   D[tmem] (+)= A[smem] x B[smem], bf16
+__device__ __forceinline__ void mma_ss(bool leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(uint32_t(leader))
+      : "memory");
+}
+//   D[tmem] (+)= A[tmem] x B[smem]: A's row m in lane m, two elements of K per 32-bit column
+__device__ __forceinline__ void mma_ts(bool leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(uint32_t(leader))
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(bool leader, uint64_t &bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(&bar)),
+      "r"(uint32_t(leader))
       : "memory");
 }
 
@@ -90,12 +120,13 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
 template <int kDV, bool kOutBF16, bool kStateOnly>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_chunked_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                          const __grid_constant__ CUtensorMap mv, const LinearArgs a, uint32_t *err_word) {
+                          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                          const LinearArgs a, uint32_t *err_word) {
   using F = Cfg<kDV, kOutBF16, kStateOnly>;
   constexpr bool kPair = F::kPair;
   extern __shared__ __align__(1024) uint8_t smem[];
   Table *tab = reinterpret_cast<Table *>(smem + F::oTab);
-  Control *ctl = reinterpret_cast<Control *>(smem + F::oTab + 2 * sizeof(Table));
+  auto *ctl = reinterpret_cast<Control<F::kNK> *>(smem + F::oTab + 2 * sizeof(Table));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H, hk = h / (a.H / a.H_k);
   const int col0 = blockIdx.y * kDV;
@@ -107,15 +138,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_free[i], 1);
+      if (i < F::kNK) mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_free[i], 1);
       mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->q_free[i], 1);
       mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_free[i], 1);
-      mbar_init(&ctl->vp_full[i], 8), mbar_init(&ctl->vp_free[i], 1);
-      mbar_init(&ctl->tab_full[i], 1), mbar_init(&ctl->tab_free[i], kStateOnly ? 8 : 12);
+      mbar_init(&ctl->vp_full[i], 4), mbar_init(&ctl->vp_free[i], 1);
+      mbar_init(&ctl->tab_full[i], 1), mbar_init(&ctl->tab_free[i], kStateOnly ? 12 : 16);
     }
     mbar_init(&ctl->qk_done, 1), mbar_init(&ctl->p_full, 4), mbar_init(&ctl->d_done, 1);
     mbar_init(&ctl->s_full, 8), mbar_init(&ctl->pv_done, 1), mbar_init(&ctl->qs_done, 1);
-    mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->d_free, 8), mbar_init(&ctl->o_full, 8), mbar_init(&ctl->drain, 1);
     ctl->abort = 0;
     fence_mbarrier_init();
   }
@@ -129,9 +160,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // A bounded wait; false once any role has given up, so that all leave together. `wait` is for
   // the single-lane roles, `wait_warp` gives all lanes of a warp one answer.
   auto wait = [&](uint64_t &bar, uint32_t parity, uint32_t code) -> bool {
-    for (uint32_t i = 0; i < kSpinLimit; ++i) {
-      if (mbar_try_wait(&bar, parity & 1)) return true;
-      if ((i & 63) == 63 && ctl->abort != 0) return false;
+    if (mbar_try_wait(&bar, parity & 1)) return true;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kSleepLimit; ++i) {
+      if (mbar_try_wait_sleep(&bar, parity & 1, kSleepNs)) return true;
+      if (ctl->abort != 0) return false;
     }
     ctl->abort = 1;
     raise_device_error(err_word, code);
@@ -146,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // waits for the chunk before); chunk n + 1's tiles go to L2 meanwhile
     if (lane == 0) {
       int issued = 0;
+#pragma unroll 1
       for (int n = 0; n < chunks; ++n) {
         const int32_t t = int32_t(s.t0) + n * kC;
         const int sk = n % F::kNK, s2 = n & 1;
@@ -181,80 +215,85 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // every load issued has landed before the CTA may end
       const int nv = (issued + 2) / 3, nq = (issued + 1) / 3, nk = issued / 3;
+#pragma unroll 1
       for (int n = nk > F::kNK ? nk - F::kNK : 0; n < nk; ++n)
         mbar_wait(&ctl->k_full[n % F::kNK], (n / F::kNK) & 1, err_word, DEVERR_TMA_TIMEOUT);
       if constexpr (!kStateOnly)
+#pragma unroll 1
         for (int n = nq > 2 ? nq - 2 : 0; n < nq; ++n)
           mbar_wait(&ctl->q_full[n & 1], (n >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
+#pragma unroll 1
       for (int n = nv > 2 ? nv - 2 : 0; n < nv; ++n)
         mbar_wait(&ctl->v_full[n & 1], (n >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
     }
   } else if (warp == 1) {
     // ---- MMAs
-    if (lane == 0) {
-      constexpr uint32_t iQK = umma_idesc_bf16(128, 128, false, false, false);
-      constexpr uint32_t iD = umma_idesc_bf16(128, kDV, true, true, false);
-      constexpr uint32_t iPV = umma_idesc_bf16(128, kDV, false, true, false);  // P V and Q S
-      const uint32_t base = smem_u32(smem);
-      for (int n = 0; n < chunks; ++n) {
-        const uint32_t K = base + F::oK + (n % F::kNK) * kTileQK, Q = base + F::oQ + (n & 1) * kTileQK,
-                       V = base + F::oV + (n & 1) * F::kTileV;
-        if (!wait(ctl->k_full[n % F::kNK], n / F::kNK, DEVERR_TMA_TIMEOUT)) break;
-        if constexpr (!kStateOnly) {
-          if (!wait(ctl->q_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
-          // P of chunk n - 1 has been read out of the columns Q K^T goes to
-          if (n > 0 && !wait(ctl->pv_done, n - 1, DEVERR_MMA_TIMEOUT)) break;
-          tc_fence_after();
+    constexpr uint32_t iQK = umma_idesc_bf16(128, 128, false, false, false);
+    constexpr uint32_t iD = umma_idesc_bf16(128, kDV, true, true, false);
+    constexpr uint32_t iPV = umma_idesc_bf16(128, kDV, false, true, false);  // P V and Q S
+    const bool leader = lane == 0;
+    const uint32_t base = smem_u32(smem);
+    // Descriptors of the first buffers; an operand elsewhere is `bytes / 16` further (addresses
+    // stay below 2^18, so the address field never carries).
+    const uint64_t dQ = desc_k(base + F::oQ), dK = desc_k(base + F::oK), dKt = desc_mn(base + F::oK, 16384);
+    const uint64_t dV = desc_mn(base + F::oV, 16384), dVP = desc_mn(base + F::oVP, 4096);
+    const uint64_t dS = desc_mn(base + F::oS, 16384);
+#pragma unroll 1
+    for (int n = 0; n < chunks; ++n) {
+      const uint32_t nk = uint32_t(n % F::kNK) * (kTileQK >> 4), nq = uint32_t(n & 1) * (kTileQK >> 4),
+                     nv = uint32_t(n & 1) * (F::kTileV >> 4);
+      if (!wait_warp(ctl->k_full[n % F::kNK], n / F::kNK, DEVERR_TMA_TIMEOUT)) break;
+      if constexpr (!kStateOnly) {
+        if (!wait_warp(ctl->q_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
+        // P of chunk n - 1 has been read out of the columns Q K^T goes to
+        if (n > 0 && !wait_warp(ctl->pv_done, n - 1, DEVERR_MMA_TIMEOUT)) break;
+        tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks) {
-            const uint32_t o = (ks >> 2) * 16384 + (ks & 3) * 32;
-            umma_f16(tQK, desc_k(Q + o), desc_k(K + o), iQK, ks > 0);
-          }
-          umma_commit(&ctl->qk_done);
+        for (int ks = 0; ks < 8; ++ks) {
+          const uint32_t o = (ks >> 2) * 1024 + (ks & 3) * 2;
+          mma_ss(leader, tQK, dQ + (nq + o), dK + (nk + o), iQK, ks > 0);
         }
-        bool ok = true;
-        for (int q = 0; q < 4; ++q) {  // K^T V', 32 tokens at a time
-          const int u = 4 * n + q;
-          ok = wait(ctl->vp_full[u & 1], u >> 1, DEVERR_MMA_TIMEOUT);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t hi = base + F::oVP + (u & 1) * 2 * F::kTileVP;
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {  // hi, lo
-            const uint32_t kk = (ks & 1) * 2048;
-            umma_f16(tD, desc_mn(K + q * 4096 + kk, 16384), desc_mn(hi + (ks >> 1) * F::kTileVP + kk, 4096), iD,
-                     q > 0 || ks > 0);
-          }
-          umma_commit(&ctl->vp_free[u & 1]);
-        }
-        if (!ok) break;
-        umma_commit(&ctl->d_done);
-        umma_commit(&ctl->k_free[n % F::kNK]);
-        if constexpr (kStateOnly) {
-          umma_commit(&ctl->v_free[n & 1]);
-        } else {
-          if (!wait(ctl->p_full, n, DEVERR_MMA_TIMEOUT)) break;
-          if (!wait(ctl->s_full, n, DEVERR_MMA_TIMEOUT)) break;  // and O of chunk n - 1 is read out
-          tc_fence_after();
-#pragma unroll
-          for (int ks = 0; ks < (kPair ? 16 : 8); ++ks)
-            umma_f16_ta(tOI, (ks < 8 ? tQK : tPL) + 8 * (ks & 7), desc_mn(V + (ks & 7) * 2048, 16384), iPV, ks > 0);
-          umma_commit(&ctl->pv_done);
-          umma_commit(&ctl->v_free[n & 1]);
-#pragma unroll
-          for (int ks = 0; ks < (kPair ? 16 : 8); ++ks) {
-            const uint32_t o = ((ks & 7) >> 2) * 16384 + (ks & 3) * 32;
-            umma_f16(tOX, desc_k(Q + o), desc_mn(base + F::oS + (ks >> 3) * F::kTileS + (ks & 7) * 2048, 16384), iPV,
-                     ks > 0);
-          }
-          umma_commit(&ctl->q_free[n & 1]);
-          umma_commit(&ctl->qs_done);
-        }
+        mma_commit(leader, ctl->qk_done);
       }
-      // no MMA is in flight when tensor memory is freed
-      umma_commit(&ctl->drain);
-      mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
+      if (n > 0 && !wait_warp(ctl->d_free, n - 1, DEVERR_MMA_TIMEOUT)) break;
+      bool ok = true;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {  // K^T V', 32 tokens at a time
+        const int u = 4 * n + q;
+        ok = wait_warp(ctl->vp_full[u & 1], u >> 1, DEVERR_MMA_TIMEOUT);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t ak = dKt + (nk + q * 256), bv = dVP + uint32_t(u & 1) * (2 * F::kTileVP >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)  // hi, lo
+          mma_ss(leader, tD, ak + (ks & 1) * 128, bv + ((ks >> 1) * (F::kTileVP >> 4) + (ks & 1) * 128), iD,
+                 q > 0 || ks > 0);
+        mma_commit(leader, ctl->vp_free[u & 1]);
+      }
+      if (!ok) break;
+      mma_commit(leader, ctl->d_done);
+      mma_commit(leader, ctl->k_free[n % F::kNK]);
+      if constexpr (kStateOnly) {
+        mma_commit(leader, ctl->v_free[n & 1]);
+      } else {
+        if (!wait_warp(ctl->p_full, n, DEVERR_MMA_TIMEOUT)) break;
+        if (!wait_warp(ctl->s_full, n, DEVERR_MMA_TIMEOUT)) break;  // and O of chunk n - 1 is read out
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < (kPair ? 16 : 8); ++ks)
+          mma_ts(leader, tOI, (ks < 8 ? tQK : tPL) + 8 * (ks & 7), dV + (nv + (ks & 7) * 128), iPV, ks > 0);
+        mma_commit(leader, ctl->pv_done);
+        mma_commit(leader, ctl->v_free[n & 1]);
+#pragma unroll
+        for (int ks = 0; ks < (kPair ? 16 : 8); ++ks)
+          mma_ss(leader, tOX, dQ + (nq + ((ks & 7) >> 2) * 1024 + (ks & 3) * 2),
+                 dS + ((ks >> 3) * (F::kTileS >> 4) + (ks & 7) * 128), iPV, ks > 0);
+        mma_commit(leader, ctl->qs_done);
+      }
     }
+    // no MMA is in flight when tensor memory is freed
+    mma_commit(leader, ctl->drain);
+    if (leader) mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
   } else if (warp == 2) {
     // ---- decay tables
     double total = 0.;
@@ -269,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     fetch(0);
+#pragma unroll 1
     for (int n = 0; n < chunks; ++n) {
       float p[4], x[4];
 #pragma unroll
@@ -295,14 +335,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += double(all);
       Table &w = tab[n & 1];
       if (!wait_warp(ctl->tab_free[n & 1], (n >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) break;
+      const float behind[4] = {t[1] + t[2] + t[3], t[2] + t[3], t[3], 0.f};
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         w.a[32 * b + lane] = p[b];
-        w.es[32 * b + lane] = ex2(x[b]);
+        const float es = ex2(x[b]);
+        if (b < 3) w.es[32 * b + lane] = es;
+        const float f = es * ex2(behind[b]);
+        const uint32_t f1 = pack_bf16x2(f, 0.f) & 0xffffu;
+        w.f[32 * b + lane] = f1 | (pack_bf16x2(f - bf16_to_f32(uint16_t(f1)), 0.f) << 16);
       }
       if (lane == 0) {
-        w.t[0] = t[0], w.t[1] = t[1], w.t[2] = t[2], w.t[3] = t[3];
-        w.after[0] = ex2(t[1] + t[2] + t[3]), w.after[1] = ex2(t[2] + t[3]), w.after[2] = ex2(t[3]), w.after[3] = 1.f;
+        w.t[0] = t[0], w.t[1] = t[1], w.t[2] = t[2];
         w.e1 = expm1f(all * kLn2);
       }
       __syncwarp();
@@ -315,60 +359,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (!kStateOnly) {
       const int w = warp & 3;
       const uint32_t row = uint32_t(32 * w) << 16;
+#pragma unroll 1
       for (int n = 0; n < chunks; ++n) {
         const Table &tb = tab[n & 1];
         if (!wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
         const float ai = tb.a[32 * w + lane];
         if (!wait_warp(ctl->qk_done, n, DEVERR_MMA_TIMEOUT)) break;
         tc_fence_after();
+        // bf16 of 32 columns over columns that have been read already
+        auto put = [&](int J, const float2(&p)[16]) {
+          float hi[16];
 #pragma unroll
-        for (int J = 0; J < 4; ++J) {
-          float hi[16], lo[16];
-          if (J <= w) {  // the whole warp alike
-            float x0[16], x1[16];
-            tmem_ld16(tQK + row + 32 * J, x0);
-            tmem_ld16(tQK + row + 32 * J + 16, x1);
-            float f[32];
-            if (J < w) {
-              float e = ai;
+          for (int j = 0; j < 16; ++j) hi[j] = __uint_as_float(pack_bf16x2(p[j].x, p[j].y));
+          tmem_st16(tQK + row + 16 * J, hi);
+          if constexpr (kPair) {
+            float lo[16];
 #pragma unroll
-              for (int B = 1; B < 3; ++B)
-                if (B > J && B < w) e += tb.t[B];
-              e = ex2(e);
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 c = *reinterpret_cast<const float4 *>(&tb.es[32 * J + j]);
-                f[j] = c.x * e, f[j + 1] = c.y * e, f[j + 2] = c.z * e, f[j + 3] = c.w * e;
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 c = *reinterpret_cast<const float4 *>(&tb.a[32 * J + j]);
-                f[j] = ex2(ai - c.x), f[j + 1] = ex2(ai - c.y), f[j + 2] = ex2(ai - c.z), f[j + 3] = ex2(ai - c.w);
-              }
+            for (int j = 0; j < 16; ++j) {
+              const float2 b = unpack_bf16x2(__float_as_uint(hi[j]));
+              lo[j] = __uint_as_float(pack_bf16x2(p[j].x - b.x, p[j].y - b.y));
             }
-            tmem_ld_wait(x0, x1);
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              float p0 = (j < 16 ? x0[j & 15] : x1[j & 15]) * f[j];
-              float p1 = (j < 16 ? x0[(j + 1) & 15] : x1[(j + 1) & 15]) * f[j + 1];
-              if (J == w) {  // selected away, not multiplied: what lies above may be infinite
-                p0 = j <= lane ? p0 : 0.f;
-                p1 = j + 1 <= lane ? p1 : 0.f;
-              }
-              const uint32_t u = pack_bf16x2(p0, p1);
-              hi[j >> 1] = __uint_as_float(u);
-              if constexpr (kPair) {
-                const float2 b = unpack_bf16x2(u);
-                lo[j >> 1] = __uint_as_float(pack_bf16x2(p0 - b.x, p1 - b.y));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) hi[j] = lo[j] = 0.f;
+            tmem_st16(tPL + row + 16 * J, lo);
           }
-          tmem_st16(tQK + row + 16 * J, hi);  // over columns read already
-          if constexpr (kPair) tmem_st16(tPL + row + 16 * J, lo);
+        };
+        auto get = [&](int J, float2(&p)[16]) {
+          float x[2][16];
+          tmem_ld16(tQK + row + 32 * J, x[0]);
+          tmem_ld16(tQK + row + 32 * J + 16, x[1]);
+          tmem_ld_wait(x[0], x[1]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) p[j] = make_float2(x[j >> 3][(2 * j) & 15], x[j >> 3][(2 * j + 1) & 15]);
+        };
+#pragma unroll 1
+        for (int J = 0; J < w; ++J) {  // blocks before the row's: row factor x column factor
+          float e = ai;  // from the end of block J to the row
+          if (J + 1 < w) e += tb.t[J + 1];
+          if (J + 2 < w) e += tb.t[J + 2];
+          e = ex2(e);
+          float2 p[16];
+          get(J, p);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 c = *reinterpret_cast<const float4 *>(&tb.es[32 * J + j]);
+            p[j >> 1] = f2_mul(p[j >> 1], f2_mul(make_float2(c.x, c.y), make_float2(e, e)));
+            p[(j >> 1) + 1] = f2_mul(p[(j >> 1) + 1], f2_mul(make_float2(c.z, c.w), make_float2(e, e)));
+          }
+          put(J, p);
+        }
+        {  // the row's own block; selected away, not multiplied: what lies above may be infinite
+          float2 p[16];
+          get(w, p);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float2 c = *reinterpret_cast<const float2 *>(&tb.a[32 * w + j]);
+            p[j >> 1].x = j <= lane ? p[j >> 1].x * ex2(ai - c.x) : 0.f;
+            p[j >> 1].y = j + 1 <= lane ? p[j >> 1].y * ex2(ai - c.y) : 0.f;
+          }
+          put(w, p);
+        }
+#pragma unroll 1
+        for (int J = w + 1; J < 4; ++J) {
+          float zero[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) zero[j] = 0.f;
+          tmem_st16(tQK + row + 16 * J, zero);
+          if constexpr (kPair) tmem_st16(tPL + row + 16 * J, zero);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -379,10 +434,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp >= 8) {
-    // ---- V', the state and the output
+  } else if (warp == 3) {
+    // ---- output tiles: whole chunks leave through TMA from the chunk's Q buffer (its last MMA is
+    // done), which is free again once the copy has read it
+    if constexpr (!kStateOnly) {
+      if (lane == 0) {
+#pragma unroll 1
+        for (int n = 0; n < chunks; ++n) {
+          if (!wait(ctl->o_full, n, DEVERR_MMA_TIMEOUT)) break;
+          if ((n + 1) * kC <= len) {
+            constexpr int kBox = kOutBF16 ? 64 : 32;
+#pragma unroll
+            for (int b = 0; b < kDV / kBox; ++b)
+              if (col0 + kBox * b < a.d_v)
+                tma_store_3d(&mo, smem + F::oQ + (n & 1) * kTileQK + b * 16384, col0 + kBox * b, h,
+                             int32_t(s.t0) + n * kC);
+            bulk_commit();
+            bulk_wait_read();
+          }
+          mbar_arrive(&ctl->q_free[n & 1]);
+        }
+        bulk_wait_all();
+      }
+    }
+  } else if (warp >= 8 && warp < 12) {
+    // ---- V': quarters of 32 tokens, two buffers
+    const int wt = tid - 256;
+    // this thread's pieces of 8 columns: column piece j of tokens t0, t0 + step, ... of a quarter
+    constexpr int step = 1024 / kDV;
+    const int j = wt % (kDV / 8), t0 = wt / (kDV / 8);
+    const uint32_t src_off = sw128_chunk(t0, j & 7, j >> 3, 128), dst_off = sw128_chunk(t0, j & 7, j >> 3, 32);
+    bool ok = true;
+#pragma unroll 1
+    for (int n = 0; ok && n < chunks; ++n) {
+      const Table &tb = tab[n & 1];
+      ok = wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT) &&
+           wait_warp(ctl->v_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT);
+      const int part = len - n * kC;  // rows from here on hold another sequence's tokens
+      if (ok && part < kC) ok = wait_warp(ctl->k_full[n % F::kNK], n / F::kNK, DEVERR_TMA_TIMEOUT);
+#pragma unroll 1
+      for (int q = 0; ok && q < 4; ++q) {
+        const int u = 4 * n + q;
+        uint8_t *src = smem + F::oV + (n & 1) * F::kTileV + q * 4096 + src_off;
+        uint8_t *dst = smem + F::oVP + (u & 1) * 2 * F::kTileVP + dst_off;
+        ok = wait_warp(ctl->vp_free[u & 1], (u >> 1) ^ 1, DEVERR_MMA_TIMEOUT);
+        if (!ok) break;
+#pragma unroll
+        for (int m = 0; m < 32 / step; ++m) {
+          // V' = f v with f = f1 + f2: hi = bf16(f1 v), whose error fits in bf16 itself, and lo =
+          // bf16(that error + f2 v)
+          const uint32_t f = tb.f[32 * q + t0 + m * step];
+          const uint32_t f1 = __byte_perm(f, 0, 0x1010), f2 = __byte_perm(f, 0, 0x3232);
+          const uint4 x = *reinterpret_cast<const uint4 *>(src + m * step * 128);
+          const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+          uint32_t h4[4], l4[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            h4[e] = mul_bf16x2(f1, xs[e]);
+            l4[e] = fma_bf16x2(f2, xs[e], fma_bf16x2(f1, xs[e], h4[e] ^ 0x80008000u));
+          }
+          *reinterpret_cast<uint4 *>(dst + m * step * 128) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
+          *reinterpret_cast<uint4 *>(dst + F::kTileVP + m * step * 128) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
+        }
+        if (part < kC) {
+          // behind the segment: zeros in V', V and K, since 0 times another sequence's infinity
+          // would not vanish in the products
+#pragma unroll 1
+          for (int m = 0; m < 32 / step; ++m) {
+            const int tt = 32 * q + t0 + m * step;
+            if (tt < part) continue;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(dst + m * step * 128) = zero;
+            *reinterpret_cast<uint4 *>(dst + F::kTileVP + m * step * 128) = zero;
+            *reinterpret_cast<uint4 *>(src + m * step * 128) = zero;
+            for (int b = 0; b < 128 / kDV; ++b)
+              *reinterpret_cast<uint4 *>(smem + F::oK + (n % F::kNK) * kTileQK +
+                                         sw128_chunk(tt, j & 7, kDV == 128 ? j >> 3 : b, 128)) = zero;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->vp_full[u & 1]);
+      }
+      if (ok && lane == 0) mbar_arrive(&ctl->tab_free[n & 1]);
+    }
+  } else if (warp >= 12) {
+    // ---- the state and the output
     constexpr int kHalf = kDV / 2;  // columns per thread
-    const int half = (warp - 8) >> 2, w = warp & 3, r = 32 * w + lane, wt = tid - 256;
+    const int half = (warp - 12) >> 2, w = warp & 3, r = 32 * w + lane;
     const uint32_t row = uint32_t(32 * w) << 16;
     const int cb = half * kHalf;  // first column within the tile
     const int64_t dd = int64_t(a.d_k) * a.d_v;
@@ -402,6 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         S[c] = x.x, S[c + 1] = x.y, S[c + 2] = x.z, S[c + 3] = x.w;
       }
     }
+    const uint32_t state_off = sw128_chunk(r, 0, cb >> 6, 128);
     auto write_state_tile = [&]() {  // the B operand of Q S: rows k, MN-major
 #pragma unroll
       for (int c = 0; c < kHalf; c += 8) {
@@ -414,71 +554,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             l[e] = pack_bf16x2(S[c + 2 * e] - b.x, S[c + 2 * e + 1] - b.y);
           }
         }
-        const uint32_t o = sw128_chunk(r, ((cb + c) >> 3) & 7, (cb + c) >> 6, 128);
+        const uint32_t o = state_off ^ ((((cb + c) >> 3) & 7) << 4);
         *reinterpret_cast<uint4 *>(smem + F::oS + o) = make_uint4(u[0], u[1], u[2], u[3]);
         if constexpr (kPair)
           *reinterpret_cast<uint4 *>(smem + F::oS + F::kTileS + o) = make_uint4(l[0], l[1], l[2], l[3]);
       }
     };
-    // quarter q of chunk n's V' (32 tokens) into its buffer
-    auto convert = [&](int n, int q) -> bool {
-      const int u = 4 * n + q;
-      const Table &tb = tab[n & 1];
-      uint8_t *V = smem + F::oV + (n & 1) * F::kTileV, *hi = smem + F::oVP + (u & 1) * 2 * F::kTileVP;
-      if (q == 0) {
-        if (!wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) return false;
-        if (!wait_warp(ctl->v_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) return false;
-      }
-      const bool partial = (n + 1) * kC > len;  // rows behind the segment hold another's tokens
-      if (partial && q == 0 && !wait_warp(ctl->k_full[n % F::kNK], n / F::kNK, DEVERR_TMA_TIMEOUT)) return false;
-      if (!wait_warp(ctl->vp_free[u & 1], (u >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) return false;
-      const float after = tb.after[q];
-#pragma unroll
-      for (int i = wt; i < 4 * kDV; i += 256) {  // pieces of 8 columns
-        const int t = i / (kDV / 8), j = i % (kDV / 8), tt = 32 * q + t;
-        uint4 *src = reinterpret_cast<uint4 *>(V + sw128_chunk(tt, j & 7, j >> 3, 128));
-        uint4 *dst = reinterpret_cast<uint4 *>(hi + sw128_chunk(t, j & 7, j >> 3, 32));
-        uint4 *dst_lo = reinterpret_cast<uint4 *>(reinterpret_cast<uint8_t *>(dst) + F::kTileVP);
-        if (partial && n * kC + tt >= len) {
-          // zero here and in K: a product of 0 with another sequence's infinity would not vanish
-          *src = *dst = *dst_lo = make_uint4(0, 0, 0, 0);
-          uint8_t *K = smem + F::oK + (n % F::kNK) * kTileQK;
-#pragma unroll
-          for (int b = 0; b < 128 / kDV; ++b)
-            *reinterpret_cast<uint4 *>(K + sw128_chunk(tt, j & 7, kDV == 128 ? j >> 3 : b, 128)) = make_uint4(0, 0, 0, 0);
-          continue;
-        }
-        const float f = tb.es[tt] * after;
-        const uint4 x = *src;
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-        uint32_t h4[4], l4[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 y = f2_mul(unpack_bf16x2(xs[e]), make_float2(f, f));
-          h4[e] = pack_bf16x2(y.x, y.y);
-          const float2 b = unpack_bf16x2(h4[e]);
-          l4[e] = pack_bf16x2(y.x - b.x, y.y - b.y);
-        }
-        *dst = make_uint4(h4[0], h4[1], h4[2], h4[3]);
-        *dst_lo = make_uint4(l4[0], l4[1], l4[2], l4[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->vp_full[u & 1]);
-      return true;
-    };
-    bool ok = true;
     if constexpr (!kStateOnly) {
       write_state_tile();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->s_full);
     }
-    if (chunks > 0) ok = convert(0, 0) && convert(0, 1);
-    for (int n = 0; ok && n < chunks; ++n) {
-      ok = convert(n, 2) && convert(n, 3);
-      if (!ok) break;
+#pragma unroll 1
+    for (int n = 0; n < chunks; ++n) {
       const Table &tb = tab[n & 1];
+      if (!wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
       const float e1 = tb.e1;
       float eG = 0.f;  // e^{G_r}, the decay of the entering state at token r
       if constexpr (!kStateOnly) {
@@ -486,60 +577,70 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int B = 0; B < 3; ++B)
           if (B < w) eG += tb.t[B];
-        eG = ex2(eG);
+        eG = a.scale * ex2(eG);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->tab_free[n & 1]);
       // the state: S <- e^{G_C} S + K^T V'
-      ok = wait_warp(ctl->d_done, n, DEVERR_MMA_TIMEOUT);
-      if (!ok) break;
+      if (!wait_warp(ctl->d_done, n, DEVERR_MMA_TIMEOUT)) break;
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < kHalf; c += 16) {
         float d[16];
         tmem_ld16_wait(tD + row + cb + c, d);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) S[c + e] = decay_step(S[c + e], e1) + d[e];
+        for (int e = 0; e < 16; e += 2) {
+          const float2 x = make_float2(S[c + e], S[c + e + 1]);
+          const float2 y = f2_add(f2_fma(make_float2(e1, e1), x, x), make_float2(d[e], d[e + 1]));
+          S[c + e] = y.x, S[c + e + 1] = y.y;
+        }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->tab_free[n & 1]);
-      if (n + 1 < chunks) ok = convert(n + 1, 0) && convert(n + 1, 1);
-      if (!ok) break;
+      if (lane == 0) mbar_arrive(&ctl->d_free);
       if constexpr (!kStateOnly) {
-        ok = wait_warp(ctl->qs_done, n, DEVERR_MMA_TIMEOUT);
-        if (!ok) break;
+        if (!wait_warp(ctl->qs_done, n, DEVERR_MMA_TIMEOUT)) break;
         tc_fence_after();
+        if (n + 1 < chunks) write_state_tile();
         const int64_t t = s.t0 + int64_t(n) * kC + r;
+        const bool whole = (n + 1) * kC <= len;
+        uint8_t *stage = smem + F::oQ + (n & 1) * kTileQK;
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 16) {
-          float oi[16], ox[16];
-          tmem_ld16(tOI + row + cb + c, oi);
-          tmem_ld16(tOX + row + cb + c, ox);
+        for (int c = 0; c < kHalf; c += 8) {
+          float oi[8], ox[8];
+          tmem_ld8(tOI + row + cb + c, oi);
+          tmem_ld8(tOX + row + cb + c, ox);
           tmem_ld_wait(oi, ox);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) oi[e] = a.scale * fmaf(eG, ox[e], oi[e]);
-          if (t < s.t1) {
-            const int col = col0 + cb + c;
-            const int64_t at = (t * a.H + h) * a.d_v + col;
+          for (int e = 0; e < 8; e += 2) {
+            const float2 y = f2_fma(make_float2(eG, eG), make_float2(ox[e], ox[e + 1]),
+                                    f2_mul(make_float2(a.scale, a.scale), make_float2(oi[e], oi[e + 1])));
+            oi[e] = y.x, oi[e + 1] = y.y;
+          }
+          const int cc = cb + c, col = col0 + cc;
+          const bool direct = !whole && t < s.t1 && col < a.d_v;  // rows of a part of a tile
+          const int64_t at = (t * a.H + h) * a.d_v + col;
+          if constexpr (kOutBF16) {
+            const uint4 u = make_uint4(pack_bf16x2(oi[0], oi[1]), pack_bf16x2(oi[2], oi[3]), pack_bf16x2(oi[4], oi[5]),
+                                       pack_bf16x2(oi[6], oi[7]));
+            if (whole) *reinterpret_cast<uint4 *>(stage + sw128_chunk(r, (cc >> 3) & 7, cc >> 6, 128)) = u;
+            else if (direct) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at) = u;
+          } else {
 #pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              if (col + e >= a.d_v) continue;
-              if constexpr (kOutBF16) {
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at + e) =
-                    make_uint4(pack_bf16x2(oi[e], oi[e + 1]), pack_bf16x2(oi[e + 2], oi[e + 3]),
-                               pack_bf16x2(oi[e + 4], oi[e + 5]), pack_bf16x2(oi[e + 6], oi[e + 7]));
-              } else {
-                float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at + e);
-                p[0] = make_float4(oi[e], oi[e + 1], oi[e + 2], oi[e + 3]);
-                p[1] = make_float4(oi[e + 4], oi[e + 5], oi[e + 6], oi[e + 7]);
-              }
+            for (int f = 0; f < 8; f += 4) {
+              const float4 u = make_float4(oi[f], oi[f + 1], oi[f + 2], oi[f + 3]);
+              if (whole) *reinterpret_cast<float4 *>(stage + sw128_chunk(r, ((cc + f) >> 2) & 7, cc >> 5, 128)) = u;
+              else if (direct) *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at + f) = u;
             }
           }
         }
-        if (n + 1 < chunks) write_state_tile();
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->s_full);
+        if (lane == 0) {
+          mbar_arrive(&ctl->s_full);
+          mbar_arrive(&ctl->o_full);
+        }
       }
     }
     float *dst = kStateOnly ? a.seg_states + (int64_t(slot) * a.H + h) * dd
@@ -563,16 +664,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int kDV, bool kOutBF16, bool kStateOnly>
-cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const LinearArgs &a,
-                       cudaStream_t stream) {
+cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
+                       const LinearArgs &a, cudaStream_t stream) {
   using F = Cfg<kDV, kOutBF16, kStateOnly>;
-  constexpr uint32_t smem = F::oTab + 2 * sizeof(Table) + sizeof(Control);
+  constexpr uint32_t smem = F::oTab + 2 * sizeof(Table) + sizeof(Control<F::kNK>);
   static_assert(smem <= 232448, "shared memory of one CTA");
   const auto kern = linear_chunked_kernel<kDV, kOutBF16, kStateOnly>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   const dim3 grid(unsigned(a.plan.slots) * unsigned(a.H), unsigned((a.d_v + kDV - 1) / kDV));
-  kern<<<grid, kThreads, smem, stream>>>(mq, mk, mv, a, device_error_word());
+  kern<<<grid, kThreads, smem, stream>>>(mq, mk, mv, mo, a, device_error_word());
   return cudaGetLastError();
 }
 
@@ -581,21 +682,22 @@ cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
 bool linear_chunked_supported(int d_k, int d_v, bool in_bf16) { return in_bf16 && d_k % 8 == 0 && d_v % 8 == 0; }
 
 cudaError_t launch_linear_chunked(const LinearArgs &a, bool out_bf16, cudaStream_t stream) {
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   if (!tensor_map_3d(&mq, a.q, true, a.total, a.H_k, a.d_k, 64, kC, true) ||
       !tensor_map_3d(&mk, a.k, true, a.total, a.H_k, a.d_k, 64, kC, true) ||
-      !tensor_map_3d(&mv, a.v, true, a.total, a.H, a.d_v, 64, kC, true))
+      !tensor_map_3d(&mv, a.v, true, a.total, a.H, a.d_v, 64, kC, true) ||
+      !tensor_map_3d(&mo, a.out, out_bf16, a.total, a.H, a.d_v, out_bf16 ? 64 : 32, kC, true))
     return cudaErrorInvalidValue;
   const bool wide = a.plan.col_tile == 128;
   if (a.plan.seg_len != 0) {
-    cudaError_t e = wide ? launch_one<128, true, true>(mq, mk, mv, a, stream)
-                         : launch_one<64, true, true>(mq, mk, mv, a, stream);
+    cudaError_t e = wide ? launch_one<128, true, true>(mq, mk, mv, mo, a, stream)
+                         : launch_one<64, true, true>(mq, mk, mv, mo, a, stream);
     if (e == cudaSuccess) e = launch_linear_scan(a, stream);
     if (e != cudaSuccess) return e;
   }
-  if (wide) return launch_one<128, true, false>(mq, mk, mv, a, stream);
-  return out_bf16 ? launch_one<64, true, false>(mq, mk, mv, a, stream)
-                  : launch_one<64, false, false>(mq, mk, mv, a, stream);
+  if (wide) return launch_one<128, true, false>(mq, mk, mv, mo, a, stream);
+  return out_bf16 ? launch_one<64, true, false>(mq, mk, mv, mo, a, stream)
+                  : launch_one<64, false, false>(mq, mk, mv, mo, a, stream);
 }
 
 }  // namespace kda
