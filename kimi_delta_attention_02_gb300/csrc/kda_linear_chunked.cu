@@ -19,11 +19,12 @@
 // take an exponential per entry. A decay below 2^-127 per token counts as 2^-127, which leaves
 // nothing in fp32 either, so g = -infinity needs no case of its own.
 //
-// Warps (20): 0 loads (TMA), 1 issues the MMAs, 2 makes the decay tables, 3 stores the output tiles
-// (TMA), 4-7 form P (one query row per thread, in place in tensor memory: P is the A operand of
-// its product), 8-11 convert V to V' in quarters of 32 tokens, 12-19 keep the state (one key row
-// and half the columns per thread) and read out the output. Per chunk the tensor pipe runs
-// Q K^T, K^T V' (hi, lo), P V, Q S: 2560 cycles for 128 value columns; everything else runs beside.
+// Warps (20): 0 loads (TMA), 1 issues the MMAs Q K^T, Q S, P V, 2 makes the decay tables, 3 issues
+// K^T V' (on its own, so that either's waits are filled by the other's work), 4-7 form P (one
+// query row per thread, in place in tensor memory: P is the A operand of its product), 8-11 convert
+// V to V' in quarters of 32 tokens, 12-19 keep the state (one key row and half the columns per
+// thread) and read out the output. Per chunk the tensor pipe runs Q K^T, K^T V' (hi, lo), P V, Q S:
+// 2560 cycles for 128 value columns; everything else runs beside.
 #include "kda_linear.cuh"
 #include "kda_tma_host.h"
 
@@ -39,7 +40,7 @@ constexpr float kMinLog2 = -127.f;
 template <int kDV, bool kOutBF16, bool kStateOnly>
 struct Cfg {
   static constexpr bool kPair = !kOutBF16 && !kStateOnly;  // P and S as hi + lo
-  static constexpr int kNK = kDV == 128 && !kStateOnly ? 1 : 2, kNQ = kStateOnly ? 0 : 2, kNV = 2;
+  static constexpr int kNK = 2, kNQ = kStateOnly ? 0 : kDV == 128 ? 1 : 2, kNV = 2;  // buffers
   static constexpr uint32_t kTileV = 256u * kDV;
   static constexpr uint32_t kTileS = kStateOnly ? 0 : 256u * kDV;   // 128 key rows x kDV bf16
   static constexpr uint32_t kTileVP = 64u * kDV;                    // a quarter of V': 32 tokens
@@ -55,11 +56,11 @@ struct Table {  // decays of one chunk, log2 units unless said otherwise
   float e1;          // e^{G_C} - 1
 };
 
-template <int kNK>
+template <int kNQ>
 struct Control {
-  uint64_t k_full[kNK], k_free[kNK], q_full[2], q_free[2], v_full[2], v_free[2];
+  uint64_t k_full[2], k_free[2], q_full[kNQ], q_free[kNQ], v_full[2], v_free[2];
   uint64_t vp_full[2], vp_free[2], tab_full[2], tab_free[2];
-  uint64_t qk_done, p_full, d_done, d_free, s_full, pv_done, qs_done, o_full, drain;
+  uint64_t qk_done, p_full, d_done, d_free, s_full, o_free, pv_done, qs_done, drain;
   uint32_t tmem;
   volatile uint32_t abort;
 };
@@ -82,8 +83,13 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   return r;
 }
 
-// The MMA warp runs as a whole, so that descriptors stay in uniform registers (a lone lane has to
-// move each one there), and its leader lane alone issues.
+// An MMA warp runs as a whole, so that descriptors stay in uniform registers (a lone lane has to
+// move each one there), and its elected lane alone issues.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 //   D[tmem] (+)= A[smem] x B[smem], bf16
 __device__ __forceinline__ void mma_ss(bool leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                        uint32_t accumulate) {
@@ -126,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool kPair = F::kPair;
   extern __shared__ __align__(1024) uint8_t smem[];
   Table *tab = reinterpret_cast<Table *>(smem + F::oTab);
-  auto *ctl = reinterpret_cast<Control<F::kNK> *>(smem + F::oTab + 2 * sizeof(Table));
+  auto *ctl = reinterpret_cast<Control<F::kNQ == 0 ? 1 : F::kNQ> *>(smem + F::oTab + 2 * sizeof(Table));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H, hk = h / (a.H / a.H_k);
   const int col0 = blockIdx.y * kDV;
@@ -138,15 +144,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      if (i < F::kNK) mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_free[i], 1);
-      mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->q_free[i], 1);
-      mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_free[i], 1);
+      mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_free[i], 1);
+      if (i < F::kNQ) mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->q_free[i], 1);
+      mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_free[i], kStateOnly ? 4 : 5);
       mbar_init(&ctl->vp_full[i], 4), mbar_init(&ctl->vp_free[i], 1);
       mbar_init(&ctl->tab_full[i], 1), mbar_init(&ctl->tab_free[i], kStateOnly ? 12 : 16);
     }
     mbar_init(&ctl->qk_done, 1), mbar_init(&ctl->p_full, 4), mbar_init(&ctl->d_done, 1);
-    mbar_init(&ctl->s_full, 8), mbar_init(&ctl->pv_done, 1), mbar_init(&ctl->qs_done, 1);
-    mbar_init(&ctl->d_free, 8), mbar_init(&ctl->o_full, 8), mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->d_free, 8), mbar_init(&ctl->s_full, 8), mbar_init(&ctl->o_free, 8);
+    mbar_init(&ctl->pv_done, 1), mbar_init(&ctl->qs_done, 1), mbar_init(&ctl->drain, kStateOnly ? 1 : 2);
     ctl->abort = 0;
     fence_mbarrier_init();
   }
@@ -175,14 +181,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    // ---- loads: chunk n's V, Q and K, each when its buffer is free (K last: with one buffer it
-    // waits for the chunk before); chunk n + 1's tiles go to L2 meanwhile
+    // ---- loads: chunk n's V, Q and K, each when its buffer is free; chunk n + 1's tiles go to L2
+    // meanwhile
     if (lane == 0) {
+      constexpr int kNQ = kStateOnly ? 1 : F::kNQ;
       int issued = 0;
 #pragma unroll 1
       for (int n = 0; n < chunks; ++n) {
         const int32_t t = int32_t(s.t0) + n * kC;
-        const int sk = n % F::kNK, s2 = n & 1;
+        const int s2 = n & 1, sq = n % kNQ;
         if (!wait(ctl->v_free[s2], (n >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) break;
         mbar_arrive_expect_tx(&ctl->v_full[s2], F::kTileV);
 #pragma unroll
@@ -190,18 +197,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(smem + F::oV + s2 * F::kTileV + b * 16384, &mv, &ctl->v_full[s2], col0 + 64 * b, h, t);
         issued = 3 * n + 1;
         if constexpr (!kStateOnly) {
-          if (!wait(ctl->q_free[s2], (n >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) break;
-          mbar_arrive_expect_tx(&ctl->q_full[s2], kTileQK);
+          if (!wait(ctl->q_free[sq], (n / kNQ) ^ 1, DEVERR_MMA_TIMEOUT)) break;
+          mbar_arrive_expect_tx(&ctl->q_full[sq], kTileQK);
 #pragma unroll
           for (int b = 0; b < 2; ++b)
-            tma_load_3d(smem + F::oQ + s2 * kTileQK + b * 16384, &mq, &ctl->q_full[s2], 64 * b, hk, t);
+            tma_load_3d(smem + F::oQ + sq * kTileQK + b * 16384, &mq, &ctl->q_full[sq], 64 * b, hk, t);
         }
         issued = 3 * n + 2;
-        if (!wait(ctl->k_free[sk], (n / F::kNK) ^ 1, DEVERR_MMA_TIMEOUT)) break;
-        mbar_arrive_expect_tx(&ctl->k_full[sk], kTileQK);
+        if (!wait(ctl->k_free[s2], (n >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) break;
+        mbar_arrive_expect_tx(&ctl->k_full[s2], kTileQK);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
-          tma_load_3d(smem + F::oK + sk * kTileQK + b * 16384, &mk, &ctl->k_full[sk], 64 * b, hk, t);
+          tma_load_3d(smem + F::oK + s2 * kTileQK + b * 16384, &mk, &ctl->k_full[s2], 64 * b, hk, t);
         issued = 3 * n + 3;
         if (n + 1 < chunks) {
 #pragma unroll
@@ -213,38 +220,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int b = 0; b < kDV / 64; ++b) tma_prefetch_l2_3d(&mv, col0 + 64 * b, h, t + kC);
         }
       }
-      // every load issued has landed before the CTA may end
+      // every load issued has landed before the CTA may end: the last of each buffer
       const int nv = (issued + 2) / 3, nq = (issued + 1) / 3, nk = issued / 3;
 #pragma unroll 1
-      for (int n = nk > F::kNK ? nk - F::kNK : 0; n < nk; ++n)
-        mbar_wait(&ctl->k_full[n % F::kNK], (n / F::kNK) & 1, err_word, DEVERR_TMA_TIMEOUT);
+      for (int n = nk > 2 ? nk - 2 : 0; n < nk; ++n)
+        mbar_wait(&ctl->k_full[n & 1], (n >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
       if constexpr (!kStateOnly)
 #pragma unroll 1
-        for (int n = nq > 2 ? nq - 2 : 0; n < nq; ++n)
-          mbar_wait(&ctl->q_full[n & 1], (n >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
+        for (int n = nq > kNQ ? nq - kNQ : 0; n < nq; ++n)
+          mbar_wait(&ctl->q_full[n % kNQ], (n / kNQ) & 1, err_word, DEVERR_TMA_TIMEOUT);
 #pragma unroll 1
       for (int n = nv > 2 ? nv - 2 : 0; n < nv; ++n)
         mbar_wait(&ctl->v_full[n & 1], (n >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
     }
   } else if (warp == 1) {
-    // ---- MMAs
-    constexpr uint32_t iQK = umma_idesc_bf16(128, 128, false, false, false);
-    constexpr uint32_t iD = umma_idesc_bf16(128, kDV, true, true, false);
-    constexpr uint32_t iPV = umma_idesc_bf16(128, kDV, false, true, false);  // P V and Q S
-    const bool leader = lane == 0;
-    const uint32_t base = smem_u32(smem);
-    // Descriptors of the first buffers; an operand elsewhere is `bytes / 16` further (addresses
-    // stay below 2^18, so the address field never carries).
-    const uint64_t dQ = desc_k(base + F::oQ), dK = desc_k(base + F::oK), dKt = desc_mn(base + F::oK, 16384);
-    const uint64_t dV = desc_mn(base + F::oV, 16384), dVP = desc_mn(base + F::oVP, 4096);
-    const uint64_t dS = desc_mn(base + F::oS, 16384);
+    // ---- Q K^T, Q S, P V
+    if constexpr (!kStateOnly) {
+      constexpr uint32_t iQK = umma_idesc_bf16(128, 128, false, false, false);
+      constexpr uint32_t iPV = umma_idesc_bf16(128, kDV, false, true, false);  // P V and Q S
+      const bool leader = elect_lane();
+      const uint32_t base = smem_u32(smem);
+      // Descriptors of the first buffers; an operand elsewhere is `bytes / 16` further (addresses
+      // stay below 2^18, so the address field never carries).
+      const uint64_t dQ = desc_k(base + F::oQ), dK = desc_k(base + F::oK);
+      const uint64_t dV = desc_mn(base + F::oV, 16384), dS = desc_mn(base + F::oS, 16384);
 #pragma unroll 1
-    for (int n = 0; n < chunks; ++n) {
-      const uint32_t nk = uint32_t(n % F::kNK) * (kTileQK >> 4), nq = uint32_t(n & 1) * (kTileQK >> 4),
-                     nv = uint32_t(n & 1) * (F::kTileV >> 4);
-      if (!wait_warp(ctl->k_full[n % F::kNK], n / F::kNK, DEVERR_TMA_TIMEOUT)) break;
-      if constexpr (!kStateOnly) {
-        if (!wait_warp(ctl->q_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
+      for (int n = 0; n < chunks; ++n) {
+        const int sq = n % F::kNQ;
+        const uint32_t nk = uint32_t(n & 1) * (kTileQK >> 4), nq = uint32_t(sq) * (kTileQK >> 4),
+                       nv = uint32_t(n & 1) * (F::kTileV >> 4);
+        if (!wait_warp(ctl->k_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
+        if (!wait_warp(ctl->q_full[sq], n / F::kNQ, DEVERR_TMA_TIMEOUT)) break;
         // P of chunk n - 1 has been read out of the columns Q K^T goes to
         if (n > 0 && !wait_warp(ctl->pv_done, n - 1, DEVERR_MMA_TIMEOUT)) break;
         tc_fence_after();
@@ -254,11 +260,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ss(leader, tQK, dQ + (nq + o), dK + (nk + o), iQK, ks > 0);
         }
         mma_commit(leader, ctl->qk_done);
+        if (!wait_warp(ctl->s_full, n, DEVERR_MMA_TIMEOUT)) break;
+        if (n > 0 && !wait_warp(ctl->o_free, n - 1, DEVERR_MMA_TIMEOUT)) break;  // O of chunk n - 1 is read out
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < (kPair ? 16 : 8); ++ks)
+          mma_ss(leader, tOX, dQ + (nq + ((ks & 7) >> 2) * 1024 + (ks & 3) * 2),
+                 dS + ((ks >> 3) * (F::kTileS >> 4) + (ks & 7) * 128), iPV, ks > 0);
+        mma_commit(leader, ctl->qs_done);
+        mma_commit(leader, ctl->q_free[sq]);
+        if (!wait_warp(ctl->p_full, n, DEVERR_MMA_TIMEOUT)) break;
+        // the last chunk's rows behind the segment: V is zeroed there before K^T V' begins
+        if ((n + 1) * kC > len && !wait_warp(ctl->d_done, n, DEVERR_MMA_TIMEOUT)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int ks = 0; ks < (kPair ? 16 : 8); ++ks)
+          mma_ts(leader, tOI, (ks < 8 ? tQK : tPL) + 8 * (ks & 7), dV + (nv + (ks & 7) * 128), iPV, ks > 0);
+        mma_commit(leader, ctl->pv_done);
+        mma_commit(leader, ctl->v_free[n & 1]);
       }
-      if (n > 0 && !wait_warp(ctl->d_free, n - 1, DEVERR_MMA_TIMEOUT)) break;
-      bool ok = true;
+      // no MMA is in flight when tensor memory is freed
+      mma_commit(leader, ctl->drain);
+      if (leader) mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
+    }
+  } else if (warp == 3) {
+    // ---- K^T V', 32 tokens at a time
+    constexpr uint32_t iD = umma_idesc_bf16(128, kDV, true, true, false);
+    const bool leader = elect_lane();
+    const uint32_t base = smem_u32(smem);
+    const uint64_t dKt = desc_mn(base + F::oK, 16384), dVP = desc_mn(base + F::oVP, 4096);
+    bool ok = true;
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {  // K^T V', 32 tokens at a time
+    for (int n = 0; ok && n < chunks; ++n) {
+      const uint32_t nk = uint32_t(n & 1) * (kTileQK >> 4);
+      if (!wait_warp(ctl->k_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
+      if (n > 0 && !wait_warp(ctl->d_free, n - 1, DEVERR_MMA_TIMEOUT)) break;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
         const int u = 4 * n + q;
         ok = wait_warp(ctl->vp_full[u & 1], u >> 1, DEVERR_MMA_TIMEOUT);
         if (!ok) break;
@@ -272,26 +310,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       mma_commit(leader, ctl->d_done);
-      mma_commit(leader, ctl->k_free[n % F::kNK]);
-      if constexpr (kStateOnly) {
-        mma_commit(leader, ctl->v_free[n & 1]);
-      } else {
-        if (!wait_warp(ctl->p_full, n, DEVERR_MMA_TIMEOUT)) break;
-        if (!wait_warp(ctl->s_full, n, DEVERR_MMA_TIMEOUT)) break;  // and O of chunk n - 1 is read out
-        tc_fence_after();
-#pragma unroll
-        for (int ks = 0; ks < (kPair ? 16 : 8); ++ks)
-          mma_ts(leader, tOI, (ks < 8 ? tQK : tPL) + 8 * (ks & 7), dV + (nv + (ks & 7) * 128), iPV, ks > 0);
-        mma_commit(leader, ctl->pv_done);
-        mma_commit(leader, ctl->v_free[n & 1]);
-#pragma unroll
-        for (int ks = 0; ks < (kPair ? 16 : 8); ++ks)
-          mma_ss(leader, tOX, dQ + (nq + ((ks & 7) >> 2) * 1024 + (ks & 3) * 2),
-                 dS + ((ks >> 3) * (F::kTileS >> 4) + (ks & 7) * 128), iPV, ks > 0);
-        mma_commit(leader, ctl->qs_done);
-      }
+      if constexpr (kStateOnly) mma_commit(leader, ctl->k_free[n & 1]);
     }
-    // no MMA is in flight when tensor memory is freed
     mma_commit(leader, ctl->drain);
     if (leader) mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
   } else if (warp == 2) {
@@ -434,29 +454,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 3) {
-    // ---- output tiles: whole chunks leave through TMA from the chunk's Q buffer (its last MMA is
-    // done), which is free again once the copy has read it
-    if constexpr (!kStateOnly) {
-      if (lane == 0) {
-#pragma unroll 1
-        for (int n = 0; n < chunks; ++n) {
-          if (!wait(ctl->o_full, n, DEVERR_MMA_TIMEOUT)) break;
-          if ((n + 1) * kC <= len) {
-            constexpr int kBox = kOutBF16 ? 64 : 32;
-#pragma unroll
-            for (int b = 0; b < kDV / kBox; ++b)
-              if (col0 + kBox * b < a.d_v)
-                tma_store_3d(&mo, smem + F::oQ + (n & 1) * kTileQK + b * 16384, col0 + kBox * b, h,
-                             int32_t(s.t0) + n * kC);
-            bulk_commit();
-            bulk_wait_read();
-          }
-          mbar_arrive(&ctl->q_free[n & 1]);
-        }
-        bulk_wait_all();
-      }
-    }
   } else if (warp >= 8 && warp < 12) {
     // ---- V': quarters of 32 tokens, two buffers
     const int wt = tid - 256;
@@ -470,8 +467,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Table &tb = tab[n & 1];
       ok = wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT) &&
            wait_warp(ctl->v_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT);
-      const int part = len - n * kC;  // rows from here on hold another sequence's tokens
-      if (ok && part < kC) ok = wait_warp(ctl->k_full[n % F::kNK], n / F::kNK, DEVERR_TMA_TIMEOUT);
+      const int part = len - n * kC;
+      if (ok && part < kC) {
+        // rows from here on hold another sequence's tokens: zeros in V and K, since 0 times another
+        // sequence's infinity would not vanish in the products
+        ok = wait_warp(ctl->k_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT);
+        uint8_t *K = smem + F::oK + (n & 1) * kTileQK;
+#pragma unroll 1
+        for (int m = 0; ok && m < kC / step; ++m) {  // each thread its own pieces of V, and K's beside
+          const int tt = t0 + m * step;
+          if (tt < part) continue;
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(smem + F::oV + (n & 1) * F::kTileV + src_off + m * step * 128) = zero;
+          for (int b = 0; b < 128 / kDV; ++b)
+            *reinterpret_cast<uint4 *>(K + sw128_chunk(tt, j & 7, kDV == 128 ? j >> 3 : b, 128)) = zero;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
 #pragma unroll 1
       for (int q = 0; ok && q < 4; ++q) {
         const int u = 4 * n + q;
@@ -496,27 +509,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4 *>(dst + m * step * 128) = make_uint4(h4[0], h4[1], h4[2], h4[3]);
           *reinterpret_cast<uint4 *>(dst + F::kTileVP + m * step * 128) = make_uint4(l4[0], l4[1], l4[2], l4[3]);
         }
-        if (part < kC) {
-          // behind the segment: zeros in V', V and K, since 0 times another sequence's infinity
-          // would not vanish in the products
-#pragma unroll 1
-          for (int m = 0; m < 32 / step; ++m) {
-            const int tt = 32 * q + t0 + m * step;
-            if (tt < part) continue;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4 *>(dst + m * step * 128) = zero;
-            *reinterpret_cast<uint4 *>(dst + F::kTileVP + m * step * 128) = zero;
-            *reinterpret_cast<uint4 *>(src + m * step * 128) = zero;
-            for (int b = 0; b < 128 / kDV; ++b)
-              *reinterpret_cast<uint4 *>(smem + F::oK + (n % F::kNK) * kTileQK +
-                                         sw128_chunk(tt, j & 7, kDV == 128 ? j >> 3 : b, 128)) = zero;
-          }
-        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->vp_full[u & 1]);
       }
-      if (ok && lane == 0) mbar_arrive(&ctl->tab_free[n & 1]);
+      if (ok && lane == 0) {
+        mbar_arrive(&ctl->tab_free[n & 1]);
+        mbar_arrive(&ctl->v_free[n & 1]);
+      }
     }
   } else if (warp >= 12) {
     // ---- the state and the output
@@ -568,6 +568,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 #pragma unroll 1
     for (int n = 0; n < chunks; ++n) {
+      if (!kStateOnly && tid == 384 && n > 0) {  // the copy of the tile before has read its buffer
+        bulk_wait_read();
+        mbar_arrive(&ctl->k_free[(n - 1) & 1]);
+      }
       const Table &tb = tab[n & 1];
       if (!wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
       const float e1 = tb.e1;
@@ -601,10 +605,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!kStateOnly) {
         if (!wait_warp(ctl->qs_done, n, DEVERR_MMA_TIMEOUT)) break;
         tc_fence_after();
-        if (n + 1 < chunks) write_state_tile();
+        if (n + 1 < chunks) {
+          write_state_tile();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->s_full);
+        }
+        if (!wait_warp(ctl->pv_done, n, DEVERR_MMA_TIMEOUT)) break;
+        tc_fence_after();
         const int64_t t = s.t0 + int64_t(n) * kC + r;
         const bool whole = (n + 1) * kC <= len;
-        uint8_t *stage = smem + F::oQ + (n & 1) * kTileQK;
+        uint8_t *stage = smem + F::oK + (n & 1) * kTileQK;
 #pragma unroll
         for (int c = 0; c < kHalf; c += 8) {
           float oi[8], ox[8];
@@ -634,15 +645,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
+        // a whole chunk's tile leaves by TMA from the chunk's K buffer, whose last MMA is done; the
+        // buffer is free again once the copy has read it
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl->s_full);
-          mbar_arrive(&ctl->o_full);
+        if (lane == 0) mbar_arrive(&ctl->o_free);
+        if (warp == 12 && whole) {
+          if (!wait_warp(ctl->o_free, n, DEVERR_MMA_TIMEOUT)) break;
+          if (lane == 0) {
+            constexpr int kBox = kOutBF16 ? 64 : 32;
+#pragma unroll
+            for (int b = 0; b < kDV / kBox; ++b)
+              if (col0 + kBox * b < a.d_v)
+                tma_store_3d(&mo, smem + F::oK + (n & 1) * kTileQK + b * 16384, col0 + kBox * b, h,
+                             int32_t(s.t0) + n * kC);
+            bulk_commit();
+          }
         }
       }
     }
+    if (!kStateOnly && tid == 384) bulk_wait_all();
     float *dst = kStateOnly ? a.seg_states + (int64_t(slot) * a.H + h) * dd
                  : (s.last && a.final_state != nullptr) ? a.final_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
     if (dst != nullptr && r < a.d_k) {
@@ -667,7 +690,7 @@ template <int kDV, bool kOutBF16, bool kStateOnly>
 cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
                        const LinearArgs &a, cudaStream_t stream) {
   using F = Cfg<kDV, kOutBF16, kStateOnly>;
-  constexpr uint32_t smem = F::oTab + 2 * sizeof(Table) + sizeof(Control<F::kNK>);
+  constexpr uint32_t smem = F::oTab + 2 * sizeof(Table) + sizeof(Control<F::kNQ == 0 ? 1 : F::kNQ>);
   static_assert(smem <= 232448, "shared memory of one CTA");
   const auto kern = linear_chunked_kernel<kDV, kOutBF16, kStateOnly>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
