@@ -166,7 +166,8 @@ def _ptr(t):
 
 def _stream_handle(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # torch.cuda.current_stream().cuda_stream without building the Stream object (0.2 against 3 us)
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -460,8 +461,43 @@ def decode(q, k, v, log_alpha, beta, state, *, out=None, out_dtype=torch.float32
     return out
 
 
-def _check_linear(q, k, v, log_decay, rows_name):
-    """Shapes and dtypes shared by linear_prefill and linear_decode; (rows, H_k, H, d_k, d_v, per_token)."""
+def _one_device(*tensors) -> int:
+    """The device index that all given tensors (None: left out) share, each contiguous on it."""
+    device = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0 or not t.is_contiguous():
+                raise ValueError("KDA tensors must be contiguous CUDA tensors")
+            if d != device:
+                if device >= 0:
+                    raise ValueError("KDA tensors must be on one CUDA device")
+                device = d
+    return device
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _used_on(stream, *tensors):
+    """Tensors allocated here for the caller's stream: the allocator must not hand their memory
+    to another stream's work before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _check_shape(name, t, shape, dtype=None):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+
+
+def _linear_sizes(q, k, v, log_decay, rows_name):
+    """Shapes and dtypes shared by linear_prefill and linear_decode: (rows, H_k, H, d_k, d_v)."""
     if q.ndim != 3 or v.ndim != 3 or k.shape != q.shape or v.shape[0] != q.shape[0]:
         raise ValueError(f"q and k must be [{rows_name}, H_k, d_k] and v [{rows_name}, H, d_v]")
     rows, H_k, d_k = q.shape
@@ -474,32 +510,7 @@ def _check_linear(q, k, v, log_decay, rows_name):
         raise TypeError("log_decay must be float32")
     if log_decay.shape != (rows, H) and log_decay.shape != (H,):
         raise ValueError(f"log_decay must be [{rows_name}, H] or [H]")
-    return rows, H_k, H, d_k, d_v, int(log_decay.ndim == 2)
-
-
-def _check_out(name, t, shape, dtype=None):
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}")
-
-
-def _check_one_device(*tensors):
-    """All given tensors contiguous and on one CUDA device, which is returned."""
-    _check_cuda(*tensors)
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1:
-        raise ValueError("KDA tensors must be on one CUDA device")
-    return devices.pop()
-
-
-def _used_on(stream, *tensors):
-    """Tensors allocated here for the caller's stream: the allocator must not hand their memory
-    to another stream's work before that stream is done with it."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    return rows, H_k, H, d_k, d_v
 
 
 def linear_workspace_size(total_tokens: int, num_seqs: int, H: int, d_k: int = 128, d_v: int = 128,
@@ -507,6 +518,11 @@ def linear_workspace_size(total_tokens: int, num_seqs: int, H: int, d_k: int = 1
     """Bytes of device scratch ``linear_prefill`` can use (``kda_linear_prefill_workspace_size``)."""
     return int(lib().kda_linear_prefill_workspace_size(int(total_tokens), int(num_seqs), int(H), int(d_k), int(d_v),
                                                        _io_dtype(dtype), _io_dtype(out_dtype), int(bool(recurrent))))
+
+
+_LINEAR_PREFILL_BYTES = ctypes.sizeof(LinearPrefillParams)
+_LINEAR_DECODE_BYTES = ctypes.sizeof(LinearDecodeParams)
+_BLOCK_NORM_BYTES = ctypes.sizeof(BlockNormParams)
 
 
 def linear_prefill(q, k, v, log_decay, cu_seqlens, init_state=None, *, out=None, final_state=None,
@@ -521,45 +537,44 @@ def linear_prefill(q, k, v, log_decay, cu_seqlens, init_state=None, *, out=None,
     out's dtype), final_state [N, H, d_k, d_v] or None). ``recurrent=True`` forces the fp32
     token-recurrent kernel. ``workspace``: ``"auto"`` allocates what ``linear_workspace_size``
     asks for, ``None`` passes none, a uint8 CUDA tensor is passed as given."""
-    T, H_k, H, d_k, d_v, per_token = _check_linear(q, k, v, log_decay, "T")
+    T, H_k, H, d_k, d_v = _linear_sizes(q, k, v, log_decay, "T")
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.ndim != 1 or cu_seqlens.shape[0] < 1:
         raise TypeError("cu_seqlens must be int32 [N + 1]")
     N = cu_seqlens.shape[0] - 1
-    device = _check_one_device(q, k, v, log_decay, cu_seqlens, init_state, out, final_state)
-    if device.index != torch.cuda.current_device():
+    given = workspace if isinstance(workspace, torch.Tensor) else None
+    device = _one_device(q, k, v, log_decay, cu_seqlens, init_state, out, final_state, given)
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return linear_prefill(q, k, v, log_decay, cu_seqlens, init_state, out=out, final_state=final_state,
                                   out_dtype=out_dtype, scale=scale, stream=stream, recurrent=recurrent,
                                   want_final=want_final, workspace=workspace)
     state_shape = (N, H, d_k, d_v)
     if init_state is not None:
-        _check_out("init_state", init_state, state_shape, torch.float32)
+        _check_shape("init_state", init_state, state_shape, torch.float32)
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=out_dtype, device=device)
+        out = torch.empty((T, H, d_v), dtype=out_dtype, device=q.device)
         _used_on(stream, out)
     else:
-        _check_out("out", out, (T, H, d_v))
+        _check_shape("out", out, (T, H, d_v))
     if final_state is not None:
-        _check_out("final_state", final_state, state_shape, torch.float32)
+        _check_shape("final_state", final_state, state_shape, torch.float32)
     elif want_final:
-        final_state = torch.empty(state_shape, dtype=torch.float32, device=device)
+        final_state = torch.empty(state_shape, dtype=torch.float32, device=q.device)
         _used_on(stream, final_state)
-    dt, odt = _io_dtype(q.dtype), _io_dtype(out.dtype)
-    if isinstance(workspace, str):
+    dt, odt, rec = _io_dtype(q.dtype), _io_dtype(out.dtype), 1 if recurrent else 0
+    handle = lib()
+    if given is None and workspace is not None:
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a uint8 CUDA tensor")
-        n = lib().kda_linear_prefill_workspace_size(T, N, H, d_k, d_v, dt, odt, int(bool(recurrent)))
-        workspace = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-        _used_on(stream, workspace)
-    elif workspace is not None and _check_one_device(workspace) != device:
-        raise ValueError("KDA tensors must be on one CUDA device")
-    p = LinearPrefillParams(ctypes.sizeof(LinearPrefillParams), dt, odt, N, H, H_k, d_k, d_v, per_token,
-                            int(bool(recurrent)), T, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                            cu_seqlens.data_ptr(), None if init_state is None else init_state.data_ptr(),
-                            out.data_ptr(), None if final_state is None else final_state.data_ptr(),
-                            None if workspace is None else workspace.data_ptr(),
-                            0 if workspace is None else workspace.numel() * workspace.element_size(), scale)
-    st = lib().kda_linear_prefill(ctypes.byref(p), _stream_handle(stream))
+        n = handle.kda_linear_prefill_workspace_size(T, N, H, d_k, d_v, dt, odt, rec)
+        if n:
+            given = torch.empty(n, dtype=torch.uint8, device=q.device)
+            _used_on(stream, given)
+    p = LinearPrefillParams(_LINEAR_PREFILL_BYTES, dt, odt, N, H, H_k, d_k, d_v, 1 if log_decay.ndim == 2 else 0, rec, T,
+                            q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), cu_seqlens.data_ptr(),
+                            _address(init_state), out.data_ptr(), _address(final_state), _address(given),
+                            0 if given is None else given.numel() * given.element_size(), scale)
+    st = handle.kda_linear_prefill(ctypes.byref(p), _stream_handle(stream))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_prefill")
     return out, final_state
@@ -569,20 +584,20 @@ def linear_decode(q, k, v, log_decay, state, *, out=None, out_dtype=torch.float3
     """One token of linear attention with one decay per head for B sequences
     (``kda_linear_decode``); ``state`` [B, H, d_k, d_v] float32 is updated in place.
     q, k [B, H_k, d_k], v [B, H, d_v], log_decay [B, H] or [H]. Returns out [B, H, d_v]."""
-    B, H_k, H, d_k, d_v, per_token = _check_linear(q, k, v, log_decay, "B")
-    device = _check_one_device(q, k, v, log_decay, state, out)
-    _check_out("state", state, (B, H, d_k, d_v), torch.float32)
-    if device.index != torch.cuda.current_device():
+    B, H_k, H, d_k, d_v = _linear_sizes(q, k, v, log_decay, "B")
+    device = _one_device(q, k, v, log_decay, state, out)
+    _check_shape("state", state, (B, H, d_k, d_v), torch.float32)
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return linear_decode(q, k, v, log_decay, state, out=out, out_dtype=out_dtype, scale=scale, stream=stream)
     if out is None:
-        out = torch.empty((B, H, d_v), dtype=out_dtype, device=device)
+        out = torch.empty((B, H, d_v), dtype=out_dtype, device=q.device)
         _used_on(stream, out)
     else:
-        _check_out("out", out, (B, H, d_v))
-    p = LinearDecodeParams(ctypes.sizeof(LinearDecodeParams), _io_dtype(q.dtype), _io_dtype(out.dtype), B, H, H_k, d_k,
-                           d_v, per_token, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                           state.data_ptr(), out.data_ptr())
+        _check_shape("out", out, (B, H, d_v))
+    p = LinearDecodeParams(_LINEAR_DECODE_BYTES, _io_dtype(q.dtype), _io_dtype(out.dtype), B, H, H_k, d_k, d_v,
+                           1 if log_decay.ndim == 2 else 0, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                           log_decay.data_ptr(), state.data_ptr(), out.data_ptr())
     st = lib().kda_linear_decode(ctypes.byref(p), _stream_handle(stream))
     if st != KDA_OK:
         raise KdaError(st, "kda_linear_decode")
@@ -622,32 +637,29 @@ def block_norm(x, y=None, *, gate=None, post_norm: bool = False, post_weight=Non
             raise ValueError("gate must be [rows, D] or [rows]")
     for w in (post_weight, channel_scale, pre_weight):
         if w is not None:
-            _check_out("a weight", w, (D,), torch.float32)
-    device = _check_one_device(x, y, gate, post_weight, channel_scale, pre_weight, residual_out, out)
-    if device.index != torch.cuda.current_device():
+            _check_shape("a weight", w, (D,), torch.float32)
+    device = _one_device(x, y, gate, post_weight, channel_scale, pre_weight, residual_out, out)
+    if device != torch._C._cuda_getDevice():
         with torch.cuda.device(device):
             return block_norm(x, y, gate=gate, post_norm=post_norm, post_weight=post_weight, scale=scale,
                               channel_scale=channel_scale, pre_weight=pre_weight, eps=eps, post_eps=post_eps,
                               residual_out=residual_out, out=out, out_dtype=out_dtype, want_out=want_out,
                               want_residual=want_residual, stream=stream)
     if residual_out is not None:
-        _check_out("residual_out", residual_out, (rows, D), x.dtype)
+        _check_shape("residual_out", residual_out, (rows, D), x.dtype)
     elif want_residual and y is not None:
         residual_out = torch.empty_like(x)
         _used_on(stream, residual_out)
     if out is not None:
-        _check_out("out", out, (rows, D))
+        _check_shape("out", out, (rows, D))
     elif want_out:
-        out = torch.empty((rows, D), dtype=x.dtype if out_dtype is None else out_dtype, device=device)
+        out = torch.empty_like(x, dtype=out_dtype)
         _used_on(stream, out)
-    p = BlockNormParams(ctypes.sizeof(BlockNormParams), _io_dtype(x.dtype), KDA_F32 if y is None else _io_dtype(y.dtype),
-                        KDA_F32 if out is None else _io_dtype(out.dtype), form, int(bool(post_norm)), D, scale, rows,
-                        x.data_ptr(), None if y is None else y.data_ptr(), None if gate is None else gate.data_ptr(),
-                        None if post_weight is None else post_weight.data_ptr(),
-                        None if channel_scale is None else channel_scale.data_ptr(),
-                        None if pre_weight is None else pre_weight.data_ptr(),
-                        None if residual_out is None else residual_out.data_ptr(),
-                        None if out is None else out.data_ptr(), eps if post_eps is None else post_eps, eps)
+    p = BlockNormParams(_BLOCK_NORM_BYTES, _io_dtype(x.dtype), KDA_F32 if y is None else _io_dtype(y.dtype),
+                        KDA_F32 if out is None else _io_dtype(out.dtype), form, 1 if post_norm else 0, D, scale, rows,
+                        x.data_ptr(), _address(y), _address(gate), _address(post_weight), _address(channel_scale),
+                        _address(pre_weight), _address(residual_out), _address(out),
+                        eps if post_eps is None else post_eps, eps)
     st = lib().kda_block_norm(ctypes.byref(p), _stream_handle(stream))
     if st != KDA_OK:
         raise KdaError(st, "kda_block_norm")

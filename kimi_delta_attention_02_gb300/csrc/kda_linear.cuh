@@ -32,7 +32,7 @@ struct LinearSlot {
   bool first, last;   // of its sequence
 };
 
-// False for an idle slot.
+// False for an idle slot. Called by whole warps.
 __device__ __forceinline__ bool linear_slot(const int32_t *__restrict__ cu, int num_seqs, int seg_len, int slot,
                                             LinearSlot &s) {
   if (seg_len == 0) {
@@ -42,11 +42,16 @@ __device__ __forceinline__ bool linear_slot(const int32_t *__restrict__ cu, int 
     s.first = s.last = true;
     return true;
   }
-  int lo = 0, hi = num_seqs - 1;  // the last n whose first slot cu[n] / L + n is <= slot
+  // The last n whose first slot cu[n] / L + n is <= slot: a warp tries 32 candidates at a time (two
+  // dependent reads for up to 1024 sequences, where halving takes ten). All lanes take part.
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = num_seqs - 1;
   while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (cu[mid] / seg_len + mid <= slot) lo = mid;
-    else hi = mid - 1;
+    const int stride = (hi - lo + 32) / 32, n = lo + lane * stride;
+    const bool fits = n <= hi && cu[n] / seg_len + n <= slot;  // true for lane 0, then false from some lane on
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, fits));
+    lo += last * stride;
+    hi = stride == 1 ? lo : (lo + stride - 1 < hi ? lo + stride - 1 : hi);
   }
   const int64_t bos = cu[lo], eos = cu[lo + 1];
   const int j = slot - (int(bos) / seg_len + lo);

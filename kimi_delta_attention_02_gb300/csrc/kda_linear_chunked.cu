@@ -19,12 +19,20 @@
 // take an exponential per entry. A decay below 2^-127 per token counts as 2^-127, which leaves
 // nothing in fp32 either, so g = -infinity needs no case of its own.
 //
+// Shared memory holds five 32 KB buffers that the chunks' tiles take in turn, Q K V Q K V ..., so that
+// a tile waits for the one five places before it: Q of chunk n for K of n - 2, K for V of n - 2, V for
+// Q of n - 1. Every one of these is done with well before its successor is needed. The output needs
+// no buffer: it goes from tensor memory through registers to global memory, 32 bytes (a whole
+// sector) per thread and store.
+//
 // Warps (20): 0 loads (TMA), 1 issues the MMAs Q K^T, Q S, P V, 2 makes the decay tables, 3 issues
 // K^T V' (on its own, so that either's waits are filled by the other's work), 4-7 form P (one
 // query row per thread, in place in tensor memory: P is the A operand of its product), 8-11 convert
 // V to V' in quarters of 32 tokens, 12-19 keep the state (one key row and half the columns per
-// thread) and read out the output. Per chunk the tensor pipe runs Q K^T, K^T V' (hi, lo), P V, Q S:
-// 2560 cycles for 128 value columns; everything else runs beside.
+// thread) and write the output (one token and half the columns). Per chunk the tensor pipe runs
+// Q K^T, K^T V' (hi, lo), P V, Q S: 2560 cycles for 128 value columns; everything else runs beside.
+#include <atomic>
+
 #include "kda_linear.cuh"
 #include "kda_tma_host.h"
 
@@ -33,34 +41,54 @@ namespace {
 
 constexpr int kC = 128;            // tokens per chunk
 constexpr int kThreads = 640;
-constexpr uint32_t kTileQK = 32768;  // 128 tokens x 128 channels bf16, two 64-channel blocks
+constexpr uint32_t kBuf = 32768;   // 128 tokens x 128 channels bf16, two 64-channel blocks
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMinLog2 = -127.f;
 
 template <int kDV, bool kOutBF16, bool kStateOnly>
 struct Cfg {
   static constexpr bool kPair = !kOutBF16 && !kStateOnly;  // P and S as hi + lo
-  static constexpr int kNK = 2, kNQ = kStateOnly ? 0 : kDV == 128 ? 1 : 2, kNV = 2;  // buffers
+  static constexpr int kBufs = kStateOnly ? 4 : 5;         // pass 1: K V K V
   static constexpr uint32_t kTileV = 256u * kDV;
   static constexpr uint32_t kTileS = kStateOnly ? 0 : 256u * kDV;   // 128 key rows x kDV bf16
   static constexpr uint32_t kTileVP = 64u * kDV;                    // a quarter of V': 32 tokens
-  static constexpr uint32_t oK = 0, oQ = oK + kNK * kTileQK, oV = oQ + kNQ * kTileQK, oS = oV + kNV * kTileV,
-                            oVP = oS + (kPair ? 2 : 1) * kTileS, oTab = oVP + 4 * kTileVP;
+  static constexpr uint32_t oS = kBufs * kBuf, oVP = oS + (kPair ? 2 : 1) * kTileS, oTab = oVP + 4 * kTileVP;
+};
+
+// The buffers of chunk n's tiles (tile i of the call in buffer i mod 5, in pass 1 i mod 4); step()
+// goes to the next chunk.
+template <bool kStateOnly>
+struct Bufs {
+  static constexpr uint32_t kBufs = kStateOnly ? 4 : 5;
+  uint32_t first = 0;
+  __device__ __forceinline__ uint32_t at(uint32_t i) const {
+    const uint32_t b = first + i;
+    return (b >= kBufs ? b - kBufs : b) * kBuf;
+  }
+  __device__ __forceinline__ uint32_t Q() const { return at(0); }
+  __device__ __forceinline__ uint32_t K() const { return at(kStateOnly ? 0 : 1); }
+  __device__ __forceinline__ uint32_t V() const { return at(kStateOnly ? 1 : 2); }
+  __device__ __forceinline__ void step() {
+    first += kStateOnly ? 2 : 3;
+    if (first >= kBufs) first -= kBufs;
+  }
 };
 
 struct Table {  // decays of one chunk, log2 units unless said otherwise
   float a[kC];       // from the block's start to the token, itself included
   float es[96];      // 2^(from behind the token to the block's end), blocks 0 .. 2
   uint32_t f[kC];    // e^{G_C - G_j} as a pair: the nearest bf16 (low half), what is left
-  float t[3];        // blocks 0 .. 2
   float e1;          // e^{G_C} - 1
+  float pad[3];
+  __device__ __forceinline__ float block(int B) const { return a[32 * B + 31]; }
 };
+static_assert(sizeof(Table) % 16 == 0, "128-bit reads of the second table");
 
-template <int kNQ>
 struct Control {
-  uint64_t k_full[2], k_free[2], q_full[kNQ], q_free[kNQ], v_full[2], v_free[2];
+  uint64_t q_full[2], k_full[2], v_full[2];            // by chunk parity
+  uint64_t qs_done[2], d_done[2], pv_done[2];          // Q S (and Q K^T before it), K^T V', P V
   uint64_t vp_full[2], vp_free[2], tab_full[2], tab_free[2];
-  uint64_t qk_done, p_full, d_done, d_free, s_full, o_free, pv_done, qs_done, drain;
+  uint64_t qk_done, p_full, d_free, s_full, o_read, drain;
   uint32_t tmem;
   volatile uint32_t abort;
 };
@@ -126,17 +154,21 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo) {
 template <int kDV, bool kOutBF16, bool kStateOnly>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_chunked_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
-                          const LinearArgs a, uint32_t *err_word) {
+                          const __grid_constant__ CUtensorMap mv, const LinearArgs a, uint32_t *err_word) {
   using F = Cfg<kDV, kOutBF16, kStateOnly>;
   constexpr bool kPair = F::kPair;
   extern __shared__ __align__(1024) uint8_t smem[];
   Table *tab = reinterpret_cast<Table *>(smem + F::oTab);
-  auto *ctl = reinterpret_cast<Control<F::kNQ == 0 ? 1 : F::kNQ> *>(smem + F::oTab + 2 * sizeof(Table));
+  Control *ctl = reinterpret_cast<Control *>(smem + F::oTab + 2 * sizeof(Table));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H, hk = h / (a.H / a.H_k);
   const int col0 = blockIdx.y * kDV;
 
+  if (tid == 0) {
+    if (!kStateOnly) tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
+  }
   LinearSlot s;
   if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, slot, s)) return;
   if (kStateOnly && s.last) return;
@@ -144,15 +176,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->k_free[i], 1);
-      if (i < F::kNQ) mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->q_free[i], 1);
-      mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_free[i], kStateOnly ? 4 : 5);
+      mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->v_full[i], 1);
+      mbar_init(&ctl->qs_done[i], 1), mbar_init(&ctl->d_done[i], 1), mbar_init(&ctl->pv_done[i], 1);
       mbar_init(&ctl->vp_full[i], 4), mbar_init(&ctl->vp_free[i], 1);
       mbar_init(&ctl->tab_full[i], 1), mbar_init(&ctl->tab_free[i], kStateOnly ? 12 : 16);
     }
-    mbar_init(&ctl->qk_done, 1), mbar_init(&ctl->p_full, 4), mbar_init(&ctl->d_done, 1);
-    mbar_init(&ctl->d_free, 8), mbar_init(&ctl->s_full, 8), mbar_init(&ctl->o_free, 8);
-    mbar_init(&ctl->pv_done, 1), mbar_init(&ctl->qs_done, 1), mbar_init(&ctl->drain, kStateOnly ? 1 : 2);
+    mbar_init(&ctl->qk_done, 1), mbar_init(&ctl->p_full, 4), mbar_init(&ctl->d_free, 8);
+    mbar_init(&ctl->s_full, 8), mbar_init(&ctl->o_read, 8), mbar_init(&ctl->drain, kStateOnly ? 1 : 2);
     ctl->abort = 0;
     fence_mbarrier_init();
   }
@@ -181,57 +211,51 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    // ---- loads: chunk n's V, Q and K, each when its buffer is free; chunk n + 1's tiles go to L2
+    // ---- loads: chunk n's Q, K and V, each when its buffer is free; chunk n + 1's tiles go to L2
     // meanwhile
     if (lane == 0) {
-      constexpr int kNQ = kStateOnly ? 1 : F::kNQ;
+      Bufs<kStateOnly> at;
       int issued = 0;
 #pragma unroll 1
-      for (int n = 0; n < chunks; ++n) {
+      for (int n = 0; n < chunks; ++n, at.step()) {
         const int32_t t = int32_t(s.t0) + n * kC;
-        const int s2 = n & 1, sq = n % kNQ;
-        if (!wait(ctl->v_free[s2], (n >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) break;
+        const int s2 = n & 1;
+        if (n >= 2 && !wait(ctl->d_done[s2], (n >> 1) - 1, DEVERR_MMA_TIMEOUT)) break;  // K (and V', so V) of n - 2
+        if constexpr (!kStateOnly) {
+          mbar_arrive_expect_tx(&ctl->q_full[s2], kBuf);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) tma_load_3d(smem + at.Q() + b * 16384, &mq, &ctl->q_full[s2], 64 * b, hk, t);
+          issued = 3 * n + 1;
+          if (n >= 2 && !wait(ctl->pv_done[s2], (n >> 1) - 1, DEVERR_MMA_TIMEOUT)) break;  // V of n - 2
+        }
+        mbar_arrive_expect_tx(&ctl->k_full[s2], kBuf);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) tma_load_3d(smem + at.K() + b * 16384, &mk, &ctl->k_full[s2], 64 * b, hk, t);
+        issued = 3 * n + 2;
+        if (!kStateOnly && n >= 1 && !wait(ctl->qs_done[s2 ^ 1], (n - 1) >> 1, DEVERR_MMA_TIMEOUT)) break;  // Q of n - 1
         mbar_arrive_expect_tx(&ctl->v_full[s2], F::kTileV);
 #pragma unroll
         for (int b = 0; b < kDV / 64; ++b)
-          tma_load_3d(smem + F::oV + s2 * F::kTileV + b * 16384, &mv, &ctl->v_full[s2], col0 + 64 * b, h, t);
-        issued = 3 * n + 1;
-        if constexpr (!kStateOnly) {
-          if (!wait(ctl->q_free[sq], (n / kNQ) ^ 1, DEVERR_MMA_TIMEOUT)) break;
-          mbar_arrive_expect_tx(&ctl->q_full[sq], kTileQK);
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            tma_load_3d(smem + F::oQ + sq * kTileQK + b * 16384, &mq, &ctl->q_full[sq], 64 * b, hk, t);
-        }
-        issued = 3 * n + 2;
-        if (!wait(ctl->k_free[s2], (n >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) break;
-        mbar_arrive_expect_tx(&ctl->k_full[s2], kTileQK);
-#pragma unroll
-        for (int b = 0; b < 2; ++b)
-          tma_load_3d(smem + F::oK + s2 * kTileQK + b * 16384, &mk, &ctl->k_full[s2], 64 * b, hk, t);
+          tma_load_3d(smem + at.V() + b * 16384, &mv, &ctl->v_full[s2], col0 + 64 * b, h, t);
         issued = 3 * n + 3;
         if (n + 1 < chunks) {
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            tma_prefetch_l2_3d(&mk, 64 * b, hk, t + kC);
             if constexpr (!kStateOnly) tma_prefetch_l2_3d(&mq, 64 * b, hk, t + kC);
+            tma_prefetch_l2_3d(&mk, 64 * b, hk, t + kC);
           }
 #pragma unroll
           for (int b = 0; b < kDV / 64; ++b) tma_prefetch_l2_3d(&mv, col0 + 64 * b, h, t + kC);
         }
       }
-      // every load issued has landed before the CTA may end: the last of each buffer
-      const int nv = (issued + 2) / 3, nq = (issued + 1) / 3, nk = issued / 3;
+      // every load issued has landed before the CTA may end: the last two of each tensor
+      const int nq = (issued + 2) / 3, nk = (issued + 1) / 3, nv = issued / 3;
 #pragma unroll 1
-      for (int n = nk > 2 ? nk - 2 : 0; n < nk; ++n)
-        mbar_wait(&ctl->k_full[n & 1], (n >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
-      if constexpr (!kStateOnly)
-#pragma unroll 1
-        for (int n = nq > kNQ ? nq - kNQ : 0; n < nq; ++n)
-          mbar_wait(&ctl->q_full[n % kNQ], (n / kNQ) & 1, err_word, DEVERR_TMA_TIMEOUT);
-#pragma unroll 1
-      for (int n = nv > 2 ? nv - 2 : 0; n < nv; ++n)
-        mbar_wait(&ctl->v_full[n & 1], (n >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
+      for (int i = 0; i < 2; ++i) {
+        if (!kStateOnly && nq > i) mbar_wait(&ctl->q_full[(nq - 1 - i) & 1], ((nq - 1 - i) >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
+        if (nk > i) mbar_wait(&ctl->k_full[(nk - 1 - i) & 1], ((nk - 1 - i) >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
+        if (nv > i) mbar_wait(&ctl->v_full[(nv - 1 - i) & 1], ((nv - 1 - i) >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
+      }
     }
   } else if (warp == 1) {
     // ---- Q K^T, Q S, P V
@@ -242,42 +266,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t base = smem_u32(smem);
       // Descriptors of the first buffers; an operand elsewhere is `bytes / 16` further (addresses
       // stay below 2^18, so the address field never carries).
-      const uint64_t dQ = desc_k(base + F::oQ), dK = desc_k(base + F::oK);
-      const uint64_t dV = desc_mn(base + F::oV, 16384), dS = desc_mn(base + F::oS, 16384);
+      const uint64_t dBuf = desc_k(base), dBufT = desc_mn(base, 16384), dS = desc_mn(base + F::oS, 16384);
+      Bufs<kStateOnly> at;
 #pragma unroll 1
-      for (int n = 0; n < chunks; ++n) {
-        const int sq = n % F::kNQ;
-        const uint32_t nk = uint32_t(n & 1) * (kTileQK >> 4), nq = uint32_t(sq) * (kTileQK >> 4),
-                       nv = uint32_t(n & 1) * (F::kTileV >> 4);
+      for (int n = 0; n < chunks; ++n, at.step()) {
+        const uint64_t dQ = dBuf + (at.Q() >> 4), dK = dBuf + (at.K() >> 4), dV = dBufT + (at.V() >> 4);
         if (!wait_warp(ctl->k_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
-        if (!wait_warp(ctl->q_full[sq], n / F::kNQ, DEVERR_TMA_TIMEOUT)) break;
+        if (!wait_warp(ctl->q_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
         // P of chunk n - 1 has been read out of the columns Q K^T goes to
-        if (n > 0 && !wait_warp(ctl->pv_done, n - 1, DEVERR_MMA_TIMEOUT)) break;
+        if (n > 0 && !wait_warp(ctl->pv_done[(n - 1) & 1], (n - 1) >> 1, DEVERR_MMA_TIMEOUT)) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           const uint32_t o = (ks >> 2) * 1024 + (ks & 3) * 2;
-          mma_ss(leader, tQK, dQ + (nq + o), dK + (nk + o), iQK, ks > 0);
+          mma_ss(leader, tQK, dQ + o, dK + o, iQK, ks > 0);
         }
         mma_commit(leader, ctl->qk_done);
         if (!wait_warp(ctl->s_full, n, DEVERR_MMA_TIMEOUT)) break;
-        if (n > 0 && !wait_warp(ctl->o_free, n - 1, DEVERR_MMA_TIMEOUT)) break;  // O of chunk n - 1 is read out
+        if (n > 0 && !wait_warp(ctl->o_read, n - 1, DEVERR_MMA_TIMEOUT)) break;  // O of chunk n - 1 is read out
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < (kPair ? 16 : 8); ++ks)
-          mma_ss(leader, tOX, dQ + (nq + ((ks & 7) >> 2) * 1024 + (ks & 3) * 2),
+          mma_ss(leader, tOX, dQ + (((ks & 7) >> 2) * 1024 + (ks & 3) * 2),
                  dS + ((ks >> 3) * (F::kTileS >> 4) + (ks & 7) * 128), iPV, ks > 0);
-        mma_commit(leader, ctl->qs_done);
-        mma_commit(leader, ctl->q_free[sq]);
+        mma_commit(leader, ctl->qs_done[n & 1]);
+        if (!wait_warp(ctl->v_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
         if (!wait_warp(ctl->p_full, n, DEVERR_MMA_TIMEOUT)) break;
         // the last chunk's rows behind the segment: V is zeroed there before K^T V' begins
-        if ((n + 1) * kC > len && !wait_warp(ctl->d_done, n, DEVERR_MMA_TIMEOUT)) break;
+        if ((n + 1) * kC > len && !wait_warp(ctl->d_done[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < (kPair ? 16 : 8); ++ks)
-          mma_ts(leader, tOI, (ks < 8 ? tQK : tPL) + 8 * (ks & 7), dV + (nv + (ks & 7) * 128), iPV, ks > 0);
-        mma_commit(leader, ctl->pv_done);
-        mma_commit(leader, ctl->v_free[n & 1]);
+          mma_ts(leader, tOI, (ks < 8 ? tQK : tPL) + 8 * (ks & 7), dV + (ks & 7) * 128, iPV, ks > 0);
+        mma_commit(leader, ctl->pv_done[n & 1]);
       }
       // no MMA is in flight when tensor memory is freed
       mma_commit(leader, ctl->drain);
@@ -288,11 +309,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t iD = umma_idesc_bf16(128, kDV, true, true, false);
     const bool leader = elect_lane();
     const uint32_t base = smem_u32(smem);
-    const uint64_t dKt = desc_mn(base + F::oK, 16384), dVP = desc_mn(base + F::oVP, 4096);
+    const uint64_t dBufT = desc_mn(base, 16384), dVP = desc_mn(base + F::oVP, 4096);
+    Bufs<kStateOnly> at;
     bool ok = true;
 #pragma unroll 1
-    for (int n = 0; ok && n < chunks; ++n) {
-      const uint32_t nk = uint32_t(n & 1) * (kTileQK >> 4);
+    for (int n = 0; ok && n < chunks; ++n, at.step()) {
       if (!wait_warp(ctl->k_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
       if (n > 0 && !wait_warp(ctl->d_free, n - 1, DEVERR_MMA_TIMEOUT)) break;
 #pragma unroll 1
@@ -301,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_warp(ctl->vp_full[u & 1], u >> 1, DEVERR_MMA_TIMEOUT);
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ak = dKt + (nk + q * 256), bv = dVP + uint32_t(u & 1) * (2 * F::kTileVP >> 4);
+        const uint64_t ak = dBufT + ((at.K() >> 4) + q * 256), bv = dVP + uint32_t(u & 1) * (2 * F::kTileVP >> 4);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)  // hi, lo
           mma_ss(leader, tD, ak + (ks & 1) * 128, bv + ((ks >> 1) * (F::kTileVP >> 4) + (ks & 1) * 128), iD,
@@ -309,8 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(leader, ctl->vp_free[u & 1]);
       }
       if (!ok) break;
-      mma_commit(leader, ctl->d_done);
-      if constexpr (kStateOnly) mma_commit(leader, ctl->k_free[n & 1]);
+      mma_commit(leader, ctl->d_done[n & 1]);
     }
     mma_commit(leader, ctl->drain);
     if (leader) mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
@@ -365,10 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t f1 = pack_bf16x2(f, 0.f) & 0xffffu;
         w.f[32 * b + lane] = f1 | (pack_bf16x2(f - bf16_to_f32(uint16_t(f1)), 0.f) << 16);
       }
-      if (lane == 0) {
-        w.t[0] = t[0], w.t[1] = t[1], w.t[2] = t[2];
-        w.e1 = expm1f(all * kLn2);
-      }
+      if (lane == 0) w.e1 = expm1f(all * kLn2);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->tab_full[n & 1]);
     }
@@ -413,8 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int J = 0; J < w; ++J) {  // blocks before the row's: row factor x column factor
           float e = ai;  // from the end of block J to the row
-          if (J + 1 < w) e += tb.t[J + 1];
-          if (J + 2 < w) e += tb.t[J + 2];
+          if (J + 1 < w) e += tb.block(J + 1);
+          if (J + 2 < w) e += tb.block(J + 2);
           e = ex2(e);
           float2 p[16];
           get(J, p);
@@ -457,28 +474,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 8 && warp < 12) {
     // ---- V': quarters of 32 tokens, two buffers
     const int wt = tid - 256;
-    // this thread's pieces of 8 columns: column piece j of tokens t0, t0 + step, ... of a quarter
+    // this thread's pieces: 8 columns (piece j) of tokens t0, t0 + step, ... of a quarter
     constexpr int step = 1024 / kDV;
     const int j = wt % (kDV / 8), t0 = wt / (kDV / 8);
     const uint32_t src_off = sw128_chunk(t0, j & 7, j >> 3, 128), dst_off = sw128_chunk(t0, j & 7, j >> 3, 32);
+    Bufs<kStateOnly> at;
     bool ok = true;
 #pragma unroll 1
-    for (int n = 0; ok && n < chunks; ++n) {
+    for (int n = 0; ok && n < chunks; ++n, at.step()) {
       const Table &tb = tab[n & 1];
       ok = wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT) &&
            wait_warp(ctl->v_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT);
+      if (!ok) break;
+      uint8_t *V = smem + at.V() + src_off;
       const int part = len - n * kC;
-      if (ok && part < kC) {
+      if (part < kC) {
         // rows from here on hold another sequence's tokens: zeros in V and K, since 0 times another
         // sequence's infinity would not vanish in the products
-        ok = wait_warp(ctl->k_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT);
-        uint8_t *K = smem + F::oK + (n & 1) * kTileQK;
+        if (!wait_warp(ctl->k_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
+        uint8_t *K = smem + at.K();
 #pragma unroll 1
-        for (int m = 0; ok && m < kC / step; ++m) {  // each thread its own pieces of V, and K's beside
+        for (int m = 0; m < kC / step; ++m) {  // each thread its own pieces of V, and K's beside
           const int tt = t0 + m * step;
           if (tt < part) continue;
           const uint4 zero = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4 *>(smem + F::oV + (n & 1) * F::kTileV + src_off + m * step * 128) = zero;
+          *reinterpret_cast<uint4 *>(V + m * step * 128) = zero;
           for (int b = 0; b < 128 / kDV; ++b)
             *reinterpret_cast<uint4 *>(K + sw128_chunk(tt, j & 7, kDV == 128 ? j >> 3 : b, 128)) = zero;
         }
@@ -486,10 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
 #pragma unroll 1
-      for (int q = 0; ok && q < 4; ++q) {
+      for (int q = 0; q < 4; ++q) {
         const int u = 4 * n + q;
-        uint8_t *src = smem + F::oV + (n & 1) * F::kTileV + q * 4096 + src_off;
-        uint8_t *dst = smem + F::oVP + (u & 1) * 2 * F::kTileVP + dst_off;
+        uint8_t *src = V + q * 4096, *dst = smem + F::oVP + (u & 1) * 2 * F::kTileVP + dst_off;
         ok = wait_warp(ctl->vp_free[u & 1], (u >> 1) ^ 1, DEVERR_MMA_TIMEOUT);
         if (!ok) break;
 #pragma unroll
@@ -513,10 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->vp_full[u & 1]);
       }
-      if (ok && lane == 0) {
-        mbar_arrive(&ctl->tab_free[n & 1]);
-        mbar_arrive(&ctl->v_free[n & 1]);
-      }
+      if (ok && lane == 0) mbar_arrive(&ctl->tab_free[n & 1]);
     }
   } else if (warp >= 12) {
     // ---- the state and the output
@@ -529,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
       const float *src = nullptr;
       if constexpr (!kStateOnly) {
-        if (a.plan.seg_len != 0) src = a.seg_states + (int64_t(slot) * a.H + h) * dd;
+        if (!s.first) src = a.seg_states + (int64_t(slot) * a.H + h) * dd;
         else if (a.init_state != nullptr) src = a.init_state + (int64_t(s.n) * a.H + h) * dd;
       }
 #pragma unroll
@@ -559,19 +575,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (kPair)
           *reinterpret_cast<uint4 *>(smem + F::oS + F::kTileS + o) = make_uint4(l[0], l[1], l[2], l[3]);
       }
-    };
-    if constexpr (!kStateOnly) {
-      write_state_tile();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->s_full);
-    }
+    };
+    if constexpr (!kStateOnly) write_state_tile();
+    // rows of the output that start on 32-byte boundaries take 32-byte stores
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | (uint32_t(a.d_v) * (kOutBF16 ? 2 : 4))) & 31) == 0;
 #pragma unroll 1
     for (int n = 0; n < chunks; ++n) {
-      if (!kStateOnly && tid == 384 && n > 0) {  // the copy of the tile before has read its buffer
-        bulk_wait_read();
-        mbar_arrive(&ctl->k_free[(n - 1) & 1]);
-      }
       const Table &tb = tab[n & 1];
       if (!wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
       const float e1 = tb.e1;
@@ -580,13 +592,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         eG = tb.a[r];
 #pragma unroll
         for (int B = 0; B < 3; ++B)
-          if (B < w) eG += tb.t[B];
+          if (B < w) eG += tb.block(B);
         eG = a.scale * ex2(eG);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->tab_free[n & 1]);
       // the state: S <- e^{G_C} S + K^T V'
-      if (!wait_warp(ctl->d_done, n, DEVERR_MMA_TIMEOUT)) break;
+      if (!wait_warp(ctl->d_done[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < kHalf; c += 16) {
@@ -603,69 +615,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->d_free);
       if constexpr (!kStateOnly) {
-        if (!wait_warp(ctl->qs_done, n, DEVERR_MMA_TIMEOUT)) break;
-        tc_fence_after();
         if (n + 1 < chunks) {
+          if (!wait_warp(ctl->qs_done[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
           write_state_tile();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->s_full);
         }
-        if (!wait_warp(ctl->pv_done, n, DEVERR_MMA_TIMEOUT)) break;
+        if (!wait_warp(ctl->pv_done[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
         tc_fence_after();
+        // the output: O = scale (P V + e^G Q S), token r in lane r
+        constexpr int kPer = kOutBF16 ? 16 : 8;  // columns of 32 bytes
+        constexpr int kEs = kOutBF16 ? 2 : 4;
         const int64_t t = s.t0 + int64_t(n) * kC + r;
-        const bool whole = (n + 1) * kC <= len;
-        uint8_t *stage = smem + F::oK + (n & 1) * kTileQK;
+        uint8_t *out = static_cast<uint8_t *>(a.out) + ((t * a.H + h) * a.d_v + col0 + cb) * kEs;
+        const int cols = t < s.t1 ? a.d_v - col0 - cb : 0;  // this row's columns from cb on
 #pragma unroll
-        for (int c = 0; c < kHalf; c += 8) {
-          float oi[8], ox[8];
-          tmem_ld8(tOI + row + cb + c, oi);
-          tmem_ld8(tOX + row + cb + c, ox);
-          tmem_ld_wait(oi, ox);
+        for (int c = 0; c < kHalf; c += kPer) {
+          uint32_t u[8];
 #pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float2 y = f2_fma(make_float2(eG, eG), make_float2(ox[e], ox[e + 1]),
-                                    f2_mul(make_float2(a.scale, a.scale), make_float2(oi[e], oi[e + 1])));
-            oi[e] = y.x, oi[e + 1] = y.y;
-          }
-          const int cc = cb + c, col = col0 + cc;
-          const bool direct = !whole && t < s.t1 && col < a.d_v;  // rows of a part of a tile
-          const int64_t at = (t * a.H + h) * a.d_v + col;
-          if constexpr (kOutBF16) {
-            const uint4 u = make_uint4(pack_bf16x2(oi[0], oi[1]), pack_bf16x2(oi[2], oi[3]), pack_bf16x2(oi[4], oi[5]),
-                                       pack_bf16x2(oi[6], oi[7]));
-            if (whole) *reinterpret_cast<uint4 *>(stage + sw128_chunk(r, (cc >> 3) & 7, cc >> 6, 128)) = u;
-            else if (direct) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.out) + at) = u;
-          } else {
+          for (int i = 0; i < kPer; i += 8) {
+            float oi[8], ox[8];
+            tmem_ld8(tOI + row + cb + c + i, oi);
+            tmem_ld8(tOX + row + cb + c + i, ox);
+            tmem_ld_wait(oi, ox);
 #pragma unroll
-            for (int f = 0; f < 8; f += 4) {
-              const float4 u = make_float4(oi[f], oi[f + 1], oi[f + 2], oi[f + 3]);
-              if (whole) *reinterpret_cast<float4 *>(stage + sw128_chunk(r, ((cc + f) >> 2) & 7, cc >> 5, 128)) = u;
-              else if (direct) *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at + f) = u;
+            for (int e = 0; e < 8; e += 2) {
+              const float2 y = f2_fma(make_float2(eG, eG), make_float2(ox[e], ox[e + 1]),
+                                      f2_mul(make_float2(a.scale, a.scale), make_float2(oi[e], oi[e + 1])));
+              if constexpr (kOutBF16) u[(i + e) >> 1] = pack_bf16x2(y.x, y.y);
+              else u[e] = __float_as_uint(y.x), u[e + 1] = __float_as_uint(y.y);
             }
           }
-        }
-        // a whole chunk's tile leaves by TMA from the chunk's K buffer, whose last MMA is done; the
-        // buffer is free again once the copy has read it
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->o_free);
-        if (warp == 12 && whole) {
-          if (!wait_warp(ctl->o_free, n, DEVERR_MMA_TIMEOUT)) break;
-          if (lane == 0) {
-            constexpr int kBox = kOutBF16 ? 64 : 32;
-#pragma unroll
-            for (int b = 0; b < kDV / kBox; ++b)
-              if (col0 + kBox * b < a.d_v)
-                tma_store_3d(&mo, smem + F::oK + (n & 1) * kTileQK + b * 16384, col0 + kBox * b, h,
-                             int32_t(s.t0) + n * kC);
-            bulk_commit();
+          if (wide && c < cols) {  // whole: cols is then a multiple of kPer
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + c * kEs), "r"(u[0]),
+                         "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                         : "memory");
+          } else {
+            if (c < cols) *reinterpret_cast<uint4 *>(out + c * kEs) = make_uint4(u[0], u[1], u[2], u[3]);
+            if (c + kPer / 2 < cols) *reinterpret_cast<uint4 *>(out + c * kEs + 16) = make_uint4(u[4], u[5], u[6], u[7]);
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->o_read);
       }
     }
-    if (!kStateOnly && tid == 384) bulk_wait_all();
     float *dst = kStateOnly ? a.seg_states + (int64_t(slot) * a.H + h) * dd
                  : (s.last && a.final_state != nullptr) ? a.final_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
     if (dst != nullptr && r < a.d_k) {
@@ -687,16 +679,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int kDV, bool kOutBF16, bool kStateOnly>
-cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const CUtensorMap &mo,
-                       const LinearArgs &a, cudaStream_t stream) {
+cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const LinearArgs &a,
+                       cudaStream_t stream) {
   using F = Cfg<kDV, kOutBF16, kStateOnly>;
-  constexpr uint32_t smem = F::oTab + 2 * sizeof(Table) + sizeof(Control<F::kNQ == 0 ? 1 : F::kNQ>);
+  constexpr uint32_t smem = F::oTab + 2 * sizeof(Table) + sizeof(Control);
   static_assert(smem <= 232448, "shared memory of one CTA");
   const auto kern = linear_chunked_kernel<kDV, kOutBF16, kStateOnly>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  // the kernel's shared memory, granted once per device (bit d for device d; past 63 at every launch)
+  static std::atomic<uint64_t> granted;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (bit == 0 || (granted.load(std::memory_order_acquire) & bit) == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    granted.fetch_or(bit, std::memory_order_release);
+  }
   const dim3 grid(unsigned(a.plan.slots) * unsigned(a.H), unsigned((a.d_v + kDV - 1) / kDV));
-  kern<<<grid, kThreads, smem, stream>>>(mq, mk, mv, mo, a, device_error_word());
+  kern<<<grid, kThreads, smem, stream>>>(mq, mk, mv, a, device_error_word());
   return cudaGetLastError();
 }
 
@@ -705,22 +706,21 @@ cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
 bool linear_chunked_supported(int d_k, int d_v, bool in_bf16) { return in_bf16 && d_k % 8 == 0 && d_v % 8 == 0; }
 
 cudaError_t launch_linear_chunked(const LinearArgs &a, bool out_bf16, cudaStream_t stream) {
-  CUtensorMap mq, mk, mv, mo;
+  CUtensorMap mq, mk, mv;
   if (!tensor_map_3d(&mq, a.q, true, a.total, a.H_k, a.d_k, 64, kC, true) ||
       !tensor_map_3d(&mk, a.k, true, a.total, a.H_k, a.d_k, 64, kC, true) ||
-      !tensor_map_3d(&mv, a.v, true, a.total, a.H, a.d_v, 64, kC, true) ||
-      !tensor_map_3d(&mo, a.out, out_bf16, a.total, a.H, a.d_v, out_bf16 ? 64 : 32, kC, true))
+      !tensor_map_3d(&mv, a.v, true, a.total, a.H, a.d_v, 64, kC, true))
     return cudaErrorInvalidValue;
   const bool wide = a.plan.col_tile == 128;
   if (a.plan.seg_len != 0) {
-    cudaError_t e = wide ? launch_one<128, true, true>(mq, mk, mv, mo, a, stream)
-                         : launch_one<64, true, true>(mq, mk, mv, mo, a, stream);
+    cudaError_t e = wide ? launch_one<128, true, true>(mq, mk, mv, a, stream)
+                         : launch_one<64, true, true>(mq, mk, mv, a, stream);
     if (e == cudaSuccess) e = launch_linear_scan(a, stream);
     if (e != cudaSuccess) return e;
   }
-  if (wide) return launch_one<128, true, false>(mq, mk, mv, mo, a, stream);
-  return out_bf16 ? launch_one<64, true, false>(mq, mk, mv, mo, a, stream)
-                  : launch_one<64, false, false>(mq, mk, mv, mo, a, stream);
+  if (wide) return launch_one<128, true, false>(mq, mk, mv, a, stream);
+  return out_bf16 ? launch_one<64, true, false>(mq, mk, mv, a, stream)
+                  : launch_one<64, false, false>(mq, mk, mv, a, stream);
 }
 
 }  // namespace kda

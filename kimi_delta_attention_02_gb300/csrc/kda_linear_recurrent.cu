@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
   const int64_t dd = int64_t(a.d_k) * a.d_v;
   const float *S0 = nullptr;
   if constexpr (!kStateOnly) {
-    if (a.plan.seg_len != 0) S0 = a.seg_states + (int64_t(slot) * a.H + h) * dd;
+    if (!s.first) S0 = a.seg_states + (int64_t(slot) * a.H + h) * dd;
     else if (a.init_state != nullptr) S0 = a.init_state + (int64_t(s.n) * a.H + h) * dd;
   }
 #pragma unroll
@@ -163,32 +163,42 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
   if (kStateOnly && tid == 0 && blockIdx.y == 0) a.seg_decay[int64_t(slot) * a.H + h] = float(decay_sum);
 }
 
-// Pass 2: the segments' end states in the workspace become their entering states,
-// E_0 = initial state, E_{j+1} = e^{D_j} E_j + B_j. One thread per state entry walks its
-// sequence's segments; the next two segments' entries are on their way meanwhile.
+// Pass 2: a segment's end state from zero, B_j, gives way to its successor's entering state in the
+// successor's slot, E_0 = initial state (read where it is), E_{j+1} = e^{D_j} E_j + B_j. One thread
+// per state entry walks its sequence's segments, the next ones' entries on their way meanwhile;
+// sequences of one segment have nothing to do.
 __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a) {
-  const int64_t dd = int64_t(a.d_k) * a.d_v;
-  const int64_t e = int64_t(blockIdx.y) * blockDim.x + threadIdx.x;
   const int h = blockIdx.x % a.H, n = blockIdx.x / a.H;
-  if (e >= dd) return;
   const int L = a.plan.seg_len;
   const int bos = a.cu[n], eos = a.cu[n + 1];
   const int segs = eos > bos ? (eos - bos + L - 1) / L : 1;
-  const int64_t slot = bos / L + n;
+  const int64_t dd = int64_t(a.d_k) * a.d_v;
+  const int64_t e = int64_t(blockIdx.y) * blockDim.x + threadIdx.x;
+  if (segs == 1 || e >= dd) return;
+  const int64_t slot = bos / L + n, step = int64_t(a.H) * dd;
   float *p = a.seg_states + (slot * a.H + h) * dd + e;
   const float *d = a.seg_decay + slot * a.H + h;
-  const int64_t step = int64_t(a.H) * dd;
   float S = a.init_state != nullptr ? a.init_state[(int64_t(n) * a.H + h) * dd + e] : 0.f;
-  float b0 = segs > 1 ? p[0] : 0.f, b1 = segs > 2 ? p[step] : 0.f;
-  float d0 = segs > 1 ? d[0] : 0.f, d1 = segs > 2 ? d[a.H] : 0.f;
-  for (int j = 0; j < segs; ++j) {
-    const float bn = j + 3 < segs ? p[2 * step] : 0.f;
-    const float dn = j + 3 < segs ? d[2 * a.H] : 0.f;
-    p[0] = S;
-    S = decay_step(S, expm1f(d0)) + b0;
-    b0 = b1, b1 = bn, d0 = d1, d1 = dn;
-    p += step;
-    d += a.H;
+  constexpr int kAhead = 4;
+  float b[kAhead], D[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    b[i] = i + 1 < segs ? p[i * step] : 0.f;
+    D[i] = i + 1 < segs ? d[i * a.H] : 0.f;
+  }
+  for (int j0 = 0; j0 + 1 < segs; j0 += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i;
+      if (j + 1 >= segs) break;
+      S = decay_step(S, expm1f(D[i])) + b[i];
+      if (j + kAhead + 1 < segs) {
+        b[i] = p[(j + kAhead) * step];
+        D[i] = d[(j + kAhead) * a.H];
+      }
+      // B_{j+1} of this slot, if there is one, was read above (kAhead >= 2)
+      p[(j + 1) * step] = S;
+    }
   }
 }
 
