@@ -17,7 +17,7 @@ struct BlockNormArgs {
   int gate_form;  // 0 none, 1 per channel, 2 per row
   int post_norm;
   float scale, post_eps, pre_eps;
-  int threads_per_row;  // set by the launcher
+  int threads_per_row, stages;  // set by the launcher
 };
 
 cudaError_t launch_block_norm(BlockNormArgs a, bool x_bf16, bool y_bf16, bool out_bf16, cudaStream_t stream);
