@@ -499,8 +499,7 @@ kda_status kda_linear_prefill(const kda_linear_prefill_params *p, void *stream) 
   const bool in_bf16 = p->in_dtype == KDA_BF16, out_bf16 = p->out_dtype == KDA_BF16;
   a.plan = linear_plan(T, p->num_seqs, p->H, p->d_k, p->d_v, in_bf16, out_bf16, p->force_recurrent != 0);
   if (p->workspace_bytes < a.plan.bytes) {  // every sequence from end to end
-    a.plan.seg_len = 0;
-    a.plan.slots = p->num_seqs;
+    a.plan.seg_len = a.plan.inner = 0;
   } else if (a.plan.bytes != 0) {
     a.seg_states = static_cast<float *>(p->workspace);
     a.seg_decay = reinterpret_cast<float *>(static_cast<uint8_t *>(p->workspace) + a.plan.state_bytes);

@@ -12,55 +12,64 @@
 
 namespace kda {
 
-// Where a call's work is cut. seg_len = 0: every (sequence, head) is one piece and slot n is
-// sequence n. Otherwise sequence n owns the slots cu[n] / L + n .. cu[n + 1] / L + n (L =
-// seg_len): the first ceil(len / L) of them hold its segments (an empty sequence holds one empty
-// segment), the others are idle. A slot is found from cu_seqlens alone, so the host needs no
-// lengths and the grid is total / L + num_seqs slots.
+// Where a call's work is cut. seg_len = 0: every (sequence, head) is one piece. Otherwise sequences
+// are cut every L = seg_len tokens from their start, and sequence n keeps its segment j at place
+// cu[n] / L + n + j of the workspace (total / L + num_seqs places are enough). Every segment but a
+// sequence's last is found from a multiple of L: i L (i = 1 .. total / L) lies in exactly one such
+// segment, behind its first token and at most at its end. So the host needs no lengths: total / L
+// pieces for those, of which some stay idle, and one piece per sequence for the last segments.
 struct LinearPlan {
   int32_t seg_len = 0;
-  int32_t slots = 0;
+  int32_t inner = 0;        // total / L
   int32_t col_tile = 0;     // value columns per CTA
   bool tensor = false;      // tensor-core kernel (bf16), else the token-recurrent one
-  size_t state_bytes = 0;   // workspace: [slots, H, d_k, d_v] fp32 entering states, then
-  size_t bytes = 0;         // [slots, H] fp32 summed log-decays
+  size_t state_bytes = 0;   // workspace: [places, H, d_k, d_v] fp32 entering states, then
+  size_t bytes = 0;         // [places, H] fp32 summed log-decays
 };
 
 struct LinearSlot {
   int n;              // sequence
+  int64_t place;      // in the workspace
   int64_t t0, t1;     // its tokens [t0, t1)
   bool first, last;   // of its sequence
 };
 
-// False for an idle slot. Called by whole warps.
-__device__ __forceinline__ bool linear_slot(const int32_t *__restrict__ cu, int num_seqs, int seg_len, int slot,
+// Piece `index`: the pieces for segments with a successor come first (they are the longest). False
+// for an idle piece. Called by whole warps.
+__device__ __forceinline__ bool linear_slot(const int32_t *__restrict__ cu, int num_seqs, int L, int inner, int index,
                                             LinearSlot &s) {
-  if (seg_len == 0) {
-    s.n = slot;
-    s.t0 = cu[slot];
-    s.t1 = cu[slot + 1];
-    s.first = s.last = true;
+  if (index >= inner) {
+    s.n = index - inner;
+    const int64_t bos = cu[s.n], eos = cu[s.n + 1];
+    const int j = L == 0 || eos == bos ? 0 : int((eos - bos - 1) / L);
+    s.place = L == 0 ? 0 : bos / L + s.n + j;
+    s.t0 = bos + int64_t(j) * L;
+    s.t1 = eos;
+    s.first = j == 0;
+    s.last = true;
     return true;
   }
-  // The last n whose first slot cu[n] / L + n is <= slot: a warp tries 32 candidates at a time (two
+  // The last n that starts before (index + 1) L: a warp tries 32 candidates at a time (two
   // dependent reads for up to 1024 sequences, where halving takes ten). All lanes take part.
+  const int64_t mark = int64_t(index + 1) * L;
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = num_seqs - 1;
   while (lo < hi) {
     const int stride = (hi - lo + 32) / 32, n = lo + lane * stride;
-    const bool fits = n <= hi && cu[n] / seg_len + n <= slot;  // true for lane 0, then false from some lane on
-    const int last = 31 - __clz(__ballot_sync(0xffffffffu, fits));
+    const bool before = n <= hi && cu[n] < mark;  // true for lane 0, then false from some lane on
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, before));
     lo += last * stride;
     hi = stride == 1 ? lo : (lo + stride - 1 < hi ? lo + stride - 1 : hi);
   }
   const int64_t bos = cu[lo], eos = cu[lo + 1];
-  const int j = slot - (int(bos) / seg_len + lo);
+  const int j = index - int(bos / L);
   s.n = lo;
-  s.t0 = bos + int64_t(j) * seg_len;
-  s.t1 = s.t0 + seg_len < eos ? s.t0 + seg_len : eos;
+  s.place = bos / L + lo + j;
+  s.t0 = bos + int64_t(j) * L;
+  s.t1 = s.t0 + L;
   s.first = j == 0;
-  s.last = s.t0 + seg_len >= eos;
-  return s.first || s.t0 < eos;
+  s.last = false;
+  return s.t1 < eos;
 }
 
 // One decay step of a state entry: e^g s, as s + (e^g - 1) s. e^g itself, rounded to fp32, would

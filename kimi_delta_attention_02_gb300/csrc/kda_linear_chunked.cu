@@ -19,11 +19,15 @@
 // take an exponential per entry. A decay below 2^-127 per token counts as 2^-127, which leaves
 // nothing in fp32 either, so g = -infinity needs no case of its own.
 //
-// Shared memory holds five 32 KB buffers that the chunks' tiles take in turn, Q K V Q K V ..., so that
-// a tile waits for the one five places before it: Q of chunk n for K of n - 2, K for V of n - 2, V for
-// Q of n - 1. Every one of these is done with well before its successor is needed. The output needs
+// Shared memory holds five 32 KB buffers that the chunks' tiles take in turn, Q V K Q V K ..., so that
+// a tile waits for the one five places before it: Q of chunk n for V of n - 2, V for K of n - 2, K for
+// Q of n - 1. The output needs
 // no buffer: it goes from tensor memory through registers to global memory, 32 bytes (a whole
 // sector) per thread and store.
+//
+// Pass 1 of a segmented call (kStateOnly) forms a segment's end state from zero, sum over its chunks of
+// e^(decay behind the chunk) K^T V', last chunk first: once that factor is below 2^-127, and so zero in
+// fp32, no earlier token leaves anything and the rest of the segment is not read.
 //
 // Warps (20): 0 loads (TMA), 1 issues the MMAs Q K^T, Q S, P V, 2 makes the decay tables, 3 issues
 // K^T V' (on its own, so that either's waits are filled by the other's work), 4-7 form P (one
@@ -66,8 +70,8 @@ struct Bufs {
     return (b >= kBufs ? b - kBufs : b) * kBuf;
   }
   __device__ __forceinline__ uint32_t Q() const { return at(0); }
-  __device__ __forceinline__ uint32_t K() const { return at(kStateOnly ? 0 : 1); }
-  __device__ __forceinline__ uint32_t V() const { return at(kStateOnly ? 1 : 2); }
+  __device__ __forceinline__ uint32_t K() const { return at(kStateOnly ? 0 : 2); }
+  __device__ __forceinline__ uint32_t V() const { return at(1); }
   __device__ __forceinline__ void step() {
     first += kStateOnly ? 2 : 3;
     if (first >= kBufs) first -= kBufs;
@@ -78,8 +82,9 @@ struct Table {  // decays of one chunk, log2 units unless said otherwise
   float a[kC];       // from the block's start to the token, itself included
   float es[96];      // 2^(from behind the token to the block's end), blocks 0 .. 2
   uint32_t f[kC];    // e^{G_C - G_j} as a pair: the nearest bf16 (low half), what is left
-  float e1;          // e^{G_C} - 1
-  float pad[3];
+  float e1;          // e^{G_C} - 1; in pass 1 e^(everything behind the chunk)
+  uint32_t stop;     // pass 1: no chunk before this one leaves anything
+  float pad[2];
   __device__ __forceinline__ float block(int B) const { return a[32 * B + 31]; }
 };
 static_assert(sizeof(Table) % 16 == 0, "128-bit reads of the second table");
@@ -161,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Table *tab = reinterpret_cast<Table *>(smem + F::oTab);
   Control *ctl = reinterpret_cast<Control *>(smem + F::oTab + 2 * sizeof(Table));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H, hk = h / (a.H / a.H_k);
+  const int h = blockIdx.x % a.H, hk = h / (a.H / a.H_k);
   const int col0 = blockIdx.y * kDV;
 
   if (tid == 0) {
@@ -170,8 +175,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&mv);
   }
   LinearSlot s;
-  if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, slot, s)) return;
-  if (kStateOnly && s.last) return;
+  if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, blockIdx.x / a.H, s)) return;
   const int len = int(s.t1 - s.t0), chunks = (len + kC - 1) / kC;
 
   if (tid == 0) {
@@ -179,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->q_full[i], 1), mbar_init(&ctl->k_full[i], 1), mbar_init(&ctl->v_full[i], 1);
       mbar_init(&ctl->qs_done[i], 1), mbar_init(&ctl->d_done[i], 1), mbar_init(&ctl->pv_done[i], 1);
       mbar_init(&ctl->vp_full[i], 4), mbar_init(&ctl->vp_free[i], 1);
-      mbar_init(&ctl->tab_full[i], 1), mbar_init(&ctl->tab_free[i], kStateOnly ? 12 : 16);
+      mbar_init(&ctl->tab_full[i], 1), mbar_init(&ctl->tab_free[i], kStateOnly ? 14 : 16);
     }
     mbar_init(&ctl->qk_done, 1), mbar_init(&ctl->p_full, 4), mbar_init(&ctl->d_free, 8);
     mbar_init(&ctl->s_full, 8), mbar_init(&ctl->o_read, 8), mbar_init(&ctl->drain, kStateOnly ? 1 : 2);
@@ -218,38 +222,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       int issued = 0;
 #pragma unroll 1
       for (int n = 0; n < chunks; ++n, at.step()) {
-        const int32_t t = int32_t(s.t0) + n * kC;
+        const int32_t t = int32_t(s.t0) + (kStateOnly ? chunks - 1 - n : n) * kC;
         const int s2 = n & 1;
-        if (n >= 2 && !wait(ctl->d_done[s2], (n >> 1) - 1, DEVERR_MMA_TIMEOUT)) break;  // K (and V', so V) of n - 2
-        if constexpr (!kStateOnly) {
-          mbar_arrive_expect_tx(&ctl->q_full[s2], kBuf);
-#pragma unroll
-          for (int b = 0; b < 2; ++b) tma_load_3d(smem + at.Q() + b * 16384, &mq, &ctl->q_full[s2], 64 * b, hk, t);
-          issued = 3 * n + 1;
-          if (n >= 2 && !wait(ctl->pv_done[s2], (n >> 1) - 1, DEVERR_MMA_TIMEOUT)) break;  // V of n - 2
+        if (kStateOnly && n > 0) {
+          if (!wait(ctl->tab_full[s2 ^ 1], (n - 1) >> 1, DEVERR_MMA_TIMEOUT)) break;
+          const bool stop = tab[s2 ^ 1].stop != 0;
+          mbar_arrive(&ctl->tab_free[s2 ^ 1]);
+          if (stop) break;
         }
-        mbar_arrive_expect_tx(&ctl->k_full[s2], kBuf);
-#pragma unroll
-        for (int b = 0; b < 2; ++b) tma_load_3d(smem + at.K() + b * 16384, &mk, &ctl->k_full[s2], 64 * b, hk, t);
-        issued = 3 * n + 2;
-        if (!kStateOnly && n >= 1 && !wait(ctl->qs_done[s2 ^ 1], (n - 1) >> 1, DEVERR_MMA_TIMEOUT)) break;  // Q of n - 1
+        if (n >= 2) {  // everything with chunk n - 2's K and V is done
+          if (!wait(ctl->d_done[s2], (n >> 1) - 1, DEVERR_MMA_TIMEOUT)) break;
+          if (!kStateOnly && !wait(ctl->pv_done[s2], (n >> 1) - 1, DEVERR_MMA_TIMEOUT)) break;
+        }
         mbar_arrive_expect_tx(&ctl->v_full[s2], F::kTileV);
 #pragma unroll
         for (int b = 0; b < kDV / 64; ++b)
           tma_load_3d(smem + at.V() + b * 16384, &mv, &ctl->v_full[s2], col0 + 64 * b, h, t);
+        issued = 3 * n + 1;
+        if constexpr (!kStateOnly) {
+          mbar_arrive_expect_tx(&ctl->q_full[s2], kBuf);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) tma_load_3d(smem + at.Q() + b * 16384, &mq, &ctl->q_full[s2], 64 * b, hk, t);
+          issued = 3 * n + 2;
+          if (n >= 1 && !wait(ctl->qs_done[s2 ^ 1], (n - 1) >> 1, DEVERR_MMA_TIMEOUT)) break;
+        }
+        mbar_arrive_expect_tx(&ctl->k_full[s2], kBuf);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) tma_load_3d(smem + at.K() + b * 16384, &mk, &ctl->k_full[s2], 64 * b, hk, t);
         issued = 3 * n + 3;
         if (n + 1 < chunks) {
+          const int32_t next = kStateOnly ? t - kC : t + kC;
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            if constexpr (!kStateOnly) tma_prefetch_l2_3d(&mq, 64 * b, hk, t + kC);
-            tma_prefetch_l2_3d(&mk, 64 * b, hk, t + kC);
+            if constexpr (!kStateOnly) tma_prefetch_l2_3d(&mq, 64 * b, hk, next);
+            tma_prefetch_l2_3d(&mk, 64 * b, hk, next);
           }
 #pragma unroll
-          for (int b = 0; b < kDV / 64; ++b) tma_prefetch_l2_3d(&mv, col0 + 64 * b, h, t + kC);
+          for (int b = 0; b < kDV / 64; ++b) tma_prefetch_l2_3d(&mv, col0 + 64 * b, h, next);
         }
       }
       // every load issued has landed before the CTA may end: the last two of each tensor
-      const int nq = (issued + 2) / 3, nk = (issued + 1) / 3, nv = issued / 3;
+      const int nv = (issued + 2) / 3, nq = (issued + 1) / 3, nk = issued / 3;
 #pragma unroll 1
       for (int i = 0; i < 2; ++i) {
         if (!kStateOnly && nq > i) mbar_wait(&ctl->q_full[(nq - 1 - i) & 1], ((nq - 1 - i) >> 1) & 1, err_word, DEVERR_TMA_TIMEOUT);
@@ -331,6 +344,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       mma_commit(leader, ctl->d_done[n & 1]);
+      if constexpr (kStateOnly) {
+        if (!wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
+        const bool stop = tab[n & 1].stop != 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->tab_free[n & 1]);
+        if (stop) break;
+      }
     }
     mma_commit(leader, ctl->drain);
     if (leader) mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
@@ -343,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto fetch = [&](int n) {
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const int i = n * kC + 32 * b + lane;
+        const int i = (kStateOnly ? chunks - 1 - n : n) * kC + 32 * b + lane;
         g[b] = i < len ? (per_token ? a.log_decay[(s.t0 + i) * a.H + h] : constant) : 0.f;
       }
     };
@@ -372,6 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int b = 0; b < 4; ++b) t[b] = __shfl_sync(0xffffffffu, p[b], 31);
       const float all = (t[0] + t[1]) + (t[2] + t[3]);
+      const float before = kStateOnly ? ex2(float(total)) : 0.f;  // of what lies behind the chunk
       total += double(all);
       Table &w = tab[n & 1];
       if (!wait_warp(ctl->tab_free[n & 1], (n >> 1) ^ 1, DEVERR_MMA_TIMEOUT)) break;
@@ -385,12 +406,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t f1 = pack_bf16x2(f, 0.f) & 0xffffu;
         w.f[32 * b + lane] = f1 | (pack_bf16x2(f - bf16_to_f32(uint16_t(f1)), 0.f) << 16);
       }
-      if (lane == 0) w.e1 = expm1f(all * kLn2);
+      const bool stop = kStateOnly && total <= double(kMinLog2);  // a NaN goes on
+      if (lane == 0) {
+        w.e1 = kStateOnly ? before : expm1f(all * kLn2);
+        w.stop = stop;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->tab_full[n & 1]);
+      if (stop) break;
     }
     if (kStateOnly && lane == 0 && blockIdx.y == 0)
-      a.seg_decay[int64_t(slot) * a.H + h] = float(total * 0.6931471805599453);
+      a.seg_decay[s.place * a.H + h] = float(total * 0.6931471805599453);
   } else if (warp >= 4 && warp < 8) {
     // ---- P: row i of Q K^T in lane i; the decays, then bf16 in place
     if constexpr (!kStateOnly) {
@@ -532,7 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->vp_full[u & 1]);
       }
+      const bool stop = kStateOnly && tb.stop != 0;
+      __syncwarp();
       if (ok && lane == 0) mbar_arrive(&ctl->tab_free[n & 1]);
+      if (stop) break;
     }
   } else if (warp >= 12) {
     // ---- the state and the output
@@ -545,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
       const float *src = nullptr;
       if constexpr (!kStateOnly) {
-        if (!s.first) src = a.seg_states + (int64_t(slot) * a.H + h) * dd;
+        if (!s.first) src = a.seg_states + (s.place * a.H + h) * dd;
         else if (a.init_state != nullptr) src = a.init_state + (int64_t(s.n) * a.H + h) * dd;
       }
 #pragma unroll
@@ -587,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Table &tb = tab[n & 1];
       if (!wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
       const float e1 = tb.e1;
+      const bool stop = kStateOnly && tb.stop != 0;
       float eG = 0.f;  // e^{G_r}, the decay of the entering state at token r
       if constexpr (!kStateOnly) {
         eG = tb.a[r];
@@ -597,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->tab_free[n & 1]);
-      // the state: S <- e^{G_C} S + K^T V'
+      // the state: S <- e^{G_C} S + K^T V' (in pass 1, S <- S + e^(behind) K^T V')
       if (!wait_warp(ctl->d_done[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
       tc_fence_after();
 #pragma unroll
@@ -606,14 +636,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld16_wait(tD + row + cb + c, d);
 #pragma unroll
         for (int e = 0; e < 16; e += 2) {
-          const float2 x = make_float2(S[c + e], S[c + e + 1]);
-          const float2 y = f2_add(f2_fma(make_float2(e1, e1), x, x), make_float2(d[e], d[e + 1]));
+          const float2 x = make_float2(S[c + e], S[c + e + 1]), dd2 = make_float2(d[e], d[e + 1]);
+          const float2 y = kStateOnly ? f2_fma(make_float2(e1, e1), dd2, x)
+                                      : f2_add(f2_fma(make_float2(e1, e1), x, x), dd2);
           S[c + e] = y.x, S[c + e + 1] = y.y;
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->d_free);
+      if (stop) break;
       if constexpr (!kStateOnly) {
         if (n + 1 < chunks) {
           if (!wait_warp(ctl->qs_done[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
@@ -658,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&ctl->o_read);
       }
     }
-    float *dst = kStateOnly ? a.seg_states + (int64_t(slot) * a.H + h) * dd
+    float *dst = kStateOnly ? a.seg_states + (s.place * a.H + h) * dd
                  : (s.last && a.final_state != nullptr) ? a.final_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
     if (dst != nullptr && r < a.d_k) {
 #pragma unroll
@@ -696,7 +728,8 @@ cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
     if (e != cudaSuccess) return e;
     granted.fetch_or(bit, std::memory_order_release);
   }
-  const dim3 grid(unsigned(a.plan.slots) * unsigned(a.H), unsigned((a.d_v + kDV - 1) / kDV));
+  const unsigned pieces = unsigned(a.plan.inner) + (kStateOnly ? 0u : unsigned(a.num_seqs));
+  const dim3 grid(pieces * unsigned(a.H), unsigned((a.d_v + kDV - 1) / kDV));
   kern<<<grid, kThreads, smem, stream>>>(mq, mk, mv, a, device_error_word());
   return cudaGetLastError();
 }

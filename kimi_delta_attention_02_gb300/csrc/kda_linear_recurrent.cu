@@ -27,11 +27,10 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
   __shared__ float s_e[2][kTok], s_g[2][kTok];  // e^g - 1; g (pass 1)
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int rg = lane & 3, pair = lane >> 2;
-  const int h = blockIdx.x % a.H, slot = blockIdx.x / a.H;
+  const int h = blockIdx.x % a.H;
   const int col0 = blockIdx.y * kCols;
   LinearSlot s;
-  if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, slot, s)) return;
-  if (kStateOnly && s.last) return;
+  if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, blockIdx.x / a.H, s)) return;
   const int hk = h / (a.H / a.H_k);
   const int col = col0 + 16 * w + 2 * pair;  // this thread's columns: col, col + 1
   const bool ok0 = col < a.d_v, ok1 = col + 1 < a.d_v;
@@ -42,7 +41,7 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
   const int64_t dd = int64_t(a.d_k) * a.d_v;
   const float *S0 = nullptr;
   if constexpr (!kStateOnly) {
-    if (!s.first) S0 = a.seg_states + (int64_t(slot) * a.H + h) * dd;
+    if (!s.first) S0 = a.seg_states + (s.place * a.H + h) * dd;
     else if (a.init_state != nullptr) S0 = a.init_state + (int64_t(s.n) * a.H + h) * dd;
   }
 #pragma unroll
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
     if (more) stage(b ^ 1);
   }
 
-  float *dst = kStateOnly ? a.seg_states + (int64_t(slot) * a.H + h) * dd
+  float *dst = kStateOnly ? a.seg_states + (s.place * a.H + h) * dd
                : (s.last && a.final_state != nullptr) ? a.final_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
   if (dst != nullptr) {
 #pragma unroll
@@ -160,51 +159,56 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
       }
     }
   }
-  if (kStateOnly && tid == 0 && blockIdx.y == 0) a.seg_decay[int64_t(slot) * a.H + h] = float(decay_sum);
+  if (kStateOnly && tid == 0 && blockIdx.y == 0) a.seg_decay[s.place * a.H + h] = float(decay_sum);
 }
 
 // Pass 2: a segment's end state from zero, B_j, gives way to its successor's entering state in the
-// successor's slot, E_0 = initial state (read where it is), E_{j+1} = e^{D_j} E_j + B_j. One thread
-// per state entry walks its sequence's segments, the next ones' entries on their way meanwhile;
-// sequences of one segment have nothing to do.
+// successor's place, E_0 = initial state (read where it is), E_{j+1} = e^{D_j} E_j + B_j. The CTAs of
+// a sequence's first segment walk its segments, kVec entries per thread, the next segments' entries on
+// their way meanwhile.
+template <int kVec>
 __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a) {
-  const int h = blockIdx.x % a.H, n = blockIdx.x / a.H;
-  const int L = a.plan.seg_len;
-  const int bos = a.cu[n], eos = a.cu[n + 1];
-  const int segs = eos > bos ? (eos - bos + L - 1) / L : 1;
+  const int h = blockIdx.x % a.H;
+  LinearSlot s;
+  if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, blockIdx.x / a.H, s) || !s.first) return;
+  const int segs = (a.cu[s.n + 1] - a.cu[s.n] + a.plan.seg_len - 1) / a.plan.seg_len;
   const int64_t dd = int64_t(a.d_k) * a.d_v;
-  const int64_t e = int64_t(blockIdx.y) * blockDim.x + threadIdx.x;
-  if (segs == 1 || e >= dd) return;
-  const int64_t slot = bos / L + n, step = int64_t(a.H) * dd;
-  float *p = a.seg_states + (slot * a.H + h) * dd + e;
-  const float *d = a.seg_decay + slot * a.H + h;
-  float S = a.init_state != nullptr ? a.init_state[(int64_t(n) * a.H + h) * dd + e] : 0.f;
+  const int64_t e = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * kVec;
+  if (e >= dd) return;
+  struct alignas(4 * kVec) Vec {
+    float v[kVec];
+  };
+  const int64_t step = int64_t(a.H) * dd;
+  float *p = a.seg_states + (s.place * a.H + h) * dd + e;
+  const float *d = a.seg_decay + s.place * a.H + h;
+  auto read = [&](int j) { return *reinterpret_cast<const Vec *>(p + j * step); };
+  Vec S = {};
+  if (a.init_state != nullptr) S = *reinterpret_cast<const Vec *>(a.init_state + (int64_t(s.n) * a.H + h) * dd + e);
   constexpr int kAhead = 4;
-  float b[kAhead], D[kAhead];
+  Vec b[kAhead] = {};
+  float D[kAhead] = {};
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) {
-    b[i] = i + 1 < segs ? p[i * step] : 0.f;
-    D[i] = i + 1 < segs ? d[i * a.H] : 0.f;
-  }
+  for (int i = 0; i < kAhead; ++i)
+    if (i + 1 < segs) b[i] = read(i), D[i] = d[i * a.H];
   for (int j0 = 0; j0 + 1 < segs; j0 += kAhead) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int j = j0 + i;
       if (j + 1 >= segs) break;
-      S = decay_step(S, expm1f(D[i])) + b[i];
-      if (j + kAhead + 1 < segs) {
-        b[i] = p[(j + kAhead) * step];
-        D[i] = d[(j + kAhead) * a.H];
-      }
-      // B_{j+1} of this slot, if there is one, was read above (kAhead >= 2)
-      p[(j + 1) * step] = S;
+      const float em1 = expm1f(D[i]);
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) S.v[v] = decay_step(S.v[v], em1) + b[i].v[v];
+      if (j + kAhead + 1 < segs) b[i] = read(j + kAhead), D[i] = d[(j + kAhead) * a.H];
+      // B_{j+1} of this place, if there is one, was read above (kAhead >= 2)
+      *reinterpret_cast<Vec *>(p + (j + 1) * step) = S;
     }
   }
 }
 
 template <bool kStateOnly>
 cudaError_t launch_pass(const LinearArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream) {
-  const dim3 grid(unsigned(a.plan.slots) * unsigned(a.H), unsigned((a.d_v + kCols - 1) / kCols));
+  const unsigned pieces = unsigned(a.plan.inner) + (kStateOnly ? 0u : unsigned(a.num_seqs));
+  const dim3 grid(pieces * unsigned(a.H), unsigned((a.d_v + kCols - 1) / kCols));
   const bool wide = a.d_k > 64;
   using Kern = void (*)(const LinearArgs);
 #define KDA_LIN(ib, ob) \
@@ -223,8 +227,10 @@ cudaError_t launch_pass(const LinearArgs &a, bool in_bf16, bool out_bf16, cudaSt
 
 cudaError_t launch_linear_scan(const LinearArgs &a, cudaStream_t stream) {
   const int64_t dd = int64_t(a.d_k) * a.d_v;
-  const dim3 grid(unsigned(a.num_seqs) * unsigned(a.H), unsigned((dd + 255) / 256));
-  linear_scan_kernel<<<grid, 256, 0, stream>>>(a);
+  const int vec = dd % 4 == 0 ? 4 : 1;  // states start on 16-byte boundaries
+  const dim3 grid(unsigned(a.plan.inner) * unsigned(a.H), unsigned((dd + 256 * vec - 1) / (256 * vec)));
+  if (vec == 4) linear_scan_kernel<4><<<grid, 256, 0, stream>>>(a);
+  else linear_scan_kernel<1><<<grid, 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -260,20 +266,19 @@ LinearPlan linear_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, boo
     const int64_t m = tasks / (H * tiles);
     if (m >= 2) len = (total + m - 1) / m;
   } else {
-    len = (total * H * tiles + tasks - 1) / tasks;
+    len = (total * H * tiles * 2 + 3 * tasks - 1) / (3 * tasks);
   }
   len = (len + unit - 1) / unit * unit;
   if (len > 0 && len < min_len) len = min_len;
   if (len > 0 && len < total) {
-    const int64_t slots = total / len + num_seqs;
-    if (slots * H <= INT32_MAX / 4) {
+    const int64_t places = total / len + num_seqs;
+    if (places * H <= INT32_MAX / 4) {
       p.seg_len = int32_t(len);
-      p.slots = int32_t(slots);
-      p.state_bytes = align256(size_t(slots) * H * d_k * d_v * 4);
-      p.bytes = p.state_bytes + align256(size_t(slots) * H * 4);
+      p.inner = int32_t(total / len);
+      p.state_bytes = align256(size_t(places) * H * d_k * d_v * 4);
+      p.bytes = p.state_bytes + align256(size_t(places) * H * 4);
     }
   }
-  if (p.seg_len == 0) p.slots = num_seqs;
   return p;
 }
 

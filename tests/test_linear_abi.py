@@ -127,32 +127,41 @@ def test_binding_refuses():
         B.block_norm(x, x, pre_weight=torch.zeros(8).double())
 
 
-def _slot(cu, L, slot):
-    """The kernels' way from a slot to (sequence, first token, end, first, last), or None if idle."""
-    n = max(m for m in range(len(cu) - 1) if cu[m] // L + m <= slot)
-    j = slot - (cu[n] // L + n)
+def _piece(cu, L, index):
+    """The kernels' way from a piece to (sequence, place, first token, end, first, last), or None if
+    idle: pieces below total // L find a segment that has a successor, the others last segments."""
+    inner = cu[-1] // L
+    if index >= inner:
+        n = index - inner
+        j = 0 if cu[n + 1] == cu[n] else (cu[n + 1] - cu[n] - 1) // L
+        return n, cu[n] // L + n + j, cu[n] + j * L, cu[n + 1], j == 0, True
+    mark = (index + 1) * L
+    n = max(m for m in range(len(cu) - 1) if cu[m] < mark)
+    j = index - cu[n] // L
     t0 = cu[n] + j * L
-    if j > 0 and t0 >= cu[n + 1]:
-        return None
-    return n, t0, min(t0 + L, cu[n + 1]), j == 0, t0 + L >= cu[n + 1]
+    return (n, cu[n] // L + n + j, t0, t0 + L, j == 0, False) if t0 + L < cu[n + 1] else None
 
 
 @pytest.mark.parametrize("seed", range(8))
 @pytest.mark.parametrize("L", [16, 64, 128, 1000])
-def test_slots_cover_every_token_once(seed, L):
+def test_pieces_cover_every_token_once(seed, L):
     r = np.random.default_rng(seed)
     lens = [int(x) for x in r.integers(0, [3, 40, 300, 5000][seed % 4], size=1 + seed * 3)]
     if seed == 3:
         lens = [0, 0, L, 0, 2 * L, L - 1, 1, L + 1, 0]
     cu = [0] + [int(x) for x in np.cumsum(lens)]
-    got = [_slot(cu, L, s) for s in range(cu[-1] // L + len(lens))]
+    got = [_piece(cu, L, i) for i in range(cu[-1] // L + len(lens))]
+    got = [g for g in got if g is not None]
+    places = [g[1] for g in got]
+    assert len(set(places)) == len(places) and max(places) < cu[-1] // L + len(lens)
     for n, length in enumerate(lens):
-        mine = [g for g in got if g is not None and g[0] == n]
+        mine = sorted((g for g in got if g[0] == n), key=lambda g: g[2])
         assert len(mine) == max(1, -(-length // L))
-        assert [g[3] for g in mine] == [True] + [False] * (len(mine) - 1)
-        assert [g[4] for g in mine] == [False] * (len(mine) - 1) + [True]
+        assert [g[1] for g in mine] == list(range(mine[0][1], mine[0][1] + len(mine)))
+        assert [g[4] for g in mine] == [True] + [False] * (len(mine) - 1)
+        assert [g[5] for g in mine] == [False] * (len(mine) - 1) + [True]
         edge = cu[n]
-        for _, a, b, _, _ in mine:
+        for _, _, a, b, _, _ in mine:
             assert a == edge
             edge = b
         assert edge == cu[n + 1]
