@@ -93,7 +93,7 @@ struct Control {
   uint64_t q_full[2], k_full[2], v_full[2];            // by chunk parity
   uint64_t qs_done[2], d_done[2], pv_done[2];          // Q S (and Q K^T before it), K^T V', P V
   uint64_t vp_full[2], vp_free[2], tab_full[2], tab_free[2];
-  uint64_t qk_done, p_full, d_free, s_full, o_read, drain;
+  uint64_t qk_done, p_full, d_free, s_full, o_read, zeroed, drain;
   uint32_t tmem;
   volatile uint32_t abort;
 };
@@ -114,6 +114,30 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   uint32_t r;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
+}
+
+// 8 floats of a state's row: 32 bytes in one access where they are aligned to that (the load/store pipe
+// takes a row per thread either way)
+__device__ __forceinline__ void load_8(const float *p, float *v) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store_8(float *p, const float *v) {
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
 }
 
 // An MMA warp runs as a whole, so that descriptors stay in uniform registers (a lone lane has to
@@ -186,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ctl->tab_full[i], 1), mbar_init(&ctl->tab_free[i], kStateOnly ? 14 : 16);
     }
     mbar_init(&ctl->qk_done, 1), mbar_init(&ctl->p_full, 4), mbar_init(&ctl->d_free, 8);
-    mbar_init(&ctl->s_full, 8), mbar_init(&ctl->o_read, 8), mbar_init(&ctl->drain, kStateOnly ? 1 : 2);
+    mbar_init(&ctl->s_full, 8), mbar_init(&ctl->o_read, 8), mbar_init(&ctl->zeroed, 4), mbar_init(&ctl->drain, kStateOnly ? 1 : 2);
     ctl->abort = 0;
     fence_mbarrier_init();
   }
@@ -215,8 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == 0) {
-    // ---- loads: chunk n's Q, K and V, each when its buffer is free; chunk n + 1's tiles go to L2
-    // meanwhile
+    // ---- loads: chunk n's V, Q and K, each when its buffer is free
     if (lane == 0) {
       Bufs<kStateOnly> at;
       int issued = 0;
@@ -250,16 +273,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int b = 0; b < 2; ++b) tma_load_3d(smem + at.K() + b * 16384, &mk, &ctl->k_full[s2], 64 * b, hk, t);
         issued = 3 * n + 3;
-        if (n + 1 < chunks) {
-          const int32_t next = kStateOnly ? t - kC : t + kC;
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            if constexpr (!kStateOnly) tma_prefetch_l2_3d(&mq, 64 * b, hk, next);
-            tma_prefetch_l2_3d(&mk, 64 * b, hk, next);
-          }
-#pragma unroll
-          for (int b = 0; b < kDV / 64; ++b) tma_prefetch_l2_3d(&mv, col0 + 64 * b, h, next);
-        }
       }
       // every load issued has landed before the CTA may end: the last two of each tensor
       const int nv = (issued + 2) / 3, nq = (issued + 1) / 3, nk = issued / 3;
@@ -305,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(leader, ctl->qs_done[n & 1]);
         if (!wait_warp(ctl->v_full[n & 1], n >> 1, DEVERR_TMA_TIMEOUT)) break;
         if (!wait_warp(ctl->p_full, n, DEVERR_MMA_TIMEOUT)) break;
-        // the last chunk's rows behind the segment: V is zeroed there before K^T V' begins
-        if ((n + 1) * kC > len && !wait_warp(ctl->d_done[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
+        // the last chunk's rows behind the segment are zeroed in V
+        if ((n + 1) * kC > len && !wait_warp(ctl->zeroed, 0, DEVERR_MMA_TIMEOUT)) break;
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < (kPair ? 16 : 8); ++ks)
@@ -530,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
+        if (!kStateOnly && lane == 0) mbar_arrive(&ctl->zeroed);
       }
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
@@ -578,12 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         else if (a.init_state != nullptr) src = a.init_state + (int64_t(s.n) * a.H + h) * dd;
       }
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 4) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = 0; c < kHalf; c += 8) {  // d_v is a multiple of 8
         const int col = col0 + cb + c;
-        if (src != nullptr && r < a.d_k && col < a.d_v)  // d_v is a multiple of 8
-          x = *reinterpret_cast<const float4 *>(src + int64_t(r) * a.d_v + col);
-        S[c] = x.x, S[c + 1] = x.y, S[c + 2] = x.z, S[c + 3] = x.w;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) S[c + e] = 0.f;
+        if (src != nullptr && r < a.d_k && col < a.d_v) load_8(src + int64_t(r) * a.d_v + col, S + c);
       }
     }
     const uint32_t state_off = sw128_chunk(r, 0, cb >> 6, 128);
@@ -694,10 +707,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : (s.last && a.final_state != nullptr) ? a.final_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
     if (dst != nullptr && r < a.d_k) {
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 4) {
+      for (int c = 0; c < kHalf; c += 8) {
         const int col = col0 + cb + c;
-        if (col < a.d_v)
-          *reinterpret_cast<float4 *>(dst + int64_t(r) * a.d_v + col) = make_float4(S[c], S[c + 1], S[c + 2], S[c + 3]);
+        if (col < a.d_v) store_8(dst + int64_t(r) * a.d_v + col, S + c);
       }
     }
   }

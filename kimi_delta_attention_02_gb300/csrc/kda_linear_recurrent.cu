@@ -259,8 +259,8 @@ LinearPlan linear_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, boo
   p.tensor = !recurrent && linear_chunked_supported(d_k, d_v, in_bf16);
   p.col_tile = !p.tensor ? kCols : out_bf16 && d_v > 64 ? 128 : 64;
   const int64_t tiles = (d_v + p.col_tile - 1) / p.col_tile;
-  const int64_t unit = p.tensor ? 128 : 16, min_len = p.tensor ? 512 : 64;
-  const int64_t tasks = p.tensor ? kPlanSMs : 2 * kPlanSMs;
+  const int64_t unit = p.tensor ? 128 : 16, min_len = p.tensor ? 512 : 48;
+  const int64_t tasks = p.tensor ? kPlanSMs : 3 * kPlanSMs;
   int64_t len = 0;
   if (num_seqs == 1) {
     const int64_t m = tasks / (H * tiles);
