@@ -386,10 +386,20 @@ kda_status kda_prologue(const void *q_raw, const void *k_raw, const void *v_raw,
  *                while e^g and the state stay finite. NaN propagates. No clamp is applied.
  *   workspace    (prefill) as in kda_prefill, of kda_linear_prefill_workspace_size() bytes: with
  *                it, sequences longer than a CTA's share of the call are cut into segments that
- *                run side by side; with less, every (sequence, head) runs from end to end. It may
- *                not be shared by calls that run at the same time (two captured graphs that may
- *                replay together need one each).
+ *                run side by side, and bf16 head sizes that are no multiple of 8 are padded for
+ *                the tensor-core kernel; with less, every (sequence, head) runs from end to end,
+ *                and such head sizes run the token-recurrent kernel. It may not be shared by
+ *                calls that run at the same time (two captured graphs that may replay together
+ *                need one each).
  *   force_recurrent (prefill) nonzero runs the fp32 token-recurrent kernel
+ *
+ * bf16 prompts run a tensor-core kernel in chunks of 128 tokens, unless their sequences are short
+ * (fewer than 16, 32 or 40 tokens on average, by head size and output type). It rounds the masked
+ * products q.k and the entering state to bf16 before their second product when the output is
+ * bf16, to pairs of bf16 (2^-16) when it is fp32, and the decayed v to such pairs for the fp32
+ * state. An infinity or NaN in v reaches every output of its chunk in that (sequence, head), and
+ * what follows; one in q, k or log_decay only what depends on it. fp32 inputs and short sequences
+ * run the fp32 token-recurrent kernel.
  *
  * Sizes: 1 <= d_k, d_v <= 128, H, H_k >= 1; decode needs B >= 1. Results are accumulated in fp32
  * and states are fp32.
@@ -434,7 +444,7 @@ kda_status kda_linear_decode(const kda_linear_decode_params *params, void *strea
  * CUDA call; the same arguments always give the same answer.
  */
 size_t kda_linear_prefill_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t H,
-                                         int32_t d_k, int32_t d_v, kda_dtype in_dtype,
+                                         int32_t H_k, int32_t d_k, int32_t d_v, kda_dtype in_dtype,
                                          kda_dtype out_dtype, int32_t force_recurrent);
 
 /*

@@ -126,7 +126,7 @@ def _declare(lib):
     lib.kda_linear_prefill.restype = i32
     lib.kda_linear_decode.argtypes = [ctypes.POINTER(LinearDecodeParams), vp]
     lib.kda_linear_decode.restype = i32
-    lib.kda_linear_prefill_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32, i32, i32]
+    lib.kda_linear_prefill_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32, i32, i32, i32]
     lib.kda_linear_prefill_workspace_size.restype = sz
     lib.kda_block_norm.argtypes = [ctypes.POINTER(BlockNormParams), vp]
     lib.kda_block_norm.restype = i32
@@ -514,9 +514,11 @@ def _linear_sizes(q, k, v, log_decay, rows_name):
 
 
 def linear_workspace_size(total_tokens: int, num_seqs: int, H: int, d_k: int = 128, d_v: int = 128,
-                          dtype=torch.bfloat16, out_dtype=torch.float32, recurrent: bool = False) -> int:
-    """Bytes of device scratch ``linear_prefill`` can use (``kda_linear_prefill_workspace_size``)."""
-    return int(lib().kda_linear_prefill_workspace_size(int(total_tokens), int(num_seqs), int(H), int(d_k), int(d_v),
+                          dtype=torch.bfloat16, out_dtype=torch.float32, recurrent: bool = False, H_k=None) -> int:
+    """Bytes of device scratch ``linear_prefill`` can use (``kda_linear_prefill_workspace_size``);
+    ``H_k`` query / key heads, H by default."""
+    return int(lib().kda_linear_prefill_workspace_size(int(total_tokens), int(num_seqs), int(H),
+                                                       int(H if H_k is None else H_k), int(d_k), int(d_v),
                                                        _io_dtype(dtype), _io_dtype(out_dtype), int(bool(recurrent))))
 
 
@@ -566,7 +568,7 @@ def linear_prefill(q, k, v, log_decay, cu_seqlens, init_state=None, *, out=None,
     if given is None and workspace is not None:
         if workspace != "auto":
             raise ValueError("workspace must be 'auto', None or a uint8 CUDA tensor")
-        n = handle.kda_linear_prefill_workspace_size(T, N, H, d_k, d_v, dt, odt, rec)
+        n = handle.kda_linear_prefill_workspace_size(T, N, H, H_k, d_k, d_v, dt, odt, rec)
         if n:
             given = torch.empty(n, dtype=torch.uint8, device=q.device)
             _used_on(stream, given)

@@ -455,12 +455,13 @@ kda_status kda_prologue(const void *q_raw, const void *k_raw, const void *v_raw,
   return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
-size_t kda_linear_prefill_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t d_k, int32_t d_v,
-                                         kda_dtype in_dtype, kda_dtype out_dtype, int32_t force_recurrent) {
-  if (check_linear_sizes(total_tokens, num_seqs, H, H, d_k, d_v, 1, in_dtype, out_dtype) != KDA_OK) return 0;
+size_t kda_linear_prefill_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t H_k, int32_t d_k,
+                                         int32_t d_v, kda_dtype in_dtype, kda_dtype out_dtype,
+                                         int32_t force_recurrent) {
+  if (check_linear_sizes(total_tokens, num_seqs, H, H_k, d_k, d_v, 1, in_dtype, out_dtype) != KDA_OK) return 0;
   if (total_tokens == 0 || num_seqs == 0) return 0;
-  return linear_plan(total_tokens, num_seqs, H, d_k, d_v, in_dtype == KDA_BF16, out_dtype == KDA_BF16,
-                     force_recurrent != 0)
+  return linear_plan(total_tokens, num_seqs, H, H_k, d_k, d_v, in_dtype == KDA_BF16, out_dtype == KDA_BF16,
+                     force_recurrent != 0, SIZE_MAX)
       .bytes;
 }
 
@@ -497,16 +498,16 @@ kda_status kda_linear_prefill(const kda_linear_prefill_params *p, void *stream) 
   a.num_seqs = p->num_seqs, a.H = p->H, a.H_k = p->H_k, a.d_k = p->d_k, a.d_v = p->d_v;
   a.per_token = p->decay_per_token, a.total = T, a.scale = p->scale;
   const bool in_bf16 = p->in_dtype == KDA_BF16, out_bf16 = p->out_dtype == KDA_BF16;
-  a.plan = linear_plan(T, p->num_seqs, p->H, p->d_k, p->d_v, in_bf16, out_bf16, p->force_recurrent != 0);
-  if (p->workspace_bytes < a.plan.bytes) {  // every sequence from end to end
-    a.plan.seg_len = a.plan.inner = 0;
-  } else if (a.plan.bytes != 0) {
-    a.seg_states = static_cast<float *>(p->workspace);
-    a.seg_decay = reinterpret_cast<float *>(static_cast<uint8_t *>(p->workspace) + a.plan.state_bytes);
+  a.plan = linear_plan(T, p->num_seqs, p->H, p->H_k, p->d_k, p->d_v, in_bf16, out_bf16, p->force_recurrent != 0,
+                       p->workspace_bytes);
+  a.workspace = static_cast<uint8_t *>(p->workspace);
+  if (a.plan.seg_len != 0) {
+    a.seg_states = reinterpret_cast<float *>(a.workspace + a.plan.states);
+    a.seg_decay = reinterpret_cast<float *>(a.workspace + a.plan.decays);
   }
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t err = a.plan.tensor && T > 0 ? launch_linear_chunked(a, out_bf16, cs)
-                                                 : launch_linear_recurrent(a, in_bf16, out_bf16, cs);
+  const cudaError_t err = a.plan.tensor ? launch_linear_chunked(a, out_bf16, cs)
+                                        : launch_linear_recurrent(a, in_bf16, out_bf16, cs);
   return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

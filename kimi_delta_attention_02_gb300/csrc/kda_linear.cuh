@@ -23,9 +23,14 @@ struct LinearPlan {
   int32_t inner = 0;        // total / L
   int32_t col_tile = 0;     // value columns per CTA
   bool tensor = false;      // tensor-core kernel (bf16), else the token-recurrent one
-  size_t state_bytes = 0;   // workspace: [places, H, d_k, d_v] fp32 entering states, then
-  size_t bytes = 0;         // [places, H] fp32 summed log-decays
+  bool pad = false;         // runs on copies whose head sizes are padded to multiples of 8
+  size_t states = 0;        // places in the workspace: [places, H, d_k, d_v] fp32 entering states,
+  size_t decays = 0;        // [places, H] fp32 summed log-decays, the padded copies
+  size_t pad_q = 0, pad_k = 0, pad_v = 0, pad_out = 0, pad_states = 0;
+  size_t bytes = 0;         // of the workspace that the plan uses
 };
+
+constexpr int kLinearTokenCols = 64;  // value columns per CTA of the token-recurrent kernel
 
 struct LinearSlot {
   int n;              // sequence
@@ -84,7 +89,8 @@ struct LinearArgs {
   const float *init_state;  // [num_seqs, H, d_k, d_v] or null
   void *out;
   float *final_state;       // or null
-  float *seg_states;        // workspace, or null (seg_len = 0)
+  uint8_t *workspace;       // or null
+  float *seg_states;        // in the workspace, or null (seg_len = 0)
   float *seg_decay;
   int num_seqs, H, H_k, d_k, d_v, per_token;
   int64_t total;
@@ -92,10 +98,15 @@ struct LinearArgs {
   LinearPlan plan;
 };
 
-LinearPlan linear_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool in_bf16, bool out_bf16,
-                       bool recurrent);
+// The plan for a call that has this much workspace (SIZE_MAX: what it would like to have).
+LinearPlan linear_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool out_bf16,
+                       bool recurrent, size_t workspace_bytes);
+// Copies what needs padding and points `a` at the copies (d_v becomes the padded one; d_k stays, the
+// states have that many rows), and brings the output and the final states back.
+cudaError_t launch_linear_pad(LinearArgs &a, cudaStream_t stream);
+cudaError_t launch_linear_unpad(const LinearArgs &a, bool out_bf16, void *out, float *final_state, int d_v,
+                                cudaStream_t stream);
 cudaError_t launch_linear_recurrent(const LinearArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream);
-bool linear_chunked_supported(int d_k, int d_v, bool in_bf16);
 cudaError_t launch_linear_chunked(const LinearArgs &a, bool out_bf16, cudaStream_t stream);
 cudaError_t launch_linear_scan(const LinearArgs &a, cudaStream_t stream);
 

@@ -1,6 +1,6 @@
 // kda_linear_chunked.cu -- linear attention with one decay per head on the tensor cores (bf16
-// inputs, head sizes that are multiples of 8): S_t = e^{g_t} S_{t-1} + k_t v_t^T,
-// o_t = scale S_t^T q_t, in chunks of 128 tokens.
+// inputs): S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t, in chunks of 128 tokens. Rows of
+// q, k and v are multiples of 16 bytes (the launch pads copies of others).
 //
 // With G the cumulative log-decay inside a chunk and S the state that enters it,
 //     O  = (D (*) Q K^T) V + diag(e^G) Q S,      D_ij = e^{G_i - G_j} for j <= i, else 0,
@@ -748,12 +748,12 @@ cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
 
 }  // namespace
 
-bool linear_chunked_supported(int d_k, int d_v, bool in_bf16) { return in_bf16 && d_k % 8 == 0 && d_v % 8 == 0; }
-
-cudaError_t launch_linear_chunked(const LinearArgs &a, bool out_bf16, cudaStream_t stream) {
+namespace {
+cudaError_t launch_passes(const LinearArgs &a, bool out_bf16, cudaStream_t stream) {
   CUtensorMap mq, mk, mv;
-  if (!tensor_map_3d(&mq, a.q, true, a.total, a.H_k, a.d_k, 64, kC, true) ||
-      !tensor_map_3d(&mk, a.k, true, a.total, a.H_k, a.d_k, 64, kC, true) ||
+  const int d_k = (a.d_k + 7) & ~7;
+  if (!tensor_map_3d(&mq, a.q, true, a.total, a.H_k, d_k, 64, kC, true) ||
+      !tensor_map_3d(&mk, a.k, true, a.total, a.H_k, d_k, 64, kC, true) ||
       !tensor_map_3d(&mv, a.v, true, a.total, a.H, a.d_v, 64, kC, true))
     return cudaErrorInvalidValue;
   const bool wide = a.plan.col_tile == 128;
@@ -766,6 +766,17 @@ cudaError_t launch_linear_chunked(const LinearArgs &a, bool out_bf16, cudaStream
   if (wide) return launch_one<128, true, false>(mq, mk, mv, a, stream);
   return out_bf16 ? launch_one<64, true, false>(mq, mk, mv, a, stream)
                   : launch_one<64, false, false>(mq, mk, mv, a, stream);
+}
+}  // namespace
+
+cudaError_t launch_linear_chunked(const LinearArgs &a, bool out_bf16, cudaStream_t stream) {
+  if (!a.plan.pad) return launch_passes(a, out_bf16, stream);
+  LinearArgs b = a;
+  cudaError_t e = launch_linear_pad(b, stream);
+  if (e == cudaSuccess) e = launch_passes(b, out_bf16, stream);
+  if (e == cudaSuccess && a.d_v % 8 != 0)
+    e = launch_linear_unpad(b, out_bf16, a.out, a.final_state, a.d_v, stream);
+  return e;
 }
 
 }  // namespace kda

@@ -15,7 +15,7 @@ namespace kda {
 namespace {
 
 constexpr int kTok = 16;    // tokens per stage
-constexpr int kCols = 64;   // value columns per CTA
+constexpr int kCols = kLinearTokenCols;
 constexpr int kThr = 128;
 
 // kRows: key rows per thread (16 for d_k <= 64, else 32). kStateOnly: pass 1 of a segmented call,
@@ -162,49 +162,6 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
   if (kStateOnly && tid == 0 && blockIdx.y == 0) a.seg_decay[s.place * a.H + h] = float(decay_sum);
 }
 
-// Pass 2: a segment's end state from zero, B_j, gives way to its successor's entering state in the
-// successor's place, E_0 = initial state (read where it is), E_{j+1} = e^{D_j} E_j + B_j. The CTAs of
-// a sequence's first segment walk its segments, kVec entries per thread, the next segments' entries on
-// their way meanwhile.
-template <int kVec>
-__global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a) {
-  const int h = blockIdx.x % a.H;
-  LinearSlot s;
-  if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, blockIdx.x / a.H, s) || !s.first) return;
-  const int segs = (a.cu[s.n + 1] - a.cu[s.n] + a.plan.seg_len - 1) / a.plan.seg_len;
-  const int64_t dd = int64_t(a.d_k) * a.d_v;
-  const int64_t e = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * kVec;
-  if (e >= dd) return;
-  struct alignas(4 * kVec) Vec {
-    float v[kVec];
-  };
-  const int64_t step = int64_t(a.H) * dd;
-  float *p = a.seg_states + (s.place * a.H + h) * dd + e;
-  const float *d = a.seg_decay + s.place * a.H + h;
-  auto read = [&](int j) { return *reinterpret_cast<const Vec *>(p + j * step); };
-  Vec S = {};
-  if (a.init_state != nullptr) S = *reinterpret_cast<const Vec *>(a.init_state + (int64_t(s.n) * a.H + h) * dd + e);
-  constexpr int kAhead = 4;
-  Vec b[kAhead] = {};
-  float D[kAhead] = {};
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (i + 1 < segs) b[i] = read(i), D[i] = d[i * a.H];
-  for (int j0 = 0; j0 + 1 < segs; j0 += kAhead) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i;
-      if (j + 1 >= segs) break;
-      const float em1 = expm1f(D[i]);
-#pragma unroll
-      for (int v = 0; v < kVec; ++v) S.v[v] = decay_step(S.v[v], em1) + b[i].v[v];
-      if (j + kAhead + 1 < segs) b[i] = read(j + kAhead), D[i] = d[(j + kAhead) * a.H];
-      // B_{j+1} of this place, if there is one, was read above (kAhead >= 2)
-      *reinterpret_cast<Vec *>(p + (j + 1) * step) = S;
-    }
-  }
-}
-
 template <bool kStateOnly>
 cudaError_t launch_pass(const LinearArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream) {
   const unsigned pieces = unsigned(a.plan.inner) + (kStateOnly ? 0u : unsigned(a.num_seqs));
@@ -225,15 +182,6 @@ cudaError_t launch_pass(const LinearArgs &a, bool in_bf16, bool out_bf16, cudaSt
 
 }  // namespace
 
-cudaError_t launch_linear_scan(const LinearArgs &a, cudaStream_t stream) {
-  const int64_t dd = int64_t(a.d_k) * a.d_v;
-  const int vec = dd % 4 == 0 ? 4 : 1;  // states start on 16-byte boundaries
-  const dim3 grid(unsigned(a.plan.inner) * unsigned(a.H), unsigned((dd + 256 * vec - 1) / (256 * vec)));
-  if (vec == 4) linear_scan_kernel<4><<<grid, 256, 0, stream>>>(a);
-  else linear_scan_kernel<1><<<grid, 256, 0, stream>>>(a);
-  return cudaGetLastError();
-}
-
 cudaError_t launch_linear_recurrent(const LinearArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream) {
   if (a.plan.seg_len != 0) {
     cudaError_t e = launch_pass<true>(a, in_bf16, out_bf16, stream);
@@ -241,45 +189,6 @@ cudaError_t launch_linear_recurrent(const LinearArgs &a, bool in_bf16, bool out_
     if (e != cudaSuccess) return e;
   }
   return launch_pass<false>(a, in_bf16, out_bf16, stream);
-}
-
-namespace {
-// The plan counts a GB300's 152 SMs (a fixed figure: the workspace query needs no device).
-constexpr int kPlanSMs = 152;
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-}  // namespace
-
-// Segments are as long as the call's tokens x heads x column tiles divided among `tasks` CTAs, so
-// that a sequence longer than a CTA's share is split and the others stay whole. Of a single
-// sequence the length is known: it is cut into as many equal segments as CTAs fit beside each
-// other.
-LinearPlan linear_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool in_bf16, bool out_bf16,
-                       bool recurrent) {
-  LinearPlan p;
-  p.tensor = !recurrent && linear_chunked_supported(d_k, d_v, in_bf16);
-  p.col_tile = !p.tensor ? kCols : out_bf16 && d_v > 64 ? 128 : 64;
-  const int64_t tiles = (d_v + p.col_tile - 1) / p.col_tile;
-  const int64_t unit = p.tensor ? 128 : 16, min_len = p.tensor ? 512 : 48;
-  const int64_t tasks = p.tensor ? kPlanSMs : 3 * kPlanSMs;
-  int64_t len = 0;
-  if (num_seqs == 1) {
-    const int64_t m = tasks / (H * tiles);
-    if (m >= 2) len = (total + m - 1) / m;
-  } else {
-    len = (total * H * tiles * 2 + 3 * tasks - 1) / (3 * tasks);
-  }
-  len = (len + unit - 1) / unit * unit;
-  if (len > 0 && len < min_len) len = min_len;
-  if (len > 0 && len < total) {
-    const int64_t places = total / len + num_seqs;
-    if (places * H <= INT32_MAX / 4) {
-      p.seg_len = int32_t(len);
-      p.inner = int32_t(total / len);
-      p.state_bytes = align256(size_t(places) * H * d_k * d_v * 4);
-      p.bytes = p.state_bytes + align256(size_t(places) * H * 4);
-    }
-  }
-  return p;
 }
 
 }  // namespace kda

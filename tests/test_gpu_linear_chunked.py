@@ -1,5 +1,5 @@
-"""kda_linear_prefill on the tensor-core kernel (bf16, head sizes that are multiples of 8), its
-segments and its pass of state sums, against the fp64 oracle.
+"""kda_linear_prefill on the tensor-core kernel (bf16), its segments and its pass of state sums,
+against the fp64 oracle.
 
 Bounds, relative to the magnitude (the same sums over absolute values). The state: its terms'
 decayed values enter as bf16 pairs, off by at most 2^-16; the decay of a term is 2 to a sum of at
@@ -43,6 +43,76 @@ def test_lengths(lens, out_dtype):
 def test_head_sizes(d_k, d_v, out_dtype):
     lens = [150, 40]
     _check(make(lens, H=3, d_k=d_k, d_v=d_v, seed=d_k + d_v), lens, scale=0.25, out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("out_dtype", [B16, F32])
+@pytest.mark.parametrize("d_k,d_v", [(1, 1), (127, 127), (13, 128), (128, 13), (65, 66), (100, 4), (7, 121), (128, 124)])
+def test_padded_head_sizes(d_k, d_v, out_dtype):
+    """Head sizes that are no multiple of 8 pass through a padded copy in the workspace; without
+    one the token-recurrent kernel runs them."""
+    lens = [150, 0, 1, 40]
+    c = make(lens, H=4, H_k=2, d_k=d_k, d_v=d_v, seed=d_k + d_v)
+    assert binding.linear_workspace_size(191, 4, 4, d_k, d_v, B16, out_dtype, H_k=2) > 0
+    _check(c, lens, scale=0.25, out_dtype=out_dtype)
+    _check(c, lens, scale=0.25, out_dtype=out_dtype, workspace=None)
+    long = [1300]  # padded and cut into segments
+    _check(make(long, H=2, d_k=d_k, d_v=d_v, seed=d_k), long, out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("lens", [[15], [16], [17], [14, 0, 34], [31, 32], [33, 31], [39, 40], [41, 39]])
+@pytest.mark.parametrize("d,out_dtype", [(128, B16), (64, F32), (60, B16)])
+def test_either_side_of_the_length_rule(lens, d, out_dtype):
+    """Sequences short on average take the token-recurrent kernel, the same as when it is asked for."""
+    c = make(lens, H=2, d_k=d, d_v=d, seed=sum(lens))
+    out, fin = _check(c, lens, out_dtype=out_dtype)
+    if sum(lens) < (40 if d == 60 else 16 if d == 128 else 32) * len(lens):
+        o, f = run(c, out_dtype=out_dtype, recurrent=True)
+        assert torch.equal(out, o) and torch.equal(fin, f)
+
+
+def test_padded_states_and_rows_behind():
+    """Through the padded copies: no initial or final states, states in place, rows behind the last
+    sequence left as they were, NaN there and in another sequence kept out."""
+    lens = [100, 90, 70]
+    c = make(lens, H=4, H_k=2, d_k=53, d_v=37, seed=4)
+    o, f, mo, mf = reference(c)
+    fine = 2.0 ** -15 + fp32_factor(130, 64)
+    for n in ("q", "k", "v"):
+        c[n][100:190] = float("nan")
+    wide = {n: torch.cat([c[n], torch.full_like(c[n][:40], float("nan"))]) for n in ("q", "k", "v", "log_decay")}
+    keep = np.r_[0:100, 190:260]
+    out = torch.full((300, 4, 37), 7.0, device="cuda", dtype=F32)
+    state = c["init_state"].clone()
+    binding.linear_prefill(wide["q"], wide["k"], wide["v"], wide["log_decay"], c["cu_seqlens"], state, out=out,
+                           final_state=state)
+    binding.check_device_error()
+    check(out[:260][keep], o[keep], mo[keep], fine, "out")
+    check(state[[0, 2]], f[[0, 2]], mf[[0, 2]], fine, "final")
+    assert (out[260:] == 7.0).all()
+    _check(make(lens, H=4, H_k=2, d_k=53, d_v=37, init=False), lens)
+    assert run(make(lens, H=4, H_k=2, d_k=53, d_v=37), want_final=False)[1] is None
+
+
+def test_unaligned_views():
+    """States and outputs that start 16 bytes off a 32-byte boundary, and packed rows behind them."""
+    lens = [140, 30]
+    c = make(lens, H=2, d_k=64, d_v=72, seed=5)
+    o, f, mo, mf = reference(c)
+    fine = 2.0 ** -15 + fp32_factor(130, 64)
+    for out_dtype in (B16, F32):
+        per = 8 if out_dtype == B16 else 4
+        flat = torch.full((170 * 2 * 72 + 2 * per,), 7.0, device="cuda", dtype=out_dtype)
+        out = flat[per:-per].view(170, 2, 72)
+        states = torch.full((2 * 2 * 64 * 72 + 8,), 7.0, device="cuda")
+        fin = states[4:-4].view(2, 2, 64, 72)
+        fin.copy_(c["init_state"])
+        run({**c, "init_state": fin}, out=out, final_state=fin)
+        if out_dtype == B16:
+            check(out, o, mo * (2.0 ** -8 + fine) + 2.0 ** -8 * np.abs(o), 1.0, "out")
+        else:
+            check(out, o, mo, fine, "out")
+        check(fin, f, mf, fine, "final")
+        assert (flat[:per] == 7).all() and (flat[-per:] == 7).all() and (states[:4] == 7).all() and (states[-4:] == 7).all()
 
 
 @pytest.mark.parametrize("H,H_k", [(6, 1), (6, 3), (8, 2)])
