@@ -30,6 +30,7 @@ struct LinearPlan {
   size_t bytes = 0;         // of the workspace that the plan uses
 };
 
+constexpr int kLinearSMs = 152;       // a GB300's (fixed: the workspace query needs no device)
 constexpr int kLinearTokenCols = 64;  // value columns per CTA of the token-recurrent kernel
 
 struct LinearSlot {

@@ -5,8 +5,6 @@
 namespace kda {
 namespace {
 
-// The plan counts a GB300's 152 SMs (a fixed figure: the workspace query needs no device).
-constexpr int kPlanSMs = 152;
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 int up8(int x) { return (x + 7) & ~7; }
 
@@ -110,7 +108,7 @@ cudaError_t launch_pad(const PadArgs &a, cudaStream_t stream) {
     const int64_t pieces = a.job[i].rows * (up8(a.job[i].d) / 8);
     most = pieces > most ? pieces : most;
   }
-  const int64_t need = (most + 255) / 256, fit = kPlanSMs * 16;
+  const int64_t need = (most + 255) / 256, fit = kLinearSMs * 16;
   linear_pad_kernel<kBack><<<dim3(unsigned(need < fit ? need : fit), unsigned(a.jobs)), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
@@ -203,7 +201,7 @@ LinearPlan linear_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int
   p.col_tile = !p.tensor ? kLinearTokenCols : wide ? 128 : 64;
   const int64_t tiles = (d_v + p.col_tile - 1) / p.col_tile;
   const int64_t unit = p.tensor ? 128 : 16, min_len = p.tensor ? 512 : 48;
-  const int64_t tasks = p.tensor ? kPlanSMs : 3 * kPlanSMs;
+  const int64_t tasks = p.tensor ? kLinearSMs : 3 * kLinearSMs;
   int64_t len = 0;
   if (num_seqs == 1) {
     const int64_t m = tasks / (H * tiles);

@@ -43,6 +43,31 @@ def test_batches_and_shared_heads(B, H, H_k, per_token):
     _steps(B, H, H_k, 32, 32, torch.bfloat16, per_token, out_dtype=torch.bfloat16, steps=2)
 
 
+@pytest.mark.parametrize("B", [2, 80])
+@pytest.mark.parametrize("d_k,d_v", [(16, 16), (128, 32), (64, 33), (33, 64), (48, 72), (128, 60), (31, 53), (65, 31),
+                                     (53, 53), (100, 53), (9, 127), (33, 118), (118, 118), (16, 128), (128, 100)])
+def test_every_tile(d_k, d_v, B):
+    """Tiles of 32, 64 and 128 columns with 64, 128 and 256 threads, four columns per thread or one;
+    8 and 320 states, so that few states take narrower tiles."""
+    _steps(B, 4, 2, d_k, d_v, torch.bfloat16, True, steps=2)
+
+
+def test_on_another_stream():
+    """With ``stream=`` the call runs there, behind what that stream has been given."""
+    side = torch.cuda.Stream()
+    c = make([1] * 2, H=2, d_k=64, d_v=64)
+    state = torch.zeros_like(c["init_state"])
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(2_000_000)
+        state.copy_(c["init_state"])
+    out = binding.linear_decode(c["q"], c["k"], c["v"], c["log_decay"], state, stream=side)
+    side.synchronize()
+    o, f, mo, mf = reference(c)
+    check(out, o, mo, fp32_factor(1, 64), "out")
+    check(state, f, mf, fp32_factor(1, 64), "state")
+
+
 def test_prompt_then_tokens_equals_a_longer_prompt():
     """Prefill of 50 tokens, then five decode steps, against the oracle's 55 tokens."""
     c = make([55], H=4, H_k=2, d_k=128, d_v=64)
