@@ -99,6 +99,18 @@ struct LinearArgs {
   LinearPlan plan;
 };
 
+// A cut sequence's first segment enters with the initial state; where the final one takes its place,
+// pass 2 leaves a copy in the workspace, because the last segment may end before the first begins.
+__host__ __device__ __forceinline__ bool linear_in_place(const LinearArgs &a) {
+  return a.init_state != nullptr && a.init_state == a.final_state;
+}
+// The state that a segment enters with, or null (zeros), in pass 3.
+__device__ __forceinline__ const float *linear_entering(const LinearArgs &a, const LinearSlot &s, int h) {
+  const int64_t dd = int64_t(a.d_k) * a.d_v;
+  if (!s.first || (!s.last && linear_in_place(a))) return a.seg_states + (s.place * a.H + h) * dd;
+  return a.init_state != nullptr ? a.init_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
+}
+
 // The plan for a call that has this much workspace (SIZE_MAX: what it would like to have).
 LinearPlan linear_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool out_bf16,
                        bool recurrent, size_t workspace_bytes);

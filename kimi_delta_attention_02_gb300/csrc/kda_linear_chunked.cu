@@ -586,11 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t dd = int64_t(a.d_k) * a.d_v;
     float S[kHalf];
     {
-      const float *src = nullptr;
-      if constexpr (!kStateOnly) {
-        if (!s.first) src = a.seg_states + (s.place * a.H + h) * dd;
-        else if (a.init_state != nullptr) src = a.init_state + (int64_t(s.n) * a.H + h) * dd;
-      }
+      const float *src = kStateOnly ? nullptr : linear_entering(a, s, h);
 #pragma unroll
       for (int c = 0; c < kHalf; c += 8) {  // d_v is a multiple of 8
         const int col = col0 + cb + c;

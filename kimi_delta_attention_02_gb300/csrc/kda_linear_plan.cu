@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a) {
 #pragma unroll
   for (int i = 0; i < kAhead; ++i)
     if (i + 1 < segs) b[i] = read(i), D[i] = d[i * a.H];
+  if (linear_in_place(a)) *reinterpret_cast<Vec *>(p) = S;  // B_0 has been read
   for (int j0 = 0; j0 + 1 < segs; j0 += kAhead) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {

@@ -39,11 +39,7 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
   float2 S[2][kRows / 2];
   auto row_of = [&](int p) { return 16 * (p >> 1) + 4 * rg + 2 * (p & 1); };
   const int64_t dd = int64_t(a.d_k) * a.d_v;
-  const float *S0 = nullptr;
-  if constexpr (!kStateOnly) {
-    if (!s.first) S0 = a.seg_states + (s.place * a.H + h) * dd;
-    else if (a.init_state != nullptr) S0 = a.init_state + (int64_t(s.n) * a.H + h) * dd;
-  }
+  const float *S0 = kStateOnly ? nullptr : linear_entering(a, s, h);
 #pragma unroll
   for (int p = 0; p < kRows / 2; ++p) {
     const int r = row_of(p);

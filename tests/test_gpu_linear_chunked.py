@@ -151,6 +151,17 @@ def test_states():
     assert run(make(lens), want_final=False)[1] is None
 
 
+@pytest.mark.parametrize("recurrent", [False, True])
+@pytest.mark.parametrize("lens", [[1300], [1025, 0, 1, 700, 1537]])
+def test_states_in_place_of_cut_sequences(lens, recurrent):
+    """The last segment's final state takes the initial state's place, which the first segment reads:
+    with many heads, so that segments of one sequence run at different times."""
+    c = make(lens, H=24, H_k=1, d_k=32, d_v=32, decay=0.01, seed=6)
+    want = run({**c, "init_state": c["init_state"].clone()}, out_dtype=F32, recurrent=recurrent, final_state=None)
+    got = run(c, out_dtype=F32, recurrent=recurrent, final_state=c["init_state"])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_forgetting_and_nan():
     lens = [300]
     c = make(lens, H=2, seed=3)
