@@ -99,15 +99,37 @@ struct LinearArgs {
   LinearPlan plan;
 };
 
+// The passes of a segmented call are launched so that one may begin while the one before it drains: a
+// kernel lets its successor begin once all its CTAs run, and a thread that reads what an earlier pass
+// wrote waits for that pass to have ended. Pass 3 only does so for segments that enter with the
+// workspace's states; sequences that are not cut, and first segments, run beside passes 1 and 2.
+// Every CTA waits before it ends, so that a pass never ends before an earlier one.
+__device__ __forceinline__ void let_next_pass_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_earlier_passes() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_pass_kernel(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, bool overlap,
+                               cudaStream_t stream, const A &...args) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = grid, c.blockDim = dim3(threads), c.dynamicSmemBytes = smem, c.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &attr, c.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kern, args...);
+}
+
 // A cut sequence's first segment enters with the initial state; where the final one takes its place,
 // pass 2 leaves a copy in the workspace, because the last segment may end before the first begins.
 __host__ __device__ __forceinline__ bool linear_in_place(const LinearArgs &a) {
   return a.init_state != nullptr && a.init_state == a.final_state;
 }
-// The state that a segment enters with, or null (zeros), in pass 3.
+// The state that a segment enters with, or null (zeros), in pass 3. Waits for it.
 __device__ __forceinline__ const float *linear_entering(const LinearArgs &a, const LinearSlot &s, int h) {
   const int64_t dd = int64_t(a.d_k) * a.d_v;
-  if (!s.first || (!s.last && linear_in_place(a))) return a.seg_states + (s.place * a.H + h) * dd;
+  if (!s.first || (!s.last && linear_in_place(a))) {
+    wait_for_earlier_passes();
+    return a.seg_states + (s.place * a.H + h) * dd;
+  }
   return a.init_state != nullptr ? a.init_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
 }
 

@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
   }
+  if constexpr (kStateOnly) let_next_pass_begin();
   LinearSlot s;
   if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, blockIdx.x / a.H, s)) return;
   const int len = int(s.t1 - s.t0), chunks = (len + kC - 1) / kC;
@@ -716,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
     tmem_dealloc(tmem, 512);
   }
+  if constexpr (!kStateOnly) wait_for_earlier_passes();
 }
 
 template <int kDV, bool kOutBF16, bool kStateOnly>
@@ -738,8 +740,8 @@ cudaError_t launch_one(const CUtensorMap &mq, const CUtensorMap &mk, const CUten
   }
   const unsigned pieces = unsigned(a.plan.inner) + (kStateOnly ? 0u : unsigned(a.num_seqs));
   const dim3 grid(pieces * unsigned(a.H), unsigned((a.d_v + kDV - 1) / kDV));
-  kern<<<grid, kThreads, smem, stream>>>(mq, mk, mv, a, device_error_word());
-  return cudaGetLastError();
+  return launch_pass_kernel(kern, grid, kThreads, smem, !kStateOnly && a.plan.seg_len != 0, stream, mq, mk, mv, a,
+                            device_error_word());
 }
 
 }  // namespace

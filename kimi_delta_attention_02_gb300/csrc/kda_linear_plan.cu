@@ -10,44 +10,46 @@ int up8(int x) { return (x + 7) & ~7; }
 
 // Pass 2: a segment's end state from zero, B_j, gives way to its successor's entering state in the
 // successor's place, E_0 = initial state (read where it is), E_{j+1} = e^{D_j} E_j + B_j. The CTAs of
-// a sequence's first segment walk its segments, kVec entries per thread, the next segments' entries on
-// their way meanwhile.
+// a sequence's first segment (blockIdx.y is the piece) walk its segments, kVec entries per thread, the
+// next segments' entries on their way meanwhile.
 template <int kVec>
 __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a) {
-  const int h = blockIdx.x % a.H;
+  let_next_pass_begin();
   LinearSlot s;
-  if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, blockIdx.x / a.H, s) || !s.first) return;
+  const bool some = linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, blockIdx.y, s) && s.first;
+  wait_for_earlier_passes();
+  if (!some) return;
   const int segs = (a.cu[s.n + 1] - a.cu[s.n] + a.plan.seg_len - 1) / a.plan.seg_len;
-  const int64_t dd = int64_t(a.d_k) * a.d_v;
-  const int64_t e = (int64_t(blockIdx.y) * blockDim.x + threadIdx.x) * kVec;
-  if (e >= dd) return;
+  const int64_t dd = int64_t(a.d_k) * a.d_v, step = int64_t(a.H) * dd;
   struct alignas(4 * kVec) Vec {
     float v[kVec];
   };
-  const int64_t step = int64_t(a.H) * dd;
-  float *p = a.seg_states + (s.place * a.H + h) * dd + e;
-  const float *d = a.seg_decay + s.place * a.H + h;
-  auto read = [&](int j) { return *reinterpret_cast<const Vec *>(p + j * step); };
-  Vec S = {};
-  if (a.init_state != nullptr) S = *reinterpret_cast<const Vec *>(a.init_state + (int64_t(s.n) * a.H + h) * dd + e);
-  constexpr int kAhead = 4;
-  Vec b[kAhead] = {};
-  float D[kAhead] = {};
+  for (int64_t e = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) * kVec; e < step;
+       e += int64_t(gridDim.x) * blockDim.x * kVec) {
+    float *p = a.seg_states + s.place * step + e;
+    const float *d = a.seg_decay + s.place * a.H + e / dd;
+    auto read = [&](int j) { return *reinterpret_cast<const Vec *>(p + j * step); };
+    Vec S = {};
+    if (a.init_state != nullptr) S = *reinterpret_cast<const Vec *>(a.init_state + s.n * step + e);
+    constexpr int kAhead = 4;
+    Vec b[kAhead] = {};
+    float D[kAhead] = {};
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (i + 1 < segs) b[i] = read(i), D[i] = d[i * a.H];
-  if (linear_in_place(a)) *reinterpret_cast<Vec *>(p) = S;  // B_0 has been read
-  for (int j0 = 0; j0 + 1 < segs; j0 += kAhead) {
+    for (int i = 0; i < kAhead; ++i)
+      if (i + 1 < segs) b[i] = read(i), D[i] = d[i * a.H];
+    if (linear_in_place(a)) *reinterpret_cast<Vec *>(p) = S;  // B_0 has been read
+    for (int j0 = 0; j0 + 1 < segs; j0 += kAhead) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i;
-      if (j + 1 >= segs) break;
-      const float em1 = expm1f(D[i]);
+      for (int i = 0; i < kAhead; ++i) {
+        const int j = j0 + i;
+        if (j + 1 >= segs) break;
+        const float em1 = expm1f(D[i]);
 #pragma unroll
-      for (int v = 0; v < kVec; ++v) S.v[v] = decay_step(S.v[v], em1) + b[i].v[v];
-      if (j + kAhead + 1 < segs) b[i] = read(j + kAhead), D[i] = d[(j + kAhead) * a.H];
-      // B_{j+1} of this place, if there is one, was read above (kAhead >= 2)
-      *reinterpret_cast<Vec *>(p + (j + 1) * step) = S;
+        for (int v = 0; v < kVec; ++v) S.v[v] = decay_step(S.v[v], em1) + b[i].v[v];
+        if (j + kAhead + 1 < segs) b[i] = read(j + kAhead), D[i] = d[(j + kAhead) * a.H];
+        // B_{j+1} of this place, if there is one, was read above (kAhead >= 2)
+        *reinterpret_cast<Vec *>(p + (j + 1) * step) = S;
+      }
     }
   }
 }
@@ -119,10 +121,11 @@ cudaError_t launch_pad(const PadArgs &a, cudaStream_t stream) {
 cudaError_t launch_linear_scan(const LinearArgs &a, cudaStream_t stream) {
   const int64_t dd = int64_t(a.d_k) * a.d_v;
   const int vec = dd % 4 == 0 ? 4 : 1;  // states start on 16-byte boundaries
-  const dim3 grid(unsigned(a.plan.inner) * unsigned(a.H), unsigned((dd + 256 * vec - 1) / (256 * vec)));
-  if (vec == 4) linear_scan_kernel<4><<<grid, 256, 0, stream>>>(a);
-  else linear_scan_kernel<1><<<grid, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  // one wave of CTAs (8 per SM) for all pieces, because most may be idle: 64 short prompts, of which none is
+  // cut, take 108 us with one wave, 110 with four
+  const int64_t need = (a.H * dd + 256 * vec - 1) / (256 * vec), fit = 8 * kLinearSMs / a.plan.inner;
+  const dim3 grid(unsigned(need < fit ? need : fit > 1 ? fit : 1), unsigned(a.plan.inner));
+  return launch_pass_kernel(vec == 4 ? linear_scan_kernel<4> : linear_scan_kernel<1>, grid, 256, 0, true, stream, a);
 }
 
 cudaError_t launch_linear_pad(LinearArgs &a, cudaStream_t stream) {
