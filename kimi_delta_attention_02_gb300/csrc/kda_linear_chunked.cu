@@ -54,7 +54,7 @@ struct Cfg {
   static constexpr bool kPair = !kOutBF16 && !kStateOnly;  // P and S as hi + lo
   static constexpr int kBufs = kStateOnly ? 4 : 5;         // pass 1: K V K V
   static constexpr uint32_t kTileV = 256u * kDV;
-  static constexpr uint32_t kTileS = kStateOnly ? 0 : 256u * kDV;   // 128 key rows x kDV bf16
+  static constexpr uint32_t kTileS = 256u * kDV;                    // 128 key rows x kDV bf16; stages states too
   static constexpr uint32_t kTileVP = 64u * kDV;                    // a quarter of V': 32 tokens
   static constexpr uint32_t oS = kBufs * kBuf, oVP = oS + (kPair ? 2 : 1) * kTileS, oTab = oVP + 4 * kTileVP;
 };
@@ -116,29 +116,56 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   return r;
 }
 
-// 8 floats of a state's row: 32 bytes in one access where they are aligned to that (the load/store pipe
-// takes a row per thread either way)
-__device__ __forceinline__ void load_8(const float *p, float *v) {
-  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
-    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
-                 : "l"(p)
-                 : "memory");
-  } else {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// A warp's part of a state, 32 rows of kCols columns with one row per lane in registers, from or to
+// global memory (row stride d_v, the first `rows` rows and `cols` columns) through 64 kCols bytes of
+// shared memory, half of the columns at a time, so that global memory sees whole lines: a row per
+// thread costs the load/store pipe three cycles for every 32 bytes (64 prompts of 40 to 250 tokens: NNN us
+// so, NNN us through shared memory).
+template <int kCols>
+struct StateRows {
+  static constexpr int kR = kCols / 2, kPer = kR / 4, kStep = 32 / kPer;  // columns, float4 per row, rows per access
+  static __device__ __forceinline__ int slot(int row, int j) { return row * kPer + (j ^ ((kPer == 8 ? row : row >> 1) & (kPer - 1))); }
+  static __device__ __forceinline__ void load(const float *src, int d_v, int rows, int cols, float4 *stage, float *S) {
+    const int lane = threadIdx.x & 31, row0 = lane / kPer, j = lane % kPer;
+    float4 x[2][kPer];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int row = row0 + i * kStep, c = h * kR + 4 * j;
+        x[h][i] = row < rows && c < cols ? *reinterpret_cast<const float4 *>(src + int64_t(row) * d_v + c)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) stage[slot(row0 + i * kStep, j)] = x[h][i];
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float4 v = stage[slot(lane, i)];
+        S[h * kR + 4 * i] = v.x, S[h * kR + 4 * i + 1] = v.y, S[h * kR + 4 * i + 2] = v.z, S[h * kR + 4 * i + 3] = v.w;
+      }
+    }
   }
-}
-__device__ __forceinline__ void store_8(float *p, const float *v) {
-  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  static __device__ __forceinline__ void store(float *dst, int d_v, int rows, int cols, float4 *stage, const float *S) {
+    const int lane = threadIdx.x & 31, row0 = lane / kPer, j = lane % kPer;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        stage[slot(lane, i)] = make_float4(S[h * kR + 4 * i], S[h * kR + 4 * i + 1], S[h * kR + 4 * i + 2], S[h * kR + 4 * i + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int row = row0 + i * kStep, c = h * kR + 4 * j;
+        if (row < rows && c < cols) *reinterpret_cast<float4 *>(dst + int64_t(row) * d_v + c) = stage[slot(row, j)];
+      }
+    }
   }
-}
+};
 
 // An MMA warp runs as a whole, so that descriptors stay in uniform registers (a lone lane has to
 // move each one there), and its elected lane alone issues.
@@ -586,16 +613,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cb = half * kHalf;  // first column within the tile
     const int64_t dd = int64_t(a.d_k) * a.d_v;
     float S[kHalf];
-    {
-      const float *src = kStateOnly ? nullptr : linear_entering(a, s, h);
+    float4 *const stage = reinterpret_cast<float4 *>(smem + F::oS + (warp - 12) * (F::kTileS / 8));
+    const int64_t part = int64_t(32 * w) * a.d_v + col0 + cb;  // this warp's part of a state
+    const int rows = a.d_k - 32 * w, width = a.d_v - col0 - cb;
+    const float *src = kStateOnly ? nullptr : linear_entering(a, s, h);
+    if (src != nullptr) {
+      StateRows<kHalf>::load(src + part, a.d_v, rows, width, stage, S);
+    } else {
 #pragma unroll
-      for (int c = 0; c < kHalf; c += 8) {  // d_v is a multiple of 8
-        const int col = col0 + cb + c;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) S[c + e] = 0.f;
-        if (src != nullptr && r < a.d_k && col < a.d_v) load_8(src + int64_t(r) * a.d_v + col, S + c);
-      }
+      for (int c = 0; c < kHalf; ++c) S[c] = 0.f;
     }
+    // the tile takes the place of what all eight warps have staged
+    if (!kStateOnly) named_bar_sync(1, 256);
     const uint32_t state_off = sw128_chunk(r, 0, cb >> 6, 128);
     auto write_state_tile = [&]() {  // the B operand of Q S: rows k, MN-major
 #pragma unroll
@@ -618,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->s_full);
     };
-    if constexpr (!kStateOnly) write_state_tile();
+    if (!kStateOnly && chunks > 0) write_state_tile();
     // rows of the output that start on 32-byte boundaries take 32-byte stores
     const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | (uint32_t(a.d_v) * (kOutBF16 ? 2 : 4))) & 31) == 0;
 #pragma unroll 1
@@ -702,13 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     float *dst = kStateOnly ? a.seg_states + (s.place * a.H + h) * dd
                  : (s.last && a.final_state != nullptr) ? a.final_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
-    if (dst != nullptr && r < a.d_k) {
-#pragma unroll
-      for (int c = 0; c < kHalf; c += 8) {
-        const int col = col0 + cb + c;
-        if (col < a.d_v) store_8(dst + int64_t(r) * a.d_v + col, S + c);
-      }
-    }
+    // (P V of the last chunk is done, and Q S before it, so nobody reads the tile)
+    if (dst != nullptr) StateRows<kHalf>::store(dst + part, a.d_v, rows, width, stage, S);
   }
   __syncwarp();
   tc_fence_before();
