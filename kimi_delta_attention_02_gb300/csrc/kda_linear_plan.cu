@@ -171,15 +171,17 @@ cudaError_t launch_linear_unpad(const LinearArgs &a, bool out_bf16, void *out, f
 // A chunk costs the tensor-core kernel the same however few tokens it holds, the token-recurrent one
 // goes by tokens, so the mean length decides. Microseconds, tensor cores / token-recurrent, at
 // sequences of 4, 16, 32 and 64 tokens:
-//   16 of 16 heads of 128   29/31   27/39   29/58   39/123     128 of them  154/107  166/156  170/246  180/426
-//   16 of 64 heads of 64    49/31   51/43   51/68   61/117     128 of them  322/121  348/191  348/336  354/623
-//   16 of 64 heads of 100   128/57  133/84  139/131 168/223    128 of them  913/369  975/563  1024/856 1137/1554
+//   16 of 64 heads of 128, bf16 out   72/58   72/85   72/126  85/210    128 of them  505/351 505/524 505/824  511/1504
+//   the same, fp32 out                   -   104/85  103/126 120/210                    -   763/527 761/826  792/1512
+//   16 of 64 heads of 64                 -    51/32   51/47   58/73                     -   335/155 337/247  345/433
+//   16 of 64 heads of 100 (padded)       -   133/85  126/126 166/210                    -   975/546 822/824 1098/1502
+//   16 of 64 heads of 53 (padded)        -      -       -     96/73                     -      -       -     588/429
 LinearPlan linear_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool out_bf16,
                        bool recurrent, size_t workspace_bytes) {
   LinearPlan p;
   // TMA addresses rows of a multiple of 16 bytes; other head sizes are padded into the workspace
   const bool odd = d_k % 8 != 0 || d_v % 8 != 0, wide = out_bf16 && d_v > 64;
-  const int64_t least = odd ? 40 : wide ? 16 : 32;
+  const int64_t least = (d_k <= 64 && d_v <= 64 ? 48 : wide && d_k > 64 ? 16 : 24) * (odd ? 2 : 1);
   p.tensor = in_bf16 && !recurrent && total >= least * num_seqs;
   const bool pad = p.tensor && odd;
   size_t at = 0;

@@ -9,6 +9,8 @@
 // through shared memory 16 tokens at a time (fp32), the next 16 waiting in registers. Two rows
 // go through one packed fp32 instruction: 3 per row pair, column and token (decay, write,
 // read-out), which bound the kernel.
+#include <type_traits>
+
 #include "kda_linear.cuh"
 
 namespace kda {
@@ -52,20 +54,28 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
   }
 
   // global -> registers -> shared memory, a stage of kTok tokens at a time
-  float rk[kTok], rq[kTok], rv[kTok * kCols / kThr], rg_ = 0.f;
+  // (as stored: a conversion here would wait for the load)
+  using Elem = std::conditional_t<kInBF16, uint16_t, float>;
+  auto raw = [](const void *p, int64_t at) { return static_cast<const Elem *>(p)[at]; };
+  auto value = [](Elem x) {
+    if constexpr (kInBF16) return bf16_to_f32(x);
+    else return x;
+  };
+  Elem rk[kTok], rq[kTok], rv[kTok * kCols / kThr];
+  float rg_ = 0.f;
   auto fetch = [&](int64_t t) {  // tokens t .. t + kTok - 1; zeros past the segment
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
       const bool ok = t + i < s.t1 && tid < a.d_k;
       const int64_t at = ((t + i) * a.H_k + hk) * a.d_k + tid;
-      rk[i] = ok ? load_elem<kInBF16>(a.k, at) : 0.f;
-      if constexpr (!kStateOnly) rq[i] = ok ? load_elem<kInBF16>(a.q, at) : 0.f;
+      rk[i] = ok ? raw(a.k, at) : Elem(0);
+      if constexpr (!kStateOnly) rq[i] = ok ? raw(a.q, at) : Elem(0);
     }
 #pragma unroll
     for (int i = 0; i < kTok * kCols / kThr; ++i) {
       const int64_t tt = t + 2 * i + (tid >> 6);
       const int c = col0 + (tid & 63);
-      rv[i] = tt < s.t1 && c < a.d_v ? load_elem<kInBF16>(a.v, (tt * a.H + h) * a.d_v + c) : 0.f;
+      rv[i] = tt < s.t1 && c < a.d_v ? raw(a.v, (tt * a.H + h) * a.d_v + c) : Elem(0);
     }
     if (tid < kTok) rg_ = t + tid < s.t1 ? a.log_decay[a.per_token ? (t + tid) * a.H + h : h] : 0.f;
   };
@@ -73,12 +83,12 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
     if (tid < 4 * kRows) {
 #pragma unroll
       for (int i = 0; i < kTok; ++i) {
-        s_k[b][i][tid] = rk[i];
-        if constexpr (!kStateOnly) s_q[b][i][tid] = rq[i];
+        s_k[b][i][tid] = value(rk[i]);
+        if constexpr (!kStateOnly) s_q[b][i][tid] = value(rq[i]);
       }
     }
 #pragma unroll
-    for (int i = 0; i < kTok * kCols / kThr; ++i) s_v[b][2 * i + (tid >> 6)][tid & 63] = rv[i];
+    for (int i = 0; i < kTok * kCols / kThr; ++i) s_v[b][2 * i + (tid >> 6)][tid & 63] = value(rv[i]);
     if (tid < kTok) {
       s_e[b][tid] = expm1f(rg_);
       if constexpr (kStateOnly) s_g[b][tid] = rg_;

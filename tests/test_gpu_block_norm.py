@@ -59,6 +59,14 @@ def test_many_rows(rows, D):
     _check(_make(rows, D))
 
 
+@pytest.mark.parametrize("rows", [1, 2, 3, 33, 6000])
+@pytest.mark.parametrize("D", [1, 9, 63, 64, 65, 120, 127, 128, 129])
+def test_several_rows_per_warp(rows, D):
+    """8, 16 and 32 lanes a row; rows past the last one in a warp, more rows than one pass takes."""
+    _check(_make(rows, D, x=B16))
+    _check(_make(rows, D, y=F32, gate="row"), out_dtype=F32)
+
+
 @pytest.mark.parametrize("x", [F32, B16])
 @pytest.mark.parametrize("y", [F32, B16])
 @pytest.mark.parametrize("out", [F32, B16])

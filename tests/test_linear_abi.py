@@ -173,12 +173,13 @@ def test_workspace_query():
                  (1000, 7, 2, 1, 100, 72, 0, 0, 0), (50, 1, 4, 2, 13, 7, 1, 1, 0)]:
         assert q(*args) == q(*args) and q(*args) % 256 == 0
     assert q(65536, 1, 16, 4, 128, 128, 1, 1, 0) > 0
-    # bf16 head sizes that are no multiple of 8: q and k [64, 2, 16], v and out [64, 4, 8], the states
-    # [1, 4, 13, 8] in fp32, each rounded up to 256 bytes; nothing for the token-recurrent kernel
-    assert q(64, 1, 4, 2, 13, 7, 1, 1, 0) == 2 * 4096 + 2 * 4096 + 1792
-    assert q(64, 1, 4, 2, 13, 7, 1, 0, 0) == 2 * 4096 + 4096 + 8192 + 1792
-    assert q(64, 1, 4, 2, 13, 8, 1, 1, 0) == 2 * 4096 and q(64, 1, 4, 2, 16, 7, 1, 1, 0) == 2 * 4096 + 2048
-    assert q(48, 1, 4, 2, 13, 7, 1, 1, 1) == 0 and q(48, 1, 4, 2, 13, 7, 0, 0, 0) == 0
+    # bf16 head sizes that are no multiple of 8: q and k [128, 2, 16], v and out [128, 4, 8], the states
+    # [1, 4, 13, 8] in fp32, each rounded up to 256 bytes; nothing for
+    # the token-recurrent kernel, which also runs short sequences
+    assert q(128, 1, 4, 2, 13, 7, 1, 1, 0) == 2 * 8192 + 2 * 8192 + 1792
+    assert q(128, 1, 4, 2, 13, 7, 1, 0, 0) == 2 * 8192 + 8192 + 16384 + 1792
+    assert q(128, 1, 4, 2, 13, 8, 1, 1, 0) == 2 * 8192 and q(128, 1, 4, 2, 16, 7, 1, 1, 0) == 2 * 8192 + 2048
+    assert q(48, 1, 4, 2, 13, 7, 1, 1, 0) == q(48, 1, 4, 2, 13, 7, 1, 1, 1) == q(48, 1, 4, 2, 13, 7, 0, 0, 0) == 0
     # invalid or empty sizes ask for nothing
     for args in [(0, 1, 1, 1, 64, 64, 1, 1, 0), (10, 0, 1, 1, 64, 64, 1, 1, 0), (10, 1, 0, 1, 64, 64, 1, 1, 0),
                  (10, 1, 1, 1, 129, 64, 1, 1, 0), (10, 1, 1, 1, 64, 64, 3, 1, 0), (-5, 1, 1, 1, 64, 64, 1, 1, 0),
