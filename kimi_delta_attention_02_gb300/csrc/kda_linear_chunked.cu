@@ -16,14 +16,18 @@
 // s_j from behind j to its block's end, t_B a whole block's (log2 units). Then e^{G_i - G_j} is
 // 2^{a_i - a_j} within a block and 2^{a_i + t_{J+1} + ... + t_{I-1}} 2^{s_j} across: no factor is
 // the difference of two long sums, none exceeds one while g <= 0, and only the diagonal blocks
-// take an exponential per entry. A decay below 2^-127 per token counts as 2^-127, which leaves
-// nothing in fp32 either, so g = -infinity needs no case of its own.
+// take an exponential per entry, of a difference of two sums: off by at most 256 x 2^-24 x ln 2 <
+// 2^-16 while a block's 32 tokens decay by 2^-256 or less. In a block that decays by more every entry
+// takes its own sum if the output is fp32; a bf16 output bears the difference (sums up to 32 x 127,
+// off by at most 2^-10.5 next to P's 2^-8; without the branch the loop is 4 % faster). A decay below
+// 2^-127 per token counts as 2^-127, which leaves nothing in fp32 either, so g = -infinity needs no
+// case of its own.
 //
 // Shared memory holds five 32 KB buffers that the chunks' tiles take in turn, Q V K Q V K ..., so that
 // a tile waits for the one five places before it: Q of chunk n for V of n - 2, V for K of n - 2, K for
-// Q of n - 1. The output needs
-// no buffer: it goes from tensor memory through registers to global memory, 32 bytes (a whole
-// sector) per thread and store.
+// Q of n - 1. The output needs no buffer: it goes from tensor memory through registers to global
+// memory, 32 bytes (a whole sector) per thread and store. The states come and go through the place of
+// their own bf16 tile.
 //
 // Pass 1 of a segmented call (kStateOnly) forms a segment's end state from zero, sum over its chunks of
 // e^(decay behind the chunk) K^T V', last chunk first: once that factor is below 2^-127, and so zero in
@@ -35,6 +39,12 @@
 // V to V' in quarters of 32 tokens, 12-19 keep the state (one key row and half the columns per
 // thread) and write the output (one token and half the columns). Per chunk the tensor pipe runs
 // Q K^T, K^T V' (hi, lo), P V, Q S: 2560 cycles for 128 value columns; everything else runs beside.
+//
+// Measured (bf16, d = 128): T = 4096, 96 heads 112 us (3.7 TB/s, 56 % of the HBM copy rate, on the 96
+// SMs that have a chain; tensor pipe 62 % busy there); T = 65536, 16 heads 310 us (3.5 TB/s); 64 prompts
+// of 40 to 250 tokens, 16 heads 96 us. What bounds a chunk is the way from one state to the next (D to
+// registers, the bf16 tile, Q S, P V, the output), 3.4 us, against 1.3 us of MMAs and 1.9 us of HBM
+// traffic with 96 SMs at it.
 #include <atomic>
 
 #include "kda_linear.cuh"
@@ -48,6 +58,7 @@ constexpr int kThreads = 640;
 constexpr uint32_t kBuf = 32768;   // 128 tokens x 128 channels bf16, two 64-channel blocks
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMinLog2 = -127.f;
+constexpr float kFarLog2 = -256.f;  // of a block's 32 tokens
 
 template <int kDV, bool kOutBF16, bool kStateOnly>
 struct Cfg {
@@ -166,6 +177,12 @@ struct StateRows {
     }
   }
 };
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float *v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
 
 // An MMA warp runs as a whole, so that descriptors stay in uniform registers (a lone lane has to
 // move each one there), and its elected lane alone issues.
@@ -510,7 +527,38 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           put(J, p);
         }
-        {  // the row's own block; selected away, not multiplied: what lies above may be infinite
+        if (kPair && tb.block(w) < kFarLog2) {
+          // long sums, whose differences would lose what lies behind a token that forgets: each entry
+          // takes the sum of its own, of the tokens from behind its column to the row
+          const int i = n * kC + 32 * w + lane;
+          float g = i < len ? a.log_decay[a.per_token ? (s.t0 + i) * a.H + h : h] * kLog2e : 0.f;
+          g = g < kMinLog2 ? kMinLog2 : g;
+#pragma unroll 1
+          for (int j0 = 0; j0 < 32; j0 += 16) {
+            float sum = 0.f, x[16], hi[8], lo[8];
+#pragma unroll 1
+            for (int j = 31; j >= j0 + 16; --j) {
+              const float next = __shfl_sync(0xffffffffu, g, j);
+              if (j <= lane) sum += next;
+            }
+            tmem_ld16_wait(tQK + row + 32 * w + j0, x);
+#pragma unroll
+            for (int j = 15; j >= 0; --j) {
+              x[j] = j0 + j <= lane ? x[j] * ex2(sum) : 0.f;
+              const float next = __shfl_sync(0xffffffffu, g, j0 + j);
+              if (j0 + j <= lane) sum += next;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t u = pack_bf16x2(x[2 * j], x[2 * j + 1]);
+              const float2 b = unpack_bf16x2(u);
+              hi[j] = __uint_as_float(u);
+              lo[j] = __uint_as_float(pack_bf16x2(x[2 * j] - b.x, x[2 * j + 1] - b.y));
+            }
+            tmem_st8(tQK + row + 16 * w + j0 / 2, hi);
+            tmem_st8(tPL + row + 16 * w + j0 / 2, lo);
+          }
+        } else {  // the row's own block; selected away, not multiplied: what lies above may be infinite
           float2 p[16];
           get(w, p);
 #pragma unroll

@@ -1,14 +1,16 @@
 // kda_linear_recurrent.cu -- linear attention with one decay per head, a token at a time, in fp32
 // on the CUDA cores: S = e^{g_t} S + k_t v_t^T, o_t = scale S^T q_t. It takes every size and both
-// dtypes (fp32 inputs, head sizes that TMA cannot address, short sequences); the tensor-core
-// kernel is the fast path of long bf16 sequences.
+// dtypes (fp32 inputs, short sequences, bf16 head sizes that lack the workspace to be padded); the
+// tensor-core kernel is the fast path of long bf16 sequences.
 //
 // A CTA of 128 threads holds 64 value columns of one segment's state in registers: lane
 // (pair, rg) of warp w owns columns 16 w + 2 pair, + 1 and the key rows 16 j + 4 rg + 0..3, so a
 // row sum ends with two shuffles inside a warp and the tokens need no CTA barrier. q, k, v pass
 // through shared memory 16 tokens at a time (fp32), the next 16 waiting in registers. Two rows
 // go through one packed fp32 instruction: 3 per row pair, column and token (decay, write,
-// read-out), which bound the kernel.
+// read-out), which bound the kernel where it fills the SMs; with few heads the chain of tokens does,
+// 0.35 us each (prompts of 700 and 333 tokens, 6 heads of 100 x 72 in fp32: 45 us in segments; 2048
+// sequences of 4 tokens and 64 heads of 64, bf16: 103 us, 2.6 TB/s of states).
 #include <type_traits>
 
 #include "kda_linear.cuh"

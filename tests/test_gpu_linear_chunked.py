@@ -20,7 +20,10 @@ B16, F32 = torch.bfloat16, torch.float32
 
 
 def _check(c, lens, scale=1.0, out_dtype=B16, **kw):
-    out, fin = run(c, scale=scale, out_dtype=out_dtype, **kw)
+    return _check_against(c, lens, out_dtype, *run(c, scale=scale, out_dtype=out_dtype, **kw), scale=scale)
+
+
+def _check_against(c, lens, out_dtype, out, fin, scale=1.0):
     o, f, mo, mf = reference(c, scale)
     fine = 2.0 ** -15 + fp32_factor(128 + max(lens) // 64, c["q"].shape[2])
     if out_dtype == B16:
@@ -151,6 +154,42 @@ def test_states():
     assert run(make(lens), want_final=False)[1] is None
 
 
+@pytest.mark.parametrize("H,d_v,out_dtype", [(77, 16, B16), (96, 16, F32), (120, 24, B16), (48, 72, F32), (96, 72, B16)])
+@pytest.mark.parametrize("init", [True, False])
+def test_one_sequence_on_many_heads(H, d_v, out_dtype, init):
+    """About as many chains as SMs, kept whole or cut in few segments; heads that forget everything."""
+    lens = [2500]
+    c = make(lens, H=H, H_k=1, d_k=16, d_v=d_v, decay=0.01, init=init, seed=H)
+    _check(c, lens, out_dtype=out_dtype)
+    c["log_decay"][300:1400, ::3] = -float("inf")
+    c["log_decay"][:, 1::3] = -0.2  # pass 1 stops early
+    out, fin = _check(c, lens, out_dtype=out_dtype)
+    again = run(c, out_dtype=out_dtype)
+    assert torch.equal(out, again[0]) and torch.equal(fin, again[1])
+    if init:  # in place
+        state = c["init_state"].clone()
+        _check_against(c, lens, out_dtype, *run({**c, "init_state": state}, out_dtype=out_dtype, final_state=state))
+
+
+@pytest.mark.parametrize("end", [2500, 2049, 900, 130, 0])
+@pytest.mark.parametrize("H", [8, 96])
+def test_a_sequence_shorter_than_the_rows(end, H):
+    """The sequence may end before the rows do, also inside the first of the planned segments."""
+    lens = [2500]
+    c = make(lens, H=H, H_k=2, d_k=16, d_v=16, decay=0.01, seed=2)
+    c["cu_seqlens"] = torch.tensor([0, end], dtype=torch.int32, device="cuda")
+    short = {n: t[:end] if n in ("q", "k", "v", "log_decay") else t for n, t in c.items()}
+    for n in ("q", "k", "v"):
+        c[n][end:] = float("nan")
+    out = torch.full((2500, H, 16), 7.0, device="cuda")
+    _, fin = run(c, out=out)
+    assert (out[end:] == 7.0).all()
+    o, f, mo, mf = reference(short)
+    fine = 2.0 ** -15 + fp32_factor(128 + 40, 16)
+    check(out[:end], o, mo, fine, "out")
+    check(fin, f, mf, fine, "final")
+
+
 @pytest.mark.parametrize("recurrent", [False, True])
 @pytest.mark.parametrize("lens", [[1300], [1025, 0, 1, 700, 1537]])
 def test_states_in_place_of_cut_sequences(lens, recurrent):
@@ -173,6 +212,17 @@ def test_forgetting_and_nan():
     nan = torch.isnan(out)
     assert nan[150:, 1].all() and not nan[:150].any() and not nan[:, 0].any()
     assert torch.isnan(fin[0, 1]).all() and not torch.isnan(fin[0, 0]).any()
+
+
+@pytest.mark.parametrize("decay", [-float("inf"), -90.0, -12.0])
+def test_accuracy_behind_many_forgetting_tokens(decay):
+    """Runs of tokens that forget all or most, which end inside a block: what follows is as exact as ever."""
+    lens = [500]
+    c = make(lens, H=3, seed=17)
+    c["log_decay"][10:60, 0] = decay
+    c["log_decay"][64:95, 1] = decay
+    c["log_decay"][130:447:2, 2] = decay
+    _check(c, lens, out_dtype=F32)
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
