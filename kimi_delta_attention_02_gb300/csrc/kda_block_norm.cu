@@ -12,6 +12,10 @@
 //    copies, two rows ahead (one when three do not fit);
 //  * other rows of up to 8192 channels are loaded into registers one row ahead;
 //  * longer rows take four pieces per thread, one row per CTA, weights from L1.
+//
+// Measured: 4096 x 7168, fp32 stream, bf16 blocks with a gate per channel 65 us (6.4 TB/s, 95 % of the
+// HBM copy rate; without shared memory 137 us); 16384 x 776 of the same 48 us, x 777 60 us (rows that
+// start anywhere: 4-byte and 2-byte accesses); 8192 x 5000 in bf16 93 us; one row 7 us.
 #include <atomic>
 
 #include "kda_block_norm.h"

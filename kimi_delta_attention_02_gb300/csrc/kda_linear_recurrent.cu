@@ -9,7 +9,7 @@
 // through shared memory 16 tokens at a time (fp32), the next 16 waiting in registers. Two rows
 // go through one packed fp32 instruction: 3 per row pair, column and token (decay, write,
 // read-out), which bound the kernel where it fills the SMs; with few heads the chain of tokens does,
-// 0.35 us each (prompts of 700 and 333 tokens, 6 heads of 100 x 72 in fp32: 45 us in segments; 2048
+// 0.35 us each (prompts of 700 and 333 tokens, 6 heads of 100 x 72 in fp32: 45 us in segments; 128
 // sequences of 4 tokens and 64 heads of 64, bf16: 103 us, 2.6 TB/s of states).
 #include <type_traits>
 
