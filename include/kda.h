@@ -383,7 +383,8 @@ kda_status kda_prologue(const void *q_raw, const void *k_raw, const void *v_raw,
  *   log_decay    g, fp32: [total_tokens, H] (decode: [B, H]) with decay_per_token = 1, or one
  *                constant per head [H] with decay_per_token = 0. Any value up to 0 including
  *                -infinity (the state is forgotten); a positive g grows the state and is computed
- *                while e^g and the state stay finite. NaN propagates. No clamp is applied.
+ *                while e to the sum of the positive ones of 128 tokens stays finite. NaN
+ *                propagates. No clamp is applied.
  *   workspace    (prefill) as in kda_prefill, of kda_linear_prefill_workspace_size() bytes: with
  *                it, sequences longer than a CTA's share of the call are cut into segments that
  *                run side by side, and bf16 head sizes that are no multiple of 8 are padded for

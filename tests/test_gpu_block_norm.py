@@ -129,3 +129,16 @@ def test_empty_and_neighbouring_rows_untouched():
         res = torch.full((8, D), 3.0, device="cuda")
         binding.block_norm(**c, out=out[:3], residual_out=res[:3])
         assert (out[3:] == 3).all() and (res[3:] == 3).all()
+
+
+def test_offsets_past_32_bits():
+    """300001 rows of 7200 channels, and 2400001 of 901: the last row is where it belongs."""
+    for rows, D in ((300001, 7200), (2400001, 901)):
+        x = torch.zeros(rows, D, device="cuda", dtype=B16)
+        y = torch.zeros(rows, D, device="cuda", dtype=B16)
+        x[-1].normal_(), y[-1].normal_()
+        r, h = binding.block_norm(x, y, post_norm=True)
+        r1, h1 = binding.block_norm(x[-1:].clone(), y[-1:].clone(), post_norm=True)
+        assert torch.equal(r[-1:], r1) and torch.equal(h[-1:], h1)
+        assert not r[:-1].any() and not h[:-1].any()
+        del x, y, r, h

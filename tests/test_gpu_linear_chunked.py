@@ -305,3 +305,55 @@ def test_captured_prefill_replays_on_new_inputs_beside_another():
     for (out, fin), (o, f, mo, mf) in zip(results, refs):
         check(out, o, mo, fine, "out")
         check(fin, f, mf, fine, "final")
+
+
+def test_where_a_nan_goes():
+    """One in q stays in its row, one in k reaches its token and later ones, one in v its chunk of 128
+    and later ones."""
+    lens = [300]
+    for name, first, rows in (("q", 150, 1), ("k", 150, 150), ("v", 128, 172)):
+        c = make(lens, H=2, H_k=2, seed=21)
+        good, _ = run(c, out_dtype=F32)
+        c[name][150, 0, 5] = float("nan")
+        out, fin = run(c, out_dtype=F32)
+        nan = torch.isnan(out).any(-1)
+        assert nan[first:first + rows, 0].any() and not nan[:, 1].any()
+        assert not nan[:first].any() and not nan[first + rows:].any()
+        assert nan[150, 0] and torch.equal(out[:first], good[:first]) and torch.equal(out[:, 1], good[:, 1])
+        assert torch.isnan(fin[0, 0]).any() == (name != "q") and not torch.isnan(fin[0, 1]).any()
+
+
+def test_eager_calls_on_two_streams():
+    """Segmented calls that overlap, each with the workspace that its call allocates."""
+    lens = [3000]
+    cases = [make(lens, H=2, decay=0.01, seed=50 + i) for i in range(4)]
+    want = [run(c, out_dtype=F32) for c in cases]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [binding.linear_prefill(**c, out_dtype=F32, stream=streams[i % 2]) for i, c in enumerate(cases)]
+    torch.cuda.synchronize()
+    binding.check_device_error()
+    for (o, f), (wo, wf) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(f, wf)
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+def test_offsets_past_32_bits(recurrent):
+    """140000 tokens x 128 heads x 128 channels: the last sequence is where it belongs."""
+    T, H, tail = 140000, 128, 200
+    g = torch.Generator("cuda").manual_seed(1)
+    q = torch.randn(T, 1, 64, device="cuda", generator=g).to(B16)
+    k = (0.1 * torch.randn(T, 1, 64, device="cuda", generator=g)).to(B16)
+    v = torch.empty(T, H, 128, device="cuda", dtype=B16).normal_(generator=g)
+    ld = -torch.rand(T, H, device="cuda", generator=g)
+    cut = T - tail
+    # sequences of 400 tokens, then the tail: nothing is cut, so a sequence does not depend on its place
+    ends = list(range(0, cut, 400)) + [cut, T]
+    cu = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    out, _ = binding.linear_prefill(q, k, v, ld, cu, out_dtype=B16, want_final=False, workspace=None, recurrent=recurrent)
+    one = torch.tensor([0, tail], dtype=torch.int32, device="cuda")
+    want, _ = binding.linear_prefill(q[cut:].contiguous(), k[cut:].contiguous(), v[cut:].contiguous(),
+                                     ld[cut:].contiguous(), one, out_dtype=B16, want_final=False, workspace=None,
+                                     recurrent=recurrent)
+    binding.check_device_error()
+    assert torch.equal(out[cut:], want)

@@ -111,3 +111,20 @@ def test_captured_step_replays_on_new_inputs():
     check(out, o, mo, fp32_factor(1, 64), "out")
     check(state, f, mf, fp32_factor(1, 64), "state")
     assert cpu(c)["q"].shape == (3, 2, 64)
+
+
+def test_offsets_past_32_bits():
+    """1100 sequences x 128 heads x 128 x 128 states: the last one is where it belongs."""
+    B, H, d = 1100, 128, 128
+    g = torch.Generator("cuda").manual_seed(1)
+    q, k = (torch.randn(B, 1, d, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    v = torch.randn(B, H, d, device="cuda", generator=g).to(torch.bfloat16)
+    ld = -torch.rand(B, H, device="cuda", generator=g)
+    state = torch.zeros(B, H, d, d, device="cuda")
+    state[-1].normal_(generator=g)
+    last = state[-1:].clone()
+    out = binding.linear_decode(q, k, v, ld, state)
+    want = binding.linear_decode(q[-1:].contiguous(), k[-1:].contiguous(), v[-1:].contiguous(), ld[-1:].contiguous(), last)
+    # the one sequence takes narrower tiles, whose read-out sums in another order
+    assert torch.equal(state[-1:], last)
+    assert ((out[-1:] - want).abs() <= 2.0 ** -14 * (q[-1:].float().abs() @ last[0].abs()).transpose(0, 1)).all()

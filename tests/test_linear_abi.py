@@ -183,5 +183,5 @@ def test_workspace_query():
     # invalid or empty sizes ask for nothing
     for args in [(0, 1, 1, 1, 64, 64, 1, 1, 0), (10, 0, 1, 1, 64, 64, 1, 1, 0), (10, 1, 0, 1, 64, 64, 1, 1, 0),
                  (10, 1, 1, 1, 129, 64, 1, 1, 0), (10, 1, 1, 1, 64, 64, 3, 1, 0), (-5, 1, 1, 1, 64, 64, 1, 1, 0),
-                 (10, 1, 4, 3, 64, 64, 1, 1, 0)]:
+                 (10, 1, 4, 3, 64, 64, 1, 1, 0), (2**31 - 1, 1, 2**28, 1, 63, 63, 1, 1, 0)]:
         assert q(*args) == 0
