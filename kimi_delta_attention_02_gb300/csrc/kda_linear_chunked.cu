@@ -40,11 +40,11 @@
 // thread) and write the output (one token and half the columns). Per chunk the tensor pipe runs
 // Q K^T, K^T V' (hi, lo), P V, Q S: 2560 cycles for 128 value columns; everything else runs beside.
 //
-// Measured (bf16, d = 128): T = 4096, 96 heads 112 us (3.7 TB/s, 56 % of the HBM copy rate, on the 96
-// SMs that have a chain; tensor pipe 62 % busy there); T = 65536, 16 heads 310 us (3.5 TB/s); 64 prompts
-// of 40 to 250 tokens, 16 heads 96 us. What bounds a chunk is the way from one state to the next (D to
-// registers, the bf16 tile, Q S, P V, the output), 3.4 us, against 1.3 us of MMAs and 1.9 us of HBM
-// traffic with 96 SMs at it.
+// Measured (bf16, d = 128): T = 4096, 96 heads 110 us (3.8 TB/s, 57 % of the HBM copy rate, on the 96
+// SMs that have a chain; tensor pipe 62 % busy there); T = 65536, 16 heads 289 us (3.7 TB/s); 64 prompts
+// of 40 to 250 tokens, 16 heads 93 us. What bounds a chunk is the way from one state to the next (D to
+// registers, the bf16 tile, Q S, P V, the output), 3.3 us, against 1.3 us of MMAs and 1.9 us of HBM
+// traffic with 96 SMs at it; the output's row-per-thread stores keep the load/store pipe for a third of it.
 #include <atomic>
 
 #include "kda_linear.cuh"
@@ -58,6 +58,7 @@ constexpr int kThreads = 640;
 constexpr uint32_t kBuf = 32768;   // 128 tokens x 128 channels bf16, two 64-channel blocks
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMinLog2 = -127.f;
+constexpr uint32_t kProbes = 2000000;
 constexpr float kFarLog2 = -256.f;  // of a block's 32 tokens
 
 template <int kDV, bool kOutBF16, bool kStateOnly>
@@ -184,6 +185,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const float *v) {
                : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
 // An MMA warp runs as a whole, so that descriptors stay in uniform registers (a lone lane has to
 // move each one there), and its elected lane alone issues.
 __device__ __forceinline__ bool elect_lane() {
@@ -279,7 +285,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     raise_device_error(err_word, code);
     return false;
   };
+  // (T = 65536, 16 heads: 292 us with plain probes on the MMA warps, 310 without, 301 on all warps; a
+  // failing probe takes 1 us, so kProbes are 2 s)
   auto wait_warp = [&](uint64_t &bar, uint32_t parity, uint32_t code) -> bool {
+    if (warp == 1 || warp == 3) {  // the MMA warps: plain probes, shorter code
+      bool ok = false;
+#pragma unroll 1
+      for (uint32_t i = 0; i < kProbes; ++i) {
+        ok = mbar_try_wait(&bar, parity & 1);
+        if (ok || ctl->abort != 0) break;
+      }
+      if (__all_sync(0xffffffffu, ok)) return true;
+      ctl->abort = 1;
+      raise_device_error(err_word, code);
+      return false;
+    }
     return __all_sync(0xffffffffu, wait(bar, parity, code)) != 0;
   };
 
@@ -312,7 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int b = 0; b < 2; ++b) tma_load_3d(smem + at.Q() + b * 16384, &mq, &ctl->q_full[s2], 64 * b, hk, t);
           issued = 3 * n + 2;
-          if (n >= 1 && !wait(ctl->qs_done[s2 ^ 1], (n - 1) >> 1, DEVERR_MMA_TIMEOUT)) break;
+          if (n >= 1) {  // K's place is Q's of chunk n - 1; meanwhile it comes as far as L2
+#pragma unroll
+            for (int b = 0; b < 2; ++b) tma_prefetch_3d(&mk, 64 * b, hk, t);
+            if (!wait(ctl->qs_done[s2 ^ 1], (n - 1) >> 1, DEVERR_MMA_TIMEOUT)) break;
+          }
         }
         mbar_arrive_expect_tx(&ctl->k_full[s2], kBuf);
 #pragma unroll
