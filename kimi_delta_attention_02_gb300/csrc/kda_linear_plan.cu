@@ -121,8 +121,9 @@ cudaError_t launch_pad(const PadArgs &a, cudaStream_t stream) {
 cudaError_t launch_linear_scan(const LinearArgs &a, cudaStream_t stream) {
   const int64_t dd = int64_t(a.d_k) * a.d_v;
   const int vec = dd % 4 == 0 ? 4 : 1;  // states start on 16-byte boundaries
-  // one wave of CTAs (8 per SM) for all pieces, because most may be idle: 64 short prompts, of which none is
-  // cut, take 108 us with one wave, 110 with four
+  // One wave of CTAs (8 per SM) for all pieces, because most may be idle: 64 short prompts, of which none is
+  // cut, take 108 us with one wave, 110 with four. (`inner` is at most one and a half times the plan's
+  // `tasks`, far below the grid's limit.)
   const int64_t need = (a.H * dd + 256 * vec - 1) / (256 * vec), fit = 8 * kLinearSMs / a.plan.inner;
   const dim3 grid(unsigned(need < fit ? need : fit > 1 ? fit : 1), unsigned(a.plan.inner));
   return launch_pass_kernel(vec == 4 ? linear_scan_kernel<4> : linear_scan_kernel<1>, grid, 256, 0, true, stream, a);

@@ -357,3 +357,12 @@ def test_offsets_past_32_bits(recurrent):
                                      recurrent=recurrent)
     binding.check_device_error()
     assert torch.equal(out[cut:], want)
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+def test_thousand_sequences_and_a_long_one(recurrent):
+    """1201 sequences, empty ones among them, of which one is cut: the pieces are found among them all."""
+    lens = [0] * 400 + [40] * 500 + [2000] + [45] * 300
+    c = make(lens, H=2, H_k=1, d_k=72, d_v=72, decay=0.02, seed=9)
+    assert binding.linear_workspace_size(sum(lens), len(lens), 2, 72, 72, B16, F32, recurrent, H_k=1) > 0
+    _check(c, lens, out_dtype=F32, recurrent=recurrent)
