@@ -78,10 +78,21 @@ __device__ __forceinline__ bool linear_slot(const int32_t *__restrict__ cu, int 
   return s.t1 < eos;
 }
 
-// One decay step of a state entry: e^g s, as s + (e^g - 1) s. e^g itself, rounded to fp32, would
-// be off by up to 2^-25 in the same direction at every token of a head with a constant decay,
-// which a memory of thousands of tokens adds up; e^g - 1 carries its error relative to itself.
-__device__ __forceinline__ float decay_step(float s, float expm1_g) { return fmaf(expm1_g, s, s); }
+// One decay step of a state entry, e^g s. Where e^g is one half or more it is s + (e^g - 1) s: e^g
+// itself, rounded to fp32, would be off by up to 2^-25 in the same direction at every token of a head
+// with a constant decay, which a memory of thousands of tokens adds up; e^g - 1 carries its error
+// relative to itself. Below one half it is e^g s: there e^g - 1, near -1, would be off by 2^-25 of
+// the state before the step, however little of it is left, and no memory is long. (For a choice at
+// every token of a loop over rows see the token-recurrent kernel's own form.)
+struct Decay {
+  float c;    // e^g - 1, or e^g
+  bool keep;  // whether s itself is added
+};
+__device__ __forceinline__ Decay decay_of(float g) {
+  const float m = expm1f(g);
+  return m < -0.5f ? Decay{expf(g), false} : Decay{m, true};  // a NaN keeps
+}
+__device__ __forceinline__ float decay_step(float s, Decay d) { return fmaf(d.c, s, d.keep ? s : 0.f); }
 
 struct LinearArgs {
   const void *q, *k, *v;

@@ -94,9 +94,10 @@ struct Table {  // decays of one chunk, log2 units unless said otherwise
   float a[kC];       // from the block's start to the token, itself included
   float es[96];      // 2^(from behind the token to the block's end), blocks 0 .. 2
   uint32_t f[kC];    // e^{G_C - G_j} as a pair: the nearest bf16 (low half), what is left
-  float e1;          // e^{G_C} - 1; in pass 1 e^(everything behind the chunk)
+  float e1;          // e^{G_C} - 1, or e^{G_C} below one half; in pass 1 e^(everything behind the chunk)
+  float keep;        // 1 or 0: how often the state itself is added to e1 times the state (see Decay)
   uint32_t stop;     // pass 1: no chunk before this one leaves anything
-  float pad[2];
+  float pad;
   __device__ __forceinline__ float block(int B) const { return a[32 * B + 31]; }
 };
 static_assert(sizeof(Table) % 16 == 0, "128-bit reads of the second table");
@@ -490,7 +491,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool stop = kStateOnly && total <= double(kMinLog2);  // a NaN goes on
       if (lane == 0) {
-        w.e1 = kStateOnly ? before : expm1f(all * kLn2);
+        if constexpr (kStateOnly) {
+          w.e1 = before;
+        } else {
+          const bool keep = !(all < -1.f);  // a NaN keeps
+          w.e1 = keep ? expm1f(all * kLn2) : ex2(all);
+          w.keep = keep ? 1.f : 0.f;
+        }
         w.stop = stop;
       }
       __syncwarp();
@@ -726,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; n < chunks; ++n) {
       const Table &tb = tab[n & 1];
       if (!wait_warp(ctl->tab_full[n & 1], n >> 1, DEVERR_MMA_TIMEOUT)) break;
-      const float e1 = tb.e1;
+      const float e1 = tb.e1, keep = kStateOnly ? 0.f : tb.keep;
       const bool stop = kStateOnly && tb.stop != 0;
       float eG = 0.f;  // e^{G_r}, the decay of the entering state at token r
       if constexpr (!kStateOnly) {
@@ -749,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 16; e += 2) {
           const float2 x = make_float2(S[c + e], S[c + e + 1]), dd2 = make_float2(d[e], d[e + 1]);
           const float2 y = kStateOnly ? f2_fma(make_float2(e1, e1), dd2, x)
-                                      : f2_add(f2_fma(make_float2(e1, e1), x, x), dd2);
+                                      : f2_fma(make_float2(e1, e1), x, f2_fma(make_float2(keep, keep), x, dd2));
           S[c + e] = y.x, S[c + e + 1] = y.y;
         }
       }

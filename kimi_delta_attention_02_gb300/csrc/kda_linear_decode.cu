@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kThr)
     }
   };
   load(0);
-  const float em1 = expm1f(log_decay[per_token ? bh : h]);
+  const Decay decay = decay_of(log_decay[per_token ? bh : h]);
   float vv[kVec];
 #pragma unroll
   for (int e = 0; e < kVec; ++e) vv[e] = ok ? load_elem<kInBF16>(v, bh * d_v + col + e) : 0.f;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThr)
         const float kr = s_k[r], qr = s_q[r];
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-          st[j][e] = fmaf(kr, vv[e], decay_step(st[j][e], em1));
+          st[j][e] = fmaf(kr, vv[e], decay_step(st[j][e], decay));
           o[e] = fmaf(qr, st[j][e], o[e]);
         }
         if (ok) {

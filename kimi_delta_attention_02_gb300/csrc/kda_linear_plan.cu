@@ -43,9 +43,9 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a) {
       for (int i = 0; i < kAhead; ++i) {
         const int j = j0 + i;
         if (j + 1 >= segs) break;
-        const float em1 = expm1f(D[i]);
+        const Decay decay = decay_of(D[i]);
 #pragma unroll
-        for (int v = 0; v < kVec; ++v) S.v[v] = decay_step(S.v[v], em1) + b[i].v[v];
+        for (int v = 0; v < kVec; ++v) S.v[v] = decay_step(S.v[v], decay) + b[i].v[v];
         if (j + kAhead + 1 < segs) b[i] = read(j + kAhead), D[i] = d[(j + kAhead) * a.H];
         // B_{j+1} of this place, if there is one, was read above (kAhead >= 2)
         *reinterpret_cast<Vec *>(p + (j + 1) * step) = S;

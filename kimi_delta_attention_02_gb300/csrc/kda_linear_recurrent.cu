@@ -7,7 +7,7 @@
 // (pair, rg) of warp w owns columns 16 w + 2 pair, + 1 and the key rows 16 j + 4 rg + 0..3, so a
 // row sum ends with two shuffles inside a warp and the tokens need no CTA barrier. q, k, v pass
 // through shared memory 16 tokens at a time (fp32), the next 16 waiting in registers. Two rows
-// go through one packed fp32 instruction: 3 per row pair, column and token (decay, write,
+// go through one packed fp32 instruction: 3 per row pair, column and token (k v, decay,
 // read-out), which bound the kernel where it fills the SMs; with few heads the chain of tokens does,
 // 0.35 us each (prompts of 700 and 333 tokens, 6 heads of 100 x 72 in fp32: 45 us in segments; 128
 // sequences of 4 tokens and 64 heads of 64, bf16: 103 us, 2.6 TB/s of states).
@@ -25,10 +25,10 @@ constexpr int kThr = 128;
 // kRows: key rows per thread (16 for d_k <= 64, else 32). kStateOnly: pass 1 of a segmented call,
 // which leaves the state from zero and the summed log-decay in the workspace.
 template <bool kInBF16, bool kOutBF16, int kRows, bool kStateOnly>
-__global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__(kThr, 3) linear_recurrent_kernel(const LinearArgs a) {
   __shared__ __align__(16) float s_k[2][kTok][4 * kRows], s_q[2][kTok][4 * kRows];
   __shared__ __align__(16) float s_v[2][kTok][kCols];
-  __shared__ float s_e[2][kTok], s_g[2][kTok];  // e^g - 1; g (pass 1)
+  __shared__ float s_e[2][kTok], s_g[2][kTok];  // e^g; g (pass 1)
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int rg = lane & 3, pair = lane >> 2;
   const int h = blockIdx.x % a.H;
@@ -81,7 +81,22 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
     }
     if (tid < kTok) rg_ = t + tid < s.t1 ? a.log_decay[a.per_token ? (t + tid) * a.H + h : h] : 0.f;
   };
-  auto stage = [&](int b) {
+  // The factor of a token's decay, e^g in fp32. Simply rounded, the factors of a constant decay would
+  // all be off the same way, which a memory of thousands of tokens adds up. So the token takes a whole
+  // ulp more or less where `rest`, what one rounding loses in ulps, times the tokens so far passes a
+  // half: factors of a constant decay stay within an ulp of e to the sum, others round either way
+  // without a bias. (Decay's choice between two forms, made in the loop over rows, costs 2.07 ms at
+  // T = 4096, 96 heads of 128 in fp32; this 1.57.)
+  auto factor = [&](float g, int64_t t) {
+    const Decay d = decay_of(g);
+    if (!d.keep) return d.c;  // e^g below one half: no memory to drift
+    const float e = 1.f + d.c;
+    const uint32_t exponent = __float_as_uint(e) & 0x7f800000u;  // an ulp is 2^-23 of its power of two
+    const float rest = (d.c - (e - 1.f)) * __uint_as_float(0x8a800000u - exponent);
+    const float n = float((t - s.t0) & 4095);
+    return fmaf(rintf((n + 1.f) * rest) - rintf(n * rest), __uint_as_float(exponent - 0x0b800000u), e);
+  };
+  auto stage = [&](int b, int64_t t) {
     if (tid < 4 * kRows) {
 #pragma unroll
       for (int i = 0; i < kTok; ++i) {
@@ -92,7 +107,7 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
 #pragma unroll
     for (int i = 0; i < kTok * kCols / kThr; ++i) s_v[b][2 * i + (tid >> 6)][tid & 63] = value(rv[i]);
     if (tid < kTok) {
-      s_e[b][tid] = expm1f(rg_);
+      s_e[b][tid] = factor(rg_, t + tid);
       if constexpr (kStateOnly) s_g[b][tid] = rg_;
     }
   };
@@ -100,7 +115,7 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
   double decay_sum = 0.;  // of the segment, pass 1 (all threads alike)
   if (s.t0 < s.t1) {
     fetch(s.t0);
-    stage(0);
+    stage(0, s.t0);
   }
   int b = 0;
   for (int64_t t = s.t0; t < s.t1; t += kTok, b ^= 1) {
@@ -126,10 +141,10 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
         for (int j = 0; j < kRows / 4; ++j) {
           const float4 k4 = *reinterpret_cast<const float4 *>(&s_k[b][i + u][16 * j + 4 * rg]);
           const float2 ka = make_float2(k4.x, k4.y), kb = make_float2(k4.z, k4.w);
-          S[0][2 * j] = f2_fma(ka, v0, f2_fma(e2, S[0][2 * j], S[0][2 * j]));
-          S[0][2 * j + 1] = f2_fma(kb, v0, f2_fma(e2, S[0][2 * j + 1], S[0][2 * j + 1]));
-          S[1][2 * j] = f2_fma(ka, v1, f2_fma(e2, S[1][2 * j], S[1][2 * j]));
-          S[1][2 * j + 1] = f2_fma(kb, v1, f2_fma(e2, S[1][2 * j + 1], S[1][2 * j + 1]));
+          S[0][2 * j] = f2_fma(e2, S[0][2 * j], f2_mul(ka, v0));
+          S[0][2 * j + 1] = f2_fma(e2, S[0][2 * j + 1], f2_mul(kb, v0));
+          S[1][2 * j] = f2_fma(e2, S[1][2 * j], f2_mul(ka, v1));
+          S[1][2 * j + 1] = f2_fma(e2, S[1][2 * j + 1], f2_mul(kb, v1));
           if constexpr (!kStateOnly) {
             const float4 q4 = *reinterpret_cast<const float4 *>(&s_q[b][i + u][16 * j + 4 * rg]);
             const float2 qa = make_float2(q4.x, q4.y), qb = make_float2(q4.z, q4.w);
@@ -151,7 +166,7 @@ __global__ void __launch_bounds__(kThr) linear_recurrent_kernel(const LinearArgs
           store_elem<kOutBF16>(a.out, ((t + i + u) * a.H + h) * a.d_v + col + c, a.scale * x);
       }
     }
-    if (more) stage(b ^ 1);
+    if (more) stage(b ^ 1, t + kTok);
   }
 
   float *dst = kStateOnly ? a.seg_states + (s.place * a.H + h) * dd
