@@ -402,8 +402,8 @@ kda_status kda_prologue(const void *q_raw, const void *k_raw, const void *v_raw,
  * what follows; one in q, k or log_decay only what depends on it. fp32 inputs and short sequences
  * run the fp32 token-recurrent kernel.
  *
- * Sizes: 1 <= d_k, d_v <= 128, H, H_k >= 1; decode needs B >= 1. Results are accumulated in fp32
- * and states are fp32.
+ * Sizes: 1 <= d_k, d_v <= 128, H, H_k >= 1, total_tokens <= 2^31 - 128; decode needs B >= 1. Results
+ * are accumulated in fp32 and states are fp32.
  */
 typedef struct kda_linear_prefill_params {
   uint32_t struct_size;       /* sizeof the struct; any other value is KDA_ERR_INVALID_ARG   */

@@ -291,7 +291,7 @@ kda_status check_linear_sizes(int64_t rows, int64_t states, int32_t H, int32_t H
   if (!valid_dtype(in_dtype) || !valid_dtype(out_dtype)) return KDA_ERR_INVALID_ARG;
   if (rows < 0 || states < 0 || H < 1 || H_k < 1 || d_k < 1 || d_v < 1) return KDA_ERR_INVALID_ARG;
   if (H % H_k != 0 || (per_token != 0 && per_token != 1)) return KDA_ERR_INVALID_ARG;
-  if (d_k > 128 || d_v > 128 || rows > INT32_MAX || states * H > INT32_MAX / 4) return KDA_ERR_UNSUPPORTED;
+  if (d_k > 128 || d_v > 128 || rows > kLinearMaxTokens || states * H > INT32_MAX / 4) return KDA_ERR_UNSUPPORTED;
   if (rows * H > INT64_MAX / 1024) return KDA_ERR_UNSUPPORTED;  // bytes of a tensor
   return KDA_OK;
 }

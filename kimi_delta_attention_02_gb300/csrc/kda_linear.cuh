@@ -30,6 +30,7 @@ struct LinearPlan {
   size_t bytes = 0;         // of the workspace that the plan uses
 };
 
+constexpr int64_t kLinearMaxTokens = 0x7fffff80;  // 2^31 - 128: token indexes rounded up to chunks stay 32-bit
 constexpr int kLinearSMs = 152;       // a GB300's (fixed: the workspace query needs no device)
 constexpr int kLinearTokenCols = 64;  // value columns per CTA of the token-recurrent kernel
 

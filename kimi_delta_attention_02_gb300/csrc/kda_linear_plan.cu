@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(256) linear_scan_kernel(const LinearArgs a) {
   const bool some = linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, blockIdx.y, s) && s.first;
   wait_for_earlier_passes();
   if (!some) return;
-  const int segs = (a.cu[s.n + 1] - a.cu[s.n] + a.plan.seg_len - 1) / a.plan.seg_len;
+  const int segs = (a.cu[s.n + 1] - a.cu[s.n] - 1) / a.plan.seg_len + 1;  // (a sum could pass 2^31)
   const int64_t dd = int64_t(a.d_k) * a.d_v, step = int64_t(a.H) * dd;
   struct alignas(4 * kVec) Vec {
     float v[kVec];

@@ -185,3 +185,17 @@ def test_workspace_query():
                  (10, 1, 1, 1, 129, 64, 1, 1, 0), (10, 1, 1, 1, 64, 64, 3, 1, 0), (-5, 1, 1, 1, 64, 64, 1, 1, 0),
                  (10, 1, 4, 3, 64, 64, 1, 1, 0), (2**31 - 1, 1, 2**28, 1, 63, 63, 1, 1, 0)]:
         assert q(*args) == 0
+
+
+def test_the_most_tokens():
+    """2^31 - 128: token indexes rounded up to a chunk of 128 stay below 2^31."""
+    most = 2**31 - 128
+    for T in (most + 1, 2**31 - 1):
+        assert _prefill(total_tokens=T, H=1, H_k=1, d_k=8, d_v=8) == UNS
+        assert B.linear_workspace_size(T, 1, 1, 8, 8) == 0
+    assert B.linear_workspace_size(most, 1, 1, 8, 8) > 0
+    # up to there the plan's segments, and what the kernels form of a length, fit in 32 bits
+    seg = -(-(-(-most // 152)) // 128) * 128
+    assert (most + 127) // 128 * 128 < 2**31 and (most - 1) // seg + 1 == 152
+    # rounding a length up to whole segments would not: that is why the count is formed without it
+    assert most + seg - 1 >= 2**31
