@@ -480,13 +480,18 @@ def _address(t):
     return None if t is None else t.data_ptr()
 
 
-def _used_on(stream, *tensors):
-    """Tensors allocated here for the caller's stream: the allocator must not hand their memory
-    to another stream's work before that stream is done with it."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+def _empty(shape, dtype, device, stream, returned=True):
+    """torch.empty for work on ``stream`` (None: the current one). The memory comes from that stream's
+    pool: the current stream's may hand out a block that work pending there still uses, which
+    another stream's kernel would not wait for. A tensor that is ``returned`` may be used on the
+    current stream too, so its memory goes back only when that is done with it."""
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 def _check_shape(name, t, shape, dtype=None):
@@ -554,15 +559,13 @@ def linear_prefill(q, k, v, log_decay, cu_seqlens, init_state=None, *, out=None,
     if init_state is not None:
         _check_shape("init_state", init_state, state_shape, torch.float32)
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=out_dtype, device=q.device)
-        _used_on(stream, out)
+        out = _empty((T, H, d_v), out_dtype, q.device, stream)
     else:
         _check_shape("out", out, (T, H, d_v))
     if final_state is not None:
         _check_shape("final_state", final_state, state_shape, torch.float32)
     elif want_final:
-        final_state = torch.empty(state_shape, dtype=torch.float32, device=q.device)
-        _used_on(stream, final_state)
+        final_state = _empty(state_shape, torch.float32, q.device, stream)
     dt, odt, rec = _io_dtype(q.dtype), _io_dtype(out.dtype), 1 if recurrent else 0
     handle = lib()
     if given is None and workspace is not None:
@@ -570,8 +573,7 @@ def linear_prefill(q, k, v, log_decay, cu_seqlens, init_state=None, *, out=None,
             raise ValueError("workspace must be 'auto', None or a uint8 CUDA tensor")
         n = handle.kda_linear_prefill_workspace_size(T, N, H, H_k, d_k, d_v, dt, odt, rec)
         if n:
-            given = torch.empty(n, dtype=torch.uint8, device=q.device)
-            _used_on(stream, given)
+            given = _empty(n, torch.uint8, q.device, stream, returned=False)
     p = LinearPrefillParams(_LINEAR_PREFILL_BYTES, dt, odt, N, H, H_k, d_k, d_v, 1 if log_decay.ndim == 2 else 0, rec, T,
                             q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), cu_seqlens.data_ptr(),
                             _address(init_state), out.data_ptr(), _address(final_state), _address(given),
@@ -593,8 +595,7 @@ def linear_decode(q, k, v, log_decay, state, *, out=None, out_dtype=torch.float3
         with torch.cuda.device(device):
             return linear_decode(q, k, v, log_decay, state, out=out, out_dtype=out_dtype, scale=scale, stream=stream)
     if out is None:
-        out = torch.empty((B, H, d_v), dtype=out_dtype, device=q.device)
-        _used_on(stream, out)
+        out = _empty((B, H, d_v), out_dtype, q.device, stream)
     else:
         _check_shape("out", out, (B, H, d_v))
     p = LinearDecodeParams(_LINEAR_DECODE_BYTES, _io_dtype(q.dtype), _io_dtype(out.dtype), B, H, H_k, d_k, d_v,
@@ -650,13 +651,11 @@ def block_norm(x, y=None, *, gate=None, post_norm: bool = False, post_weight=Non
     if residual_out is not None:
         _check_shape("residual_out", residual_out, (rows, D), x.dtype)
     elif want_residual and y is not None:
-        residual_out = torch.empty_like(x)
-        _used_on(stream, residual_out)
+        residual_out = _empty(x.shape, x.dtype, x.device, stream)
     if out is not None:
         _check_shape("out", out, (rows, D))
     elif want_out:
-        out = torch.empty_like(x, dtype=out_dtype)
-        _used_on(stream, out)
+        out = _empty(x.shape, out_dtype or x.dtype, x.device, stream)
     p = BlockNormParams(_BLOCK_NORM_BYTES, _io_dtype(x.dtype), KDA_F32 if y is None else _io_dtype(y.dtype),
                         KDA_F32 if out is None else _io_dtype(out.dtype), form, 1 if post_norm else 0, D, scale, rows,
                         x.data_ptr(), _address(y), _address(gate), _address(post_weight), _address(channel_scale),
