@@ -171,6 +171,20 @@ def _stream_handle(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream, returned=True):
+    """torch.empty for work on ``stream`` (None: the current one). The memory comes from that stream's
+    pool: the current stream's may hand out a block that work pending there still uses, which
+    another stream's kernel would not wait for. A tensor that is ``returned`` may be used on the
+    current stream too, so its memory goes back only when that is done with it."""
+    if stream is None or device.index is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _io_dtype(dtype) -> int:
     if dtype == torch.bfloat16:
         return KDA_BF16
@@ -190,7 +204,7 @@ def workspace_size(total_tokens: int, num_seqs: int, H: int, d_k: int = 128, d_v
     return int(lib().kda_prefill_workspace_size(int(total_tokens), int(num_seqs), int(H), int(d_k), int(d_v)))
 
 
-def _workspace(workspace, T, N, H, d_k, d_v, device):
+def _workspace(workspace, T, N, H, d_k, d_v, device, stream):
     """(pointer, bytes) of the scratch handed to the library: ``"auto"`` allocates what
     ``kda_prefill_workspace_size`` asks for (through torch's caching allocator), ``None`` passes
     none (one CTA per chain), a uint8 CUDA tensor is passed as given."""
@@ -202,7 +216,7 @@ def _workspace(workspace, T, N, H, d_k, d_v, device):
         n = workspace_size(T, N, H, d_k, d_v)
         if n == 0:
             return None, 0
-        workspace = torch.empty(n, dtype=torch.uint8, device=device)
+        workspace = _empty(n, torch.uint8, device, stream, returned=False)
     _check_cuda(workspace)
     return ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
 
@@ -229,17 +243,17 @@ def prefill(q, k, v, log_alpha, beta, cu_seqlens, init_state=None, *, out=None, 
     if cu_seqlens.dtype != torch.int32:
         raise TypeError("cu_seqlens must be int32")
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=out_dtype, device=q.device)
+        out = _empty((T, H, d_v), out_dtype, q.device, stream)
     odt = _io_dtype(out.dtype)
     if final_state is None and want_final:
-        final_state = torch.empty((N, H, d_k, d_v), dtype=torch.float32, device=q.device)
+        final_state = _empty((N, H, d_k, d_v), torch.float32, q.device, stream)
     _check_cuda(q, k, v, log_alpha, beta, cu_seqlens, init_state, out, final_state)
     args = (_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(cu_seqlens), N, T, H, d_k, d_v, dt,
             odt, float(lower_bound), float(scale), _ptr(init_state), _ptr(out), _ptr(final_state))
     if recurrent:
         st = lib().kda_prefill_recurrent(*args, _stream_handle(stream))
     else:
-        ws, ws_bytes = _workspace(workspace, T, N, H, d_k, d_v, q.device)
+        ws, ws_bytes = _workspace(workspace, T, N, H, d_k, d_v, q.device, stream)
         st = lib().kda_prefill(*args, ws, ws_bytes, _stream_handle(stream))
     if st != KDA_OK:
         raise KdaError(st, "kda_prefill_recurrent" if recurrent else "kda_prefill")
@@ -283,10 +297,10 @@ def prefill_gated(q, k, v, z, A_log, beta, cu_seqlens, init_state=None, *, out=N
     if cu_seqlens.dtype != torch.int32:
         raise TypeError("cu_seqlens must be int32")
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=out_dtype, device=q.device)
+        out = _empty((T, H, d_v), out_dtype, q.device, stream)
     odt = _io_dtype(out.dtype)
     if final_state is None and want_final:
-        final_state = torch.empty((N, H, d_k, d_v), dtype=torch.float32, device=q.device)
+        final_state = _empty((N, H, d_k, d_v), torch.float32, q.device, stream)
     _check_cuda(q, k, v, z, A_log, beta, cu_seqlens, init_state, out, final_state)
     fn = lib().kda_prefill_gated_recurrent if recurrent else lib().kda_prefill_gated
     st = fn(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A_log), _ptr(beta), _ptr(cu_seqlens), N, T, H, d_k, d_v, dt,
@@ -338,11 +352,11 @@ def prefill_ex(q, k, v, beta, cu_seqlens, *, log_alpha=None, lower_bound: float 
     if beta.dtype != torch.float32 or cu_seqlens.dtype != torch.int32:
         raise TypeError("beta must be float32 and cu_seqlens int32")
     if out is None:
-        out = torch.empty((T, H, d_v), dtype=out_dtype, device=q.device)
+        out = _empty((T, H, d_v), out_dtype, q.device, stream)
     if final_state is None and want_final:
-        final_state = torch.empty((N, H, d_k, d_v), dtype=torch.float32, device=q.device)
+        final_state = _empty((N, H, d_k, d_v), torch.float32, q.device, stream)
     _check_cuda(q, k, v, decay, A, beta, cu_seqlens, init_state, out_gate, norm_weight, out, final_state)
-    ws, ws_bytes = _workspace(None if recurrent else workspace, T, N, H, d_k, d_v, q.device)
+    ws, ws_bytes = _workspace(None if recurrent else workspace, T, N, H, d_k, d_v, q.device, stream)
     p = PrefillParams(struct_size=ctypes.sizeof(PrefillParams), in_dtype=_io_dtype(q.dtype),
                       out_dtype=_io_dtype(out.dtype), decay_form=form, num_seqs=N, H=H, d_k=d_k, d_v=d_v,
                       total_tokens=T, q=q.data_ptr(), k=k.data_ptr(), v=v.data_ptr(), decay=decay.data_ptr(),
@@ -375,7 +389,7 @@ def decode_ex(q, k, v, beta, state, *, log_alpha=None, lower_bound: float = -5.0
     if out_gate is not None and out_gate.dtype != q.dtype:
         raise TypeError("out_gate must have the dtype of q")
     if out is None:
-        out = torch.empty((B, H, d_v), dtype=out_dtype, device=q.device)
+        out = _empty((B, H, d_v), out_dtype, q.device, stream)
     _check_cuda(q, k, v, decay, A, beta, state, out_gate, norm_weight, conv_weight, conv_state, out)
     if conv_state is not None and conv_state.dtype != q.dtype:
         raise TypeError("conv_state must have the dtype of q")
@@ -410,11 +424,11 @@ def prologue(q_raw, k_raw, v_raw, conv_weight, cu_seqlens, conv_init=None, *, l2
         raise TypeError("conv_weight must be float32 and cu_seqlens int32")
     if conv_init is not None and conv_init.dtype != q_raw.dtype:
         raise TypeError("conv_init must have the dtype of q")
-    q = torch.empty_like(q_raw) if q is None else q
-    k = torch.empty_like(k_raw) if k is None else k
-    v = torch.empty_like(v_raw) if v is None else v
+    q = _empty(q_raw.shape, q_raw.dtype, q_raw.device, stream) if q is None else q
+    k = _empty(k_raw.shape, k_raw.dtype, k_raw.device, stream) if k is None else k
+    v = _empty(v_raw.shape, v_raw.dtype, v_raw.device, stream) if v is None else v
     if conv_final is None and want_final:
-        conv_final = torch.empty((N, H, 3, 2 * d_k + d_v), dtype=q_raw.dtype, device=q_raw.device)
+        conv_final = _empty((N, H, 3, 2 * d_k + d_v), q_raw.dtype, q_raw.device, stream)
     _check_cuda(q_raw, k_raw, v_raw, conv_weight, cu_seqlens, conv_init, q, k, v, conv_final)
     st = lib().kda_prologue(_ptr(q_raw), _ptr(k_raw), _ptr(v_raw), _ptr(conv_weight), _ptr(cu_seqlens), N, T, H,
                             d_k, d_v, dt, _ptr(conv_init), float(l2_eps), _ptr(q), _ptr(k), _ptr(v),
@@ -433,7 +447,7 @@ def decode_gated(q, k, v, z, A_log, beta, state, *, out=None, out_dtype=torch.fl
     if z.dtype != q.dtype or A_log.dtype != torch.float32:
         raise TypeError("z must have the dtype of q, A_log must be float32")
     if out is None:
-        out = torch.empty((B, H, d_v), dtype=out_dtype, device=q.device)
+        out = _empty((B, H, d_v), out_dtype, q.device, stream)
     odt = _io_dtype(out.dtype)
     _check_cuda(q, k, v, z, A_log, beta, state, out)
     st = lib().kda_decode_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(z), _ptr(A_log), _ptr(beta), _ptr(state), _ptr(out),
@@ -451,7 +465,7 @@ def decode(q, k, v, log_alpha, beta, state, *, out=None, out_dtype=torch.float32
     d_v = v.shape[-1]
     dt = _io_dtype(q.dtype)
     if out is None:
-        out = torch.empty((B, H, d_v), dtype=out_dtype, device=q.device)
+        out = _empty((B, H, d_v), out_dtype, q.device, stream)
     odt = _io_dtype(out.dtype)
     _check_cuda(q, k, v, log_alpha, beta, state, out)
     st = lib().kda_decode(_ptr(q), _ptr(k), _ptr(v), _ptr(log_alpha), _ptr(beta), _ptr(state), _ptr(out), B, H,
@@ -478,20 +492,6 @@ def _one_device(*tensors) -> int:
 
 def _address(t):
     return None if t is None else t.data_ptr()
-
-
-def _empty(shape, dtype, device, stream, returned=True):
-    """torch.empty for work on ``stream`` (None: the current one). The memory comes from that stream's
-    pool: the current stream's may hand out a block that work pending there still uses, which
-    another stream's kernel would not wait for. A tensor that is ``returned`` may be used on the
-    current stream too, so its memory goes back only when that is done with it."""
-    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(device.index):
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
-    if returned:
-        t.record_stream(torch.cuda.current_stream(device))
-    return t
 
 
 def _check_shape(name, t, shape, dtype=None):

@@ -75,3 +75,12 @@ def test_prefill_dtype_checks():
         B.prefill(c.q, c.k, c.v, c.log_alpha, c.beta, c.cu_seqlens.long())
     with pytest.raises(TypeError, match="float32"):
         B.prefill(c.q, c.k, c.v, c.log_alpha.double(), c.beta, c.cu_seqlens)
+
+
+def test_host_tensors_are_refused_with_a_stream_too():
+    class Stream:
+        cuda_stream = 1
+
+    c = _case()
+    with pytest.raises(ValueError, match=CUDA_ONLY):
+        B.prefill(c.q, c.k, c.v, c.log_alpha, c.beta, c.cu_seqlens, c.init_state, stream=Stream())
