@@ -16,10 +16,12 @@
 // s_j from behind j to its block's end, t_B a whole block's (log2 units). Then e^{G_i - G_j} is
 // 2^{a_i - a_j} within a block and 2^{a_i + t_{J+1} + ... + t_{I-1}} 2^{s_j} across: no factor is
 // the difference of two long sums, none exceeds one while g <= 0, and only the diagonal blocks
-// take an exponential per entry, of a difference of two sums: off by at most 256 x 2^-24 x ln 2 <
-// 2^-16 while a block's 32 tokens decay by 2^-256 or less. In a block that decays by more every entry
-// takes its own sum if the output is fp32; a bf16 output bears the difference (sums up to 32 x 127,
-// off by at most 2^-10.5 next to P's 2^-8; without the branch the loop is 4 % faster). A decay below
+// take an exponential per entry, of a difference of two sums a. Each sum is made in five levels: off by
+// at most 5 x 2^-24 of itself, and 2^-24 for its terms' own roundings, so their difference is off by
+// 11 x 2^-24 x ln 2 of the block's sum: less than 2^-16 while its 32 tokens decay by 2^-32 or less. In a block that
+// decays by more every entry takes its own sum if the output is fp32 (T = 4096, 96 heads of 128 that
+// all do: 255 us, 218 without); a bf16 output bears the difference (sums up to 32 x 127, off by at
+// most 2^-9, seen 2^-10.4, next to P's 2^-8; without the branch the loop is 4 % faster). A decay below
 // 2^-127 per token counts as 2^-127, which leaves nothing in fp32 either, so g = -infinity needs no
 // case of its own.
 //
@@ -59,7 +61,7 @@ constexpr uint32_t kBuf = 32768;   // 128 tokens x 128 channels bf16, two 64-cha
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kMinLog2 = -127.f;
 constexpr uint32_t kProbes = 2000000;
-constexpr float kFarLog2 = -256.f;  // of a block's 32 tokens
+constexpr float kFarLog2 = -32.f;  // of a block's 32 tokens
 
 template <int kDV, bool kOutBF16, bool kStateOnly>
 struct Cfg {
