@@ -382,9 +382,12 @@ kda_status kda_prologue(const void *q_raw, const void *k_raw, const void *v_raw,
  *   q, k         [total_tokens, H_k, d_k] (decode: [B, H_k, d_k])   in_dtype
  *   log_decay    g, fp32: [total_tokens, H] (decode: [B, H]) with decay_per_token = 1, or one
  *                constant per head [H] with decay_per_token = 0. Any value up to 0 including
- *                -infinity (the state is forgotten); a positive g grows the state and is computed
- *                while e to the sum of the positive ones of 128 tokens stays finite. NaN
- *                propagates. No clamp is applied.
+ *                -infinity (the state is forgotten). A positive g grows the state; it is computed
+ *                while no run of consecutive tokens sums above 40. A run of tokens that sums below
+ *                -87 counts as forgetting what enters it (e^-48 of that may be left), also where
+ *                growth before or behind it would have kept some: the tensor-core kernel takes a g
+ *                below -88 as -88, and leaves a token out of a segment's end state where less than
+ *                e^-87 of it is left at the end. NaN propagates.
  *   workspace    (prefill) as in kda_prefill, of kda_linear_prefill_workspace_size() bytes: with
  *                it, sequences longer than a CTA's share of the call are cut into segments that
  *                run side by side, and bf16 head sizes that are no multiple of 8 are padded for

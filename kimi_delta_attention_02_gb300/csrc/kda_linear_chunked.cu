@@ -22,8 +22,8 @@
 // decays by more every entry takes its own sum if the output is fp32 (T = 4096, 96 heads of 128 that
 // all do: 255 us, 218 without); a bf16 output bears the difference (sums up to 32 x 127, off by at
 // most 2^-9, seen 2^-10.4, next to P's 2^-8; without the branch the loop is 4 % faster). A decay below
-// 2^-127 per token counts as 2^-127, which leaves nothing in fp32 either, so g = -infinity needs no
-// case of its own.
+// 2^-127 per token counts as 2^-127, which leaves nothing in fp32 either unless a state of 2^100 entered it
+// or growth follows (up to e^40 by the header, so e^-48 is left), so g = -infinity needs no case of its own.
 //
 // Shared memory holds five 32 KB buffers that the chunks' tiles take in turn, Q V K Q V K ..., so that
 // a tile waits for the one five places before it: Q of chunk n for V of n - 2, V for K of n - 2, K for
@@ -33,7 +33,8 @@
 //
 // Pass 1 of a segmented call (kStateOnly) forms a segment's end state from zero, sum over its chunks of
 // e^(decay behind the chunk) K^T V', last chunk first: once that factor is below 2^-127, and so zero in
-// fp32, no earlier token leaves anything and the rest of the segment is not read.
+// fp32, no earlier token leaves anything and the rest of the segment is not read. (With a positive g
+// before, some would be left: the header counts what enters a run of tokens that sums below -87 as forgotten.)
 //
 // Warps (20): 0 loads (TMA), 1 issues the MMAs Q K^T, Q S, P V, 2 makes the decay tables, 3 issues
 // K^T V' (on its own, so that either's waits are filled by the other's work), 4-7 form P (one

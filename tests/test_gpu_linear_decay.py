@@ -152,3 +152,36 @@ def test_a_constant_decay_does_not_drift(per_token):
     mean = ((fin.double() - want) / want).mean((0, 2, 3)).abs().cpu()
     bound = 2.0 ** -23 + T * g.abs().cpu() * 2.0 ** -23 + 6 * (T / 3 / 4096) ** 0.5 * 2.0 ** -24
     assert (mean <= bound).all(), (mean, bound)
+
+
+@pytest.mark.parametrize("out_dtype", [B16, F32])
+@pytest.mark.parametrize("recurrent", [False, True])
+def test_growth_among_decays(out_dtype, recurrent):
+    """Log-decays of either sign, whose runs all sum to between -18 and 18 (26 in log2 units), cut and
+    uncut. On the tensor-core kernel a sum over a block passes 31 additions and 32 roundings of its terms,
+    each of at most 26, and an entry takes a difference of two: 126 x 26 x 2^-24 x ln 2 < 2^-12."""
+    T, H = 1500, 4
+    c = make([T], H=H, d_k=64, d_v=64, seed=6)
+    g = torch.Generator().manual_seed(6)
+    level = 6 * torch.sin(torch.arange(T + 1)[:, None] * torch.tensor([0.01, 0.11, 0.7, 3.0])) + 6 * torch.rand(T + 1, H, generator=g) - 3
+    c["log_decay"] = (level[1:] - level[:-1]).float().cuda()
+    o, f, mo, mf = reference(c)
+    fine = 2.0 ** -12 + 2.0 ** -15 + fp32_factor(T, 64)
+    half = 2.0 ** -8 if out_dtype == B16 else 0.0
+    for workspace in ("auto", None):
+        out, fin = run(c, out_dtype=out_dtype, recurrent=recurrent, workspace=workspace)
+        check(out, o, mo * (half + fine) + half * np.abs(o), 1.0, "out")
+        check(fin, f, mf, fine, "final")
+
+
+@pytest.mark.parametrize("recurrent", [False, True])
+def test_what_a_long_decay_forgets_stays_forgotten(recurrent):
+    """Growth by up to e^40 behind tokens that forget brings back e^-48 of the state at most."""
+    for where, then in ((5, 9), (5, 100), (5, 1000), (130, 2300)):
+        for g in (-float("inf"), -1e4, -88.0):
+            c = _still([2500], H=2, seed=2)
+            c["log_decay"][where], c["log_decay"][then] = g, 40.0
+            most = float(np.exp(-48.0)) * float(c["init_state"].abs().max())
+            for workspace in ("auto", None):
+                out, fin = run(c, recurrent=recurrent, workspace=workspace)
+                assert float(fin.abs().max()) <= 1.0001 * most
