@@ -474,7 +474,9 @@ size_t kda_linear_prefill_workspace_size(int64_t total_tokens, int32_t num_seqs,
  * needs post_norm = 1; pre_weight needs out. Outputs overlap no input and not each other
  * (residual_out == x excepted). x, y, gate and the outputs are 16-byte aligned, the weights too.
  * Sizes: rows >= 0, 1 <= D <= 16384. eps finite and >= 0; a row of zeros with eps = 0 gives NaN,
- * as the formula does. Reads and writes each tensor once.
+ * as the formula does. Squares are summed in fp32, so rows of y and x' that are normalised hold
+ * values below 1e17 (beyond, their squares' sum may overflow, and the row's norm is 0), and with eps = 0
+ * some above 1e-18. Reads and writes each tensor once.
  */
 typedef enum { KDA_GATE_NONE = 0, KDA_GATE_CHANNEL = 1, KDA_GATE_ROW = 2 } kda_gate_form;
 

@@ -142,3 +142,14 @@ def test_offsets_past_32_bits():
         assert torch.equal(r[-1:], r1) and torch.equal(h[-1:], h1)
         assert not r[:-1].any() and not h[:-1].any()
         del x, y, r, h
+
+
+@pytest.mark.parametrize("D", [64, 777, 2048, 7168, 12288])
+@pytest.mark.parametrize("size", [1e17 / 6, 1e-18])
+def test_rows_of_the_largest_and_smallest_values(D, size):
+    """Squares stay within fp32: 16384 x (10^17)^2 = 1.6 x 10^38, and those of 10^-18 are normal numbers."""
+    for c in (_make(3, D, x=F32, y=F32), _make(3, D, x=F32, y=F32, post=False, weights=False)):
+        c["x"], c["y"] = (size / 3 * c["x"]).clamp(-1e17, 1e17), (size * c["y"]).clamp(-1e17, 1e17)
+        if not c["post_norm"]:
+            c["y"] = c["y"] / 3
+        _check(c, eps=0.0, out_dtype=F32)
