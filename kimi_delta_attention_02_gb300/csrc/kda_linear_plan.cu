@@ -172,17 +172,23 @@ cudaError_t launch_linear_unpad(const LinearArgs &a, bool out_bf16, void *out, f
 // A chunk costs the tensor-core kernel the same however few tokens it holds, the token-recurrent one
 // goes by tokens, so the mean length decides. Microseconds, tensor cores / token-recurrent, at
 // sequences of 4, 16, 32 and 64 tokens:
-//   16 of 64 heads of 128, bf16 out   72/58   72/85   72/126  85/210    128 of them  505/351 505/524 505/824  511/1504
-//   the same, fp32 out                   -   104/85  103/126 120/210                    -   763/527 761/826  792/1512
-//   16 of 64 heads of 64                 -    51/32   51/47   58/73                     -   335/155 337/247  345/433
-//   16 of 64 heads of 100 (padded)       -   133/85  126/126 166/210                    -   975/546 822/824 1098/1502
-//   16 of 64 heads of 53 (padded)        -      -       -     96/73                     -      -       -     588/429
+//   16 of 64 heads of 128, bf16 out   71/53   72/75   73/113  88/189    128 of them  488/295 511/466 512/748  520/1332
+//   the same, fp32 out               103/52  103/75  103/113 120/190                 728/295 760/466 758/747  791/1332
+//   16 of 64 heads of 64              51/32   50/31   50/44   56/69                  311/99  332/150 335/243  345/429
+// and of padded head sizes at 32, 48, 72 and 96 tokens:
+//   16 of 64 heads of 100, bf16 out  142/108 161/147 176/209 194/265    128 of them 1018/723 1081/1000 1197/1473 1314/1900
+//   the same, fp32 out               180/108 201/147 219/209 236/266               1327/723 1412/1000 1536/1473 1670/1898
+//   16 of 64 heads of 53              78/44   89/57   98/77  111/94                 537/238  575/328  634/479  694/608
+// The mean counts empty sequences, and hides a long one among short ones: one of 8192 tokens beside 600
+// empty ones, 32 heads of 128, takes the token-recurrent kernel, 1400 us of which the states' traffic is 400
+// (alone 100 us on the tensor cores). The host knows no lengths.
 LinearPlan linear_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool out_bf16,
                        bool recurrent, size_t workspace_bytes) {
   LinearPlan p;
   // TMA addresses rows of a multiple of 16 bytes; other head sizes are padded into the workspace
   const bool odd = d_k % 8 != 0 || d_v % 8 != 0, wide = out_bf16 && d_v > 64;
-  const int64_t least = (d_k <= 64 && d_v <= 64 ? 48 : wide && d_k > 64 ? 16 : 24) * (odd ? 2 : 1);
+  const bool small = d_k <= 64 && d_v <= 64;
+  const int64_t least = (small ? 48 : wide && d_k > 64 ? 16 : 24) * (!odd ? 1 : small ? 2 : 3);
   p.tensor = in_bf16 && !recurrent && total >= least * num_seqs;
   const bool pad = p.tensor && odd;
   size_t at = 0;
