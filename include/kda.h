@@ -398,7 +398,9 @@ kda_status kda_prologue(const void *q_raw, const void *k_raw, const void *v_raw,
  *   force_recurrent (prefill) nonzero runs the fp32 token-recurrent kernel
  *
  * bf16 prompts run a tensor-core kernel in chunks of 128 tokens, unless their sequences are short
- * (fewer than 16 to 96 tokens on average, by head sizes and output type). It rounds the masked
+ * (fewer than 16 to 96 tokens on average, by head sizes and output type; empty sequences count, so
+ * a cu_seqlens with many of them may send a long prompt to the token-recurrent kernel, several times
+ * slower there: leave them out where speed matters). It rounds the masked
  * products q.k and the entering state to bf16 before their second product when the output is
  * bf16, to pairs of bf16 (2^-16) when it is fp32, and the decayed v to such pairs for the fp32
  * state. An infinity or NaN in v reaches every output of its chunk in that (sequence, head), and

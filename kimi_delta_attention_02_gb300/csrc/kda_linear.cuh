@@ -115,7 +115,8 @@ struct LinearArgs {
 // kernel lets its successor begin once all its CTAs run, and a thread that reads what an earlier pass
 // wrote waits for that pass to have ended. Pass 3 only does so for segments that enter with the
 // workspace's states; sequences that are not cut, and first segments, run beside passes 1 and 2.
-// Every CTA waits before it ends, so that a pass never ends before an earlier one.
+// Every CTA that has a piece waits before it ends (idle ones return at once), and pass 3 always has some, a
+// last segment for each sequence, so that it never ends before an earlier pass; all CTAs of pass 2 wait.
 __device__ __forceinline__ void let_next_pass_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_earlier_passes() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <typename... P, typename... A>

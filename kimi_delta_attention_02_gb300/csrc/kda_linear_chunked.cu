@@ -43,8 +43,8 @@
 // thread) and write the output (one token and half the columns). Per chunk the tensor pipe runs
 // Q K^T, K^T V' (hi, lo), P V, Q S: 2560 cycles for 128 value columns; everything else runs beside.
 //
-// Measured (bf16, d = 128): T = 4096, 96 heads 110 us (3.8 TB/s, 57 % of the HBM copy rate, on the 96
-// SMs that have a chain; tensor pipe 62 % busy there); T = 65536, 16 heads 289 us (3.7 TB/s); 64 prompts
+// Measured (bf16, d = 128): T = 4096, 96 heads 109 us (3.8 TB/s, 57 % of the HBM copy rate, on the 96
+// SMs that have a chain; tensor pipe 63 % busy there); T = 65536, 16 heads 290 us (3.7 TB/s); 64 prompts
 // of 40 to 250 tokens, 16 heads 93 us. What bounds a chunk is the way from one state to the next (D to
 // registers, the bf16 tile, Q S, P V, the output), 3.3 us, against 1.3 us of MMAs and 1.9 us of HBM
 // traffic with 96 SMs at it; the output's row-per-thread stores keep the load/store pipe for a third of it.
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     raise_device_error(err_word, code);
     return false;
   };
-  // (T = 65536, 16 heads: 292 us with plain probes on the MMA warps, 310 without, 301 on all warps; a
+  // (T = 65536, 16 heads, in one run: 292 us with plain probes on the MMA warps, 310 without, 301 on all warps; a
   // failing probe takes 1 us, so kProbes are 2 s)
   auto wait_warp = [&](uint64_t &bar, uint32_t parity, uint32_t code) -> bool {
     if (warp == 1 || warp == 3) {  // the MMA warps: plain probes, shorter code

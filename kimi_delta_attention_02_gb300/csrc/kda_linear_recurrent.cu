@@ -9,8 +9,9 @@
 // through shared memory 16 tokens at a time (fp32), the next 16 waiting in registers. Two rows
 // go through one packed fp32 instruction: 3 per row pair, column and token (k v, decay,
 // read-out), which bound the kernel where it fills the SMs; with few heads the chain of tokens does,
-// 0.35 us each (prompts of 700 and 333 tokens, 6 heads of 100 x 72 in fp32: 45 us in segments; 128
-// sequences of 4 tokens and 64 heads of 64, bf16: 103 us, 2.6 TB/s of states).
+// 0.35 us each (prompts of 700 and 333 tokens, 6 heads of 100 x 72 in fp32: 43 us in segments; 128
+// sequences of 4 tokens and 64 heads of 64, bf16: 99 us, 2.7 TB/s of states; T = 4096, 96 heads of 128 in
+// fp32: 1.57 ms, of it 1.11 in pass 3, whose load/store pipe is 67 % busy, fp32 58 % and issue 47 %).
 #include <type_traits>
 
 #include "kda_linear.cuh"
