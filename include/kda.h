@@ -499,6 +499,124 @@ typedef struct kda_block_norm_params {
 kda_status kda_block_norm(const kda_block_norm_params *params, void *stream);
 
 /*
+ * The gated delta rule with one decay per head -- the recurrence at the top of this file with a
+ * scalar decay in place of the channel-wise one (the Gated DeltaNet row of the mapping table in
+ * Kimi K3 -- Architecture Notes, section 1.2). Per sequence and value head h, with the query / key
+ * head h / (H / H_k):
+ *
+ *     S_t = (I - beta_t k_t k_t^T) e^{g_t} S_{t-1} + beta_t k_t v_t^T ,    o_t = scale * S_t^T q_t
+ *
+ * kda_delta_prefill runs packed variable-length sequences, kda_delta_decode one token for B
+ * sequences. Layouts, alignment, aliasing, log_decay, the workspace and error rules are those of
+ * kda_linear_prefill and kda_linear_decode; what is added:
+ *
+ *   beta         [total_tokens, H] (decode: [B, H]) fp32, any finite value. With beta |k|^2 in
+ *                [0, 2] the state's norm only shrinks between writes; outside, the recurrence itself
+ *                grows from token to token, and so do the rounding errors of every kernel.
+ *
+ * Sizes: as kda_linear_prefill. Results are accumulated in fp32 and states are fp32.
+ */
+typedef struct kda_delta_prefill_params {
+  uint32_t struct_size;       /* sizeof the struct; any other value is KDA_ERR_INVALID_ARG   */
+  kda_dtype in_dtype, out_dtype;
+  int32_t num_seqs, H, H_k, d_k, d_v;
+  int32_t decay_per_token;    /* 1: log_decay [total_tokens, H], 0: [H]                      */
+  int32_t force_recurrent;
+  int64_t total_tokens;
+  const void *q, *k;          /* [total_tokens, H_k, d_k]                                    */
+  const void *v;              /* [total_tokens, H, d_v]                                      */
+  const float *log_decay;
+  const float *beta;          /* [total_tokens, H]                                           */
+  const int32_t *cu_seqlens;  /* [num_seqs + 1]                                              */
+  const float *init_state;    /* [num_seqs, H, d_k, d_v] or NULL                             */
+  void *out;                  /* [total_tokens, H, d_v], out_dtype                           */
+  float *final_state;         /* [num_seqs, H, d_k, d_v] or NULL; may equal init_state       */
+  void *workspace;            /* device scratch or NULL                                      */
+  size_t workspace_bytes;
+  float scale;
+} kda_delta_prefill_params;
+
+typedef struct kda_delta_decode_params {
+  uint32_t struct_size;
+  kda_dtype in_dtype, out_dtype;
+  int32_t B, H, H_k, d_k, d_v;
+  int32_t decay_per_token;    /* 1: log_decay [B, H], 0: [H]                                 */
+  float scale;
+  const void *q, *k;          /* [B, H_k, d_k]                                               */
+  const void *v;              /* [B, H, d_v]                                                 */
+  const float *log_decay;
+  const float *beta;          /* [B, H]                                                      */
+  float *state;               /* [B, H, d_k, d_v], updated in place                          */
+  void *out;                  /* [B, H, d_v], out_dtype                                      */
+} kda_delta_decode_params;
+
+kda_status kda_delta_prefill(const kda_delta_prefill_params *params, void *stream);
+kda_status kda_delta_decode(const kda_delta_decode_params *params, void *stream);
+
+/*
+ * Bytes of workspace kda_delta_prefill can use for these sizes (0: none). Pure host function, no
+ * CUDA call; the same arguments always give the same answer.
+ */
+size_t kda_delta_prefill_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t H_k,
+                                        int32_t d_k, int32_t d_v, kda_dtype in_dtype, kda_dtype out_dtype,
+                                        int32_t force_recurrent);
+
+/*
+ * kda_norm_rotate -- the norm of each query and key head, then rotary positions, in one pass: the
+ * input stage of a layer whose positions come from a rotation instead of kda_prologue's short
+ * convolution. Per token t and head, for each of q and k (x: one head's d channels):
+ *
+ *     n = weight (*) x / sqrt(mean(x^2) + eps)    KDA_NORM_RMS
+ *     n = x / sqrt(sum(x^2) + eps)                KDA_NORM_L2
+ *     n = x                                       KDA_NORM_NONE
+ *     y_a = n_a cos(p) - n_b sin(p),  y_b = n_b cos(p) + n_a sin(p),  p = position * inv_freq[i]
+ *
+ * for the channel pair (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) with interleaved = 1,
+ * i < rot_dim / 2; channels from rot_dim on pass as they are (y = n). position is that of token t on
+ * the axis pair_axis[i]: one axis for text, several (time, height, width) for images and video.
+ *
+ *   q, k          [tokens, H_q, d] and [tokens, H_k, d] in_dtype. Tokens lie q_stride (k_stride)
+ *                 elements apart, at least H d, so that parts of a fused projection's rows can be
+ *                 passed as they are; a head's channels and a token's heads are contiguous. k may
+ *                 be NULL (H_k = 0, k_out NULL).
+ *   positions     [num_axes, tokens], int32 or int64 (position_bytes 4 or 8), any value. Angles
+ *                 are formed in fixed point, as turns modulo one, and lose nothing at far positions.
+ *   inv_freq      [rot_dim / 2] fp32: radians per position of each pair
+ *   pair_axis     host array inside the struct: the axis of each pair, below num_axes
+ *   q_weight, k_weight  [d] fp32 or NULL (ones); only with KDA_NORM_RMS
+ *   q_out, k_out  as q and k, out_dtype, with strides of their own. Each may be its own input
+ *                 (same pointer, stride and dtype): the rotation is then in place.
+ *
+ * rot_dim = 0 norms only (positions and inv_freq NULL). Outputs overlap no input (their own
+ * excepted) and not each other; rows of a fused buffer that interleave without sharing an element do
+ * not overlap. Element alignment is enough for q, k and the outputs (2 or 4 bytes); rows that start
+ * on 16-byte boundaries with d a multiple of 8 are faster. Sizes: tokens >= 0, 1 <= d <= 256,
+ * rot_dim even and <= d, 1 <= num_axes <= 4, H_q >= 1. eps finite and >= 0; a row of zeros with
+ * eps = 0 gives NaN, as the formula does. Squares are summed in fp32.
+ */
+typedef enum { KDA_NORM_NONE = 0, KDA_NORM_RMS = 1, KDA_NORM_L2 = 2 } kda_norm_form;
+
+typedef struct kda_norm_rotate_params {
+  uint32_t struct_size;
+  kda_dtype in_dtype, out_dtype;
+  kda_norm_form norm;
+  int32_t H_q, H_k, d, rot_dim;
+  int32_t interleaved;
+  int32_t num_axes, position_bytes;
+  float eps;
+  int64_t tokens;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;  /* elements from token to token */
+  const void *q, *k;
+  const float *q_weight, *k_weight;
+  const void *positions;
+  const float *inv_freq;
+  void *q_out, *k_out;
+  uint8_t pair_axis[128];
+} kda_norm_rotate_params;
+
+kda_status kda_norm_rotate(const kda_norm_rotate_params *params, void *stream);
+
+/*
  * kda_check_device_error -- reads and clears the library's device error word in
  * one atomic exchange, enqueued on `stream` behind the work already there, then
  * synchronises `stream` and returns what the word held: KDA_OK, KDA_ERR_TIMEOUT

@@ -89,6 +89,45 @@ class BlockNormParams(ctypes.Structure):
                 ("pre_eps", ctypes.c_float)]
 
 
+class DeltaPrefillParams(ctypes.Structure):
+    """``kda_delta_prefill_params`` of include/kda.h, field for field."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("num_seqs", ctypes.c_int32), ("H", ctypes.c_int32), ("H_k", ctypes.c_int32), ("d_k", ctypes.c_int32),
+                ("d_v", ctypes.c_int32), ("decay_per_token", ctypes.c_int32), ("force_recurrent", ctypes.c_int32),
+                ("total_tokens", ctypes.c_int64), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("log_decay", ctypes.c_void_p), ("beta", ctypes.c_void_p),
+                ("cu_seqlens", ctypes.c_void_p), ("init_state", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("final_state", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t), ("scale", ctypes.c_float)]
+
+
+class DeltaDecodeParams(ctypes.Structure):
+    """``kda_delta_decode_params`` of include/kda.h, field for field."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("H_k", ctypes.c_int32), ("d_k", ctypes.c_int32),
+                ("d_v", ctypes.c_int32), ("decay_per_token", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("log_decay", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("state", ctypes.c_void_p),
+                ("out", ctypes.c_void_p)]
+
+
+KDA_NORM_NONE, KDA_NORM_RMS, KDA_NORM_L2 = 0, 1, 2
+_NORMS = {None: KDA_NORM_NONE, "rms": KDA_NORM_RMS, "l2": KDA_NORM_L2}
+
+
+class NormRotateParams(ctypes.Structure):
+    """``kda_norm_rotate_params`` of include/kda.h, field for field."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("H_q", ctypes.c_int32), ("H_k", ctypes.c_int32), ("d", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("position_bytes", ctypes.c_int32), ("eps", ctypes.c_float), ("tokens", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("k_out_stride", ctypes.c_int64), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+                ("pair_axis", ctypes.c_uint8 * 128)]
+
+
 class KdaError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -130,6 +169,14 @@ def _declare(lib):
     lib.kda_linear_prefill_workspace_size.restype = sz
     lib.kda_block_norm.argtypes = [ctypes.POINTER(BlockNormParams), vp]
     lib.kda_block_norm.restype = i32
+    lib.kda_delta_prefill.argtypes = [ctypes.POINTER(DeltaPrefillParams), vp]
+    lib.kda_delta_prefill.restype = i32
+    lib.kda_delta_decode.argtypes = [ctypes.POINTER(DeltaDecodeParams), vp]
+    lib.kda_delta_decode.restype = i32
+    lib.kda_delta_prefill_workspace_size.argtypes = [i64, i32, i32, i32, i32, i32, i32, i32, i32]
+    lib.kda_delta_prefill_workspace_size.restype = sz
+    lib.kda_norm_rotate.argtypes = [ctypes.POINTER(NormRotateParams), vp]
+    lib.kda_norm_rotate.restype = i32
     lib.kda_check_device_error.argtypes = [vp]
     lib.kda_check_device_error.restype = i32
     lib.kda_status_string.argtypes = [i32]
@@ -665,6 +712,198 @@ def block_norm(x, y=None, *, gate=None, post_norm: bool = False, post_weight=Non
     if st != KDA_OK:
         raise KdaError(st, "kda_block_norm")
     return (x if y is None and residual_out is None and want_residual else residual_out), out
+
+
+def delta_workspace_size(total_tokens: int, num_seqs: int, H: int, d_k: int = 128, d_v: int = 128,
+                         dtype=torch.bfloat16, out_dtype=torch.float32, recurrent: bool = False, H_k=None) -> int:
+    """Bytes of device scratch ``delta_prefill`` can use (``kda_delta_prefill_workspace_size``);
+    ``H_k`` query / key heads, H by default."""
+    return int(lib().kda_delta_prefill_workspace_size(int(total_tokens), int(num_seqs), int(H),
+                                                      int(H if H_k is None else H_k), int(d_k), int(d_v),
+                                                      _io_dtype(dtype), _io_dtype(out_dtype), int(bool(recurrent))))
+
+
+_DELTA_PREFILL_BYTES = ctypes.sizeof(DeltaPrefillParams)
+_DELTA_DECODE_BYTES = ctypes.sizeof(DeltaDecodeParams)
+_NORM_ROTATE_BYTES = ctypes.sizeof(NormRotateParams)
+_PairAxis = ctypes.c_uint8 * 128
+_NO_AXIS = _PairAxis()
+
+
+def delta_prefill(q, k, v, log_decay, beta, cu_seqlens, init_state=None, *, out=None, final_state=None,
+                  out_dtype=torch.float32, scale: float = 1.0, stream=None, recurrent: bool = False,
+                  want_final: bool = True, workspace="auto"):
+    """The gated delta rule with one decay per head over packed variable-length sequences
+    (``kda_delta_prefill``): S_t = (I - beta_t k_t k_t^T) e^{g_t} S_{t-1} + beta_t k_t v_t^T,
+    o_t = scale S_t^T q_t.
+
+    beta [T, H] float32; everything else as in ``linear_prefill``: q, k [T, H_k, d_k], v [T, H, d_v]
+    (bf16 or fp32, one dtype; value head h reads query / key head h // (H // H_k)); log_decay g
+    [T, H] or, constant, [H] float32; cu_seqlens [N+1] int32 (device); init_state [N, H, d_k, d_v]
+    float32 or None. Returns (out [T, H, d_v] in ``out_dtype`` (or out's dtype), final_state
+    [N, H, d_k, d_v] or None). ``recurrent=True`` forces the fp32 token-recurrent kernel.
+    ``workspace``: ``"auto"`` allocates what ``delta_workspace_size`` asks for, ``None`` passes none,
+    a uint8 CUDA tensor is passed as given."""
+    T, H_k, H, d_k, d_v = _linear_sizes(q, k, v, log_decay, "T")
+    _check_shape("beta", beta, (T, H), torch.float32)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.ndim != 1 or cu_seqlens.shape[0] < 1:
+        raise TypeError("cu_seqlens must be int32 [N + 1]")
+    N = cu_seqlens.shape[0] - 1
+    given = workspace if isinstance(workspace, torch.Tensor) else None
+    device = _one_device(q, k, v, log_decay, beta, cu_seqlens, init_state, out, final_state, given)
+    if device != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return delta_prefill(q, k, v, log_decay, beta, cu_seqlens, init_state, out=out, final_state=final_state,
+                                 out_dtype=out_dtype, scale=scale, stream=stream, recurrent=recurrent,
+                                 want_final=want_final, workspace=workspace)
+    state_shape = (N, H, d_k, d_v)
+    if init_state is not None:
+        _check_shape("init_state", init_state, state_shape, torch.float32)
+    if out is None:
+        out = _empty((T, H, d_v), out_dtype, q.device, stream)
+    else:
+        _check_shape("out", out, (T, H, d_v))
+    if final_state is not None:
+        _check_shape("final_state", final_state, state_shape, torch.float32)
+    elif want_final:
+        final_state = _empty(state_shape, torch.float32, q.device, stream)
+    dt, odt, rec = _io_dtype(q.dtype), _io_dtype(out.dtype), 1 if recurrent else 0
+    handle = lib()
+    if given is None and workspace is not None:
+        if workspace != "auto":
+            raise ValueError("workspace must be 'auto', None or a uint8 CUDA tensor")
+        n = handle.kda_delta_prefill_workspace_size(T, N, H, H_k, d_k, d_v, dt, odt, rec)
+        if n:
+            given = _empty(n, torch.uint8, q.device, stream, returned=False)
+    p = DeltaPrefillParams(_DELTA_PREFILL_BYTES, dt, odt, N, H, H_k, d_k, d_v, 1 if log_decay.ndim == 2 else 0, rec, T,
+                           q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), beta.data_ptr(),
+                           cu_seqlens.data_ptr(), _address(init_state), out.data_ptr(), _address(final_state),
+                           _address(given), 0 if given is None else given.numel() * given.element_size(), scale)
+    st = handle.kda_delta_prefill(ctypes.byref(p), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_delta_prefill")
+    return out, final_state
+
+
+def delta_decode(q, k, v, log_decay, beta, state, *, out=None, out_dtype=torch.float32, scale: float = 1.0,
+                 stream=None):
+    """One token of the gated delta rule with one decay per head for B sequences
+    (``kda_delta_decode``); ``state`` [B, H, d_k, d_v] float32 is updated in place.
+    q, k [B, H_k, d_k], v [B, H, d_v], log_decay [B, H] or [H], beta [B, H]. Returns out [B, H, d_v]."""
+    B, H_k, H, d_k, d_v = _linear_sizes(q, k, v, log_decay, "B")
+    device = _one_device(q, k, v, log_decay, beta, state, out)
+    _check_shape("beta", beta, (B, H), torch.float32)
+    _check_shape("state", state, (B, H, d_k, d_v), torch.float32)
+    if device != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return delta_decode(q, k, v, log_decay, beta, state, out=out, out_dtype=out_dtype, scale=scale,
+                                stream=stream)
+    if out is None:
+        out = _empty((B, H, d_v), out_dtype, q.device, stream)
+    else:
+        _check_shape("out", out, (B, H, d_v))
+    p = DeltaDecodeParams(_DELTA_DECODE_BYTES, _io_dtype(q.dtype), _io_dtype(out.dtype), B, H, H_k, d_k, d_v,
+                          1 if log_decay.ndim == 2 else 0, scale, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                          log_decay.data_ptr(), beta.data_ptr(), state.data_ptr(), out.data_ptr())
+    st = lib().kda_delta_decode(ctypes.byref(p), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_delta_decode")
+    return out
+
+
+def _heads_of_rows(name, x):
+    """The token stride of [T, heads, d] whose heads and channels are contiguous (a part of a fused
+    projection's rows, or a whole tensor)."""
+    T, H, d = x.shape
+    if (d > 1 and x.stride(2) != 1) or (H > 1 and x.stride(1) != d):
+        raise ValueError(f"{name}: a token's heads and channels must be contiguous")
+    return x.stride(0) if T > 1 else H * d
+
+
+def norm_rotate(q, k, positions, inv_freq, *, norm="rms", q_weight=None, k_weight=None, eps: float = 1e-6,
+                interleaved: bool = False, pair_axis=None, q_out=None, k_out=None, out_dtype=None, stream=None):
+    """The norm of each query and key head, then rotary positions, in one pass (``kda_norm_rotate``):
+    n = weight * x / sqrt(mean(x^2) + eps) (``norm="rms"``), x / sqrt(sum(x^2) + eps) (``"l2"``) or x
+    (None); then channel pair i of the first 2 * len(inv_freq) channels, (i, i + len(inv_freq)) or,
+    ``interleaved``, (2 i, 2 i + 1), turns by position * inv_freq[i].
+
+    q [T, H_q, d], k [T, H_k, d] or None, bf16 or fp32, one dtype; tokens may lie further apart than
+    H * d elements (parts of a fused projection's rows). positions int32 or int64, [T] or, for several
+    axes, [A, T] with ``pair_axis``, the axis of each pair (a sequence of ints). inv_freq [rot / 2]
+    float32, or positions and inv_freq None: no rotation. Weights [d] float32 or None (ones), with
+    "rms" only. Returns (q', k' or None) in ``out_dtype`` (the dtype of q by default) or in q_out and
+    k_out, which may be q and k themselves."""
+    if q.ndim != 3 or (k is not None and (k.ndim != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2])):
+        raise ValueError("q must be [T, H_q, d] and k [T, H_k, d]")
+    T, H_q, d = q.shape
+    H_k = 0 if k is None else k.shape[1]
+    if k is not None and (H_k < 1 or k.dtype != q.dtype):
+        raise TypeError("q and k must share one dtype, k with a head at least")
+    if norm not in _NORMS:
+        raise ValueError("norm must be 'rms', 'l2' or None")
+    for w in (q_weight, k_weight):
+        if w is not None:
+            _check_shape("a weight", w, (d,), torch.float32)
+    if k is None and (k_weight is not None or k_out is not None):
+        raise ValueError("k_weight and k_out belong to k")
+    half, axes, size = 0, 1, 8
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq belong together")
+    if inv_freq is not None:
+        if inv_freq.ndim != 1 or inv_freq.dtype != torch.float32:
+            raise TypeError("inv_freq must be float32 [rot / 2]")
+        half = inv_freq.shape[0]
+        if 2 * half > min(d, 256):
+            raise ValueError("inv_freq has more pairs than a head has channels for")
+        if positions.dtype != torch.int64 and positions.dtype != torch.int32:
+            raise TypeError("positions must be int32 or int64")
+        size = positions.element_size()
+        if positions.ndim == 2 and pair_axis is not None:
+            axes = positions.shape[0]
+        if positions.shape != ((T,) if pair_axis is None else (axes, T)) or axes < 1:
+            raise ValueError("positions must be [T], or [A, T] with pair_axis")
+    axis_of = _NO_AXIS
+    if pair_axis is not None:
+        if len(pair_axis) != half:
+            raise ValueError("pair_axis must name an axis for each pair of inv_freq")
+        if half and not 0 <= min(pair_axis) <= max(pair_axis) < min(axes, 256):
+            raise ValueError("pair_axis names an axis that positions does not have")
+        axis_of = _PairAxis.from_buffer_copy(bytes(pair_axis).ljust(128, b"\0"))
+    device = _one_device(positions, inv_freq, q_weight, k_weight)
+    for t in (q, k, q_out, k_out):
+        if t is not None:
+            at = t.get_device()
+            if at < 0 or (device >= 0 and at != device):
+                raise ValueError("KDA tensors must be on one CUDA device")
+            device = at
+    if device != torch._C._cuda_getDevice():
+        with torch.cuda.device(device):
+            return norm_rotate(q, k, positions, inv_freq, norm=norm, q_weight=q_weight, k_weight=k_weight, eps=eps,
+                               interleaved=interleaved, pair_axis=pair_axis, q_out=q_out, k_out=k_out,
+                               out_dtype=out_dtype, stream=stream)
+    dtype = out_dtype or q.dtype
+    for name, x in (("q_out", q_out), ("k_out", k_out)):
+        if x is not None:
+            _check_shape(name, x, q.shape if name == "q_out" else k.shape)
+            if out_dtype is not None and x.dtype != out_dtype:
+                raise TypeError(f"{name} must be {out_dtype}")
+            dtype = x.dtype
+    if q_out is None:
+        q_out = _empty(q.shape, dtype, q.device, stream)
+    if k is not None and k_out is None:
+        k_out = _empty(k.shape, dtype, k.device, stream)
+    if k is not None and k_out.dtype != q_out.dtype:
+        raise TypeError("q_out and k_out must share one dtype")
+    p = NormRotateParams(_NORM_ROTATE_BYTES, _io_dtype(q.dtype), _io_dtype(q_out.dtype), _NORMS[norm], H_q, H_k, d,
+                         2 * half, 1 if interleaved else 0, axes, size, eps, T, _heads_of_rows("q", q),
+                         0 if k is None else _heads_of_rows("k", k), _heads_of_rows("q_out", q_out),
+                         0 if k is None else _heads_of_rows("k_out", k_out), q.data_ptr(), _address(k),
+                         _address(q_weight), _address(k_weight), _address(positions), _address(inv_freq),
+                         q_out.data_ptr(), _address(k_out), axis_of)
+    st = lib().kda_norm_rotate(ctypes.byref(p), _stream_handle(stream))
+    if st != KDA_OK:
+        raise KdaError(st, "kda_norm_rotate")
+    return q_out, k_out
 
 
 def check_device_error(stream=None):

@@ -5,7 +5,9 @@
 
 #include "kda_block_norm.h"
 #include "kda_common.cuh"
+#include "kda_delta.cuh"
 #include "kda_linear.cuh"
+#include "kda_norm_rotate.h"
 
 #include <atomic>
 #include <mutex>
@@ -311,6 +313,21 @@ bool outputs_clear(const Range *outs, int n_out, const Range *ins, int n_in) {
   return true;
 }
 
+// A tensor's rows, one per token, `stride` bytes apart (at least `bytes`). Two such tensors of T tokens
+// may lie inside each other's range, like the parts of a fused projection: with one stride they share
+// a byte only if some row of one meets a row of the other.
+struct Rows {
+  const void *p;
+  int64_t bytes, stride;
+};
+bool rows_overlap(const Rows &x, const Rows &y, int64_t T) {
+  if (!overlaps(x.p, size_t((T - 1) * x.stride + x.bytes), y.p, size_t((T - 1) * y.stride + y.bytes))) return false;
+  if (x.stride != y.stride) return true;
+  const int64_t between = reinterpret_cast<intptr_t>(y.p) - reinterpret_cast<intptr_t>(x.p);
+  const int64_t off = ((between % x.stride) + x.stride) % x.stride;
+  return !(off >= x.bytes && off + y.bytes <= x.stride);
+}
+
 }  // namespace
 }  // namespace kda
 
@@ -570,6 +587,138 @@ kda_status kda_block_norm(const kda_block_norm_params *p, void *stream) {
   a.scale = p->scale, a.post_eps = p->post_eps, a.pre_eps = p->pre_eps;
   const cudaError_t err = launch_block_norm(a, p->x_dtype == KDA_BF16, p->y_dtype == KDA_BF16,
                                             p->out_dtype == KDA_BF16, static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_delta_prefill_workspace_size(int64_t total_tokens, int32_t num_seqs, int32_t H, int32_t H_k, int32_t d_k,
+                                        int32_t d_v, kda_dtype in_dtype, kda_dtype out_dtype,
+                                        int32_t force_recurrent) {
+  (void)force_recurrent;
+  if (check_linear_sizes(total_tokens, num_seqs, H, H_k, d_k, d_v, 1, in_dtype, out_dtype) != KDA_OK) return 0;
+  return 0;
+}
+
+kda_status kda_delta_prefill(const kda_delta_prefill_params *p, void *stream) {
+  if (p == nullptr || p->struct_size != sizeof(kda_delta_prefill_params)) return KDA_ERR_INVALID_ARG;
+  const kda_status st = check_linear_sizes(p->total_tokens, p->num_seqs, p->H, p->H_k, p->d_k, p->d_v,
+                                           p->decay_per_token, p->in_dtype, p->out_dtype);
+  if (st != KDA_OK) return st;
+  const int64_t T = p->total_tokens;
+  if (T > 0 && p->num_seqs == 0) return KDA_ERR_INVALID_ARG;
+  if (p->cu_seqlens == nullptr || !aligned4(p->cu_seqlens)) return KDA_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (!p->q || !p->k || !p->v || !p->log_decay || !p->beta || !p->out) return KDA_ERR_INVALID_ARG;
+    if (!aligned16(p->q) || !aligned16(p->k) || !aligned16(p->v) || !aligned16(p->out) || !aligned4(p->log_decay) ||
+        !aligned4(p->beta))
+      return KDA_ERR_INVALID_ARG;
+  }
+  if (!aligned16(p->init_state) || !aligned16(p->final_state)) return KDA_ERR_INVALID_ARG;
+  if ((p->workspace == nullptr) != (p->workspace_bytes == 0) || !aligned16(p->workspace)) return KDA_ERR_INVALID_ARG;
+  const size_t es = p->in_dtype == KDA_BF16 ? 2 : 4, eo = p->out_dtype == KDA_BF16 ? 2 : 4;
+  const size_t nk = size_t(T) * p->H_k * p->d_k * es, nv = size_t(T) * p->H * p->d_v;
+  const size_t ns = size_t(p->num_seqs) * p->H * p->d_k * p->d_v * 4;
+  const bool in_place = p->final_state != nullptr && p->final_state == p->init_state;
+  const Range ins[7] = {{p->q, nk}, {p->k, nk}, {p->v, nv * es},
+                        {p->log_decay, size_t(p->decay_per_token ? T : 1) * p->H * 4}, {p->beta, size_t(T) * p->H * 4},
+                        {p->cu_seqlens, (size_t(p->num_seqs) + 1) * 4}, {in_place ? nullptr : p->init_state, ns}};
+  const Range outs[3] = {{p->out, nv * eo}, {p->final_state, ns}, {p->workspace, p->workspace_bytes}};
+  if (!outputs_clear(outs, 3, ins, 7)) return KDA_ERR_INVALID_ARG;
+  if (p->num_seqs == 0) return KDA_OK;
+  if (T == 0 && p->final_state == nullptr) return KDA_OK;
+
+  DeltaArgs a{};
+  a.q = p->q, a.k = p->k, a.v = p->v, a.log_decay = p->log_decay, a.beta = p->beta, a.cu = p->cu_seqlens;
+  a.init_state = p->init_state, a.out = p->out, a.final_state = p->final_state;
+  a.num_seqs = p->num_seqs, a.H = p->H, a.H_k = p->H_k, a.d_k = p->d_k, a.d_v = p->d_v;
+  a.per_token = p->decay_per_token, a.total = T, a.scale = p->scale;
+  const cudaError_t err = launch_delta_recurrent(a, p->in_dtype == KDA_BF16, p->out_dtype == KDA_BF16,
+                                                 static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_delta_decode(const kda_delta_decode_params *p, void *stream) {
+  if (p == nullptr || p->struct_size != sizeof(kda_delta_decode_params)) return KDA_ERR_INVALID_ARG;
+  if (p->B < 1) return KDA_ERR_INVALID_ARG;
+  const kda_status st =
+      check_linear_sizes(p->B, p->B, p->H, p->H_k, p->d_k, p->d_v, p->decay_per_token, p->in_dtype, p->out_dtype);
+  if (st != KDA_OK) return st;
+  if (!p->q || !p->k || !p->v || !p->log_decay || !p->beta || !p->state || !p->out) return KDA_ERR_INVALID_ARG;
+  if (!aligned16(p->q) || !aligned16(p->k) || !aligned16(p->v) || !aligned16(p->state) || !aligned16(p->out) ||
+      !aligned4(p->log_decay) || !aligned4(p->beta))
+    return KDA_ERR_INVALID_ARG;
+  const size_t es = p->in_dtype == KDA_BF16 ? 2 : 4, eo = p->out_dtype == KDA_BF16 ? 2 : 4;
+  const size_t nk = size_t(p->B) * p->H_k * p->d_k * es, nv = size_t(p->B) * p->H * p->d_v;
+  const Range ins[5] = {{p->q, nk}, {p->k, nk}, {p->v, nv * es},
+                        {p->log_decay, size_t(p->decay_per_token ? p->B : 1) * p->H * 4},
+                        {p->beta, size_t(p->B) * p->H * 4}};
+  const Range outs[2] = {{p->out, nv * eo}, {p->state, nv * p->d_k * 4}};
+  if (!outputs_clear(outs, 2, ins, 5)) return KDA_ERR_INVALID_ARG;
+  const cudaError_t err =
+      launch_delta_decode(p->q, p->k, p->v, p->log_decay, p->decay_per_token != 0, p->beta, p->state, p->out, p->B,
+                          p->H, p->H_k, p->d_k, p->d_v, p->in_dtype == KDA_BF16, p->out_dtype == KDA_BF16, p->scale,
+                          static_cast<cudaStream_t>(stream));
+  return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+kda_status kda_norm_rotate(const kda_norm_rotate_params *p, void *stream) {
+  if (p == nullptr || p->struct_size != sizeof(kda_norm_rotate_params)) return KDA_ERR_INVALID_ARG;
+  if (!valid_dtype(p->in_dtype) || !valid_dtype(p->out_dtype)) return KDA_ERR_INVALID_ARG;
+  if (p->norm != KDA_NORM_NONE && p->norm != KDA_NORM_RMS && p->norm != KDA_NORM_L2) return KDA_ERR_INVALID_ARG;
+  if (p->tokens < 0 || p->H_q < 1 || p->H_k < 0 || p->d < 1) return KDA_ERR_INVALID_ARG;
+  if (p->rot_dim < 0 || p->rot_dim > p->d || p->rot_dim % 2 != 0) return KDA_ERR_INVALID_ARG;
+  if ((p->interleaved != 0 && p->interleaved != 1) || !finite_nonneg(p->eps)) return KDA_ERR_INVALID_ARG;
+  if (p->d > kRotateMaxD || p->num_axes > kRotateMaxAxes || p->tokens > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  const int half = p->rot_dim / 2;
+  if (half > 0) {
+    if (p->num_axes < 1 || (p->position_bytes != 4 && p->position_bytes != 8)) return KDA_ERR_INVALID_ARG;
+    for (int i = 0; i < half; ++i)
+      if (p->pair_axis[i] >= p->num_axes) return KDA_ERR_INVALID_ARG;
+  }
+  if (p->norm != KDA_NORM_RMS && (p->q_weight != nullptr || p->k_weight != nullptr)) return KDA_ERR_INVALID_ARG;
+  if ((p->H_k == 0) != (p->k == nullptr && p->k_out == nullptr)) return KDA_ERR_INVALID_ARG;
+  const int64_t wq = int64_t(p->H_q) * p->d, wk = int64_t(p->H_k) * p->d;
+  if (p->q_stride < wq || p->q_out_stride < wq || p->k_stride < wk || p->k_out_stride < wk) return KDA_ERR_INVALID_ARG;
+  const int64_t most = INT64_MAX / 16 / (p->tokens > 0 ? p->tokens : 1);  // bytes of a tensor
+  if (p->q_stride > most || p->q_out_stride > most || p->k_stride > most || p->k_out_stride > most)
+    return KDA_ERR_UNSUPPORTED;
+  if (p->tokens == 0) return KDA_OK;
+  const int64_t ei = p->in_dtype == KDA_BF16 ? 2 : 4, eo = p->out_dtype == KDA_BF16 ? 2 : 4;
+  const auto aligned = [](const void *x, int64_t bytes) { return reinterpret_cast<uintptr_t>(x) % uintptr_t(bytes) == 0; };
+  if (p->q == nullptr || p->q_out == nullptr || (p->H_k > 0 && (p->k == nullptr || p->k_out == nullptr)))
+    return KDA_ERR_INVALID_ARG;
+  if (half > 0 && (p->positions == nullptr || p->inv_freq == nullptr || !aligned(p->positions, p->position_bytes)))
+    return KDA_ERR_INVALID_ARG;
+  if (!aligned(p->q, ei) || !aligned(p->k, ei) || !aligned(p->q_out, eo) || !aligned(p->k_out, eo) ||
+      !aligned4(p->q_weight) || !aligned4(p->k_weight) || !aligned4(p->inv_freq))
+    return KDA_ERR_INVALID_ARG;
+  // rows of a token, in bytes: outputs share none with inputs (their own in place excepted) or each other
+  const Rows q{p->q, wq * ei, p->q_stride * ei}, k{p->k, wk * ei, p->k_stride * ei};
+  const Rows qo{p->q_out, wq * eo, p->q_out_stride * eo}, ko{p->k_out, wk * eo, p->k_out_stride * eo};
+  const auto same = [&](const Rows &x, const Rows &y) { return x.p == y.p && x.stride == y.stride && ei == eo; };
+  const int64_t T = p->tokens;
+  if (!same(q, qo) && rows_overlap(q, qo, T)) return KDA_ERR_INVALID_ARG;
+  if (p->H_k > 0) {
+    if (!same(k, ko) && rows_overlap(k, ko, T)) return KDA_ERR_INVALID_ARG;
+    if (rows_overlap(q, ko, T) || rows_overlap(k, qo, T) || rows_overlap(qo, ko, T)) return KDA_ERR_INVALID_ARG;
+  }
+  const Range small[4] = {{p->q_weight, size_t(p->d) * 4}, {p->k_weight, size_t(p->d) * 4},
+                          {half > 0 ? p->positions : nullptr, size_t(p->num_axes) * T * p->position_bytes},
+                          {half > 0 ? p->inv_freq : nullptr, size_t(half) * 4}};
+  const Range outs[2] = {{p->q_out, size_t((T - 1) * qo.stride + qo.bytes)},
+                         {p->k_out, size_t(p->H_k > 0 ? (T - 1) * ko.stride + ko.bytes : 0)}};
+  for (const Range &o : outs)
+    for (const Range &i : small)
+      if (overlaps(o.p, o.bytes, i.p, i.bytes)) return KDA_ERR_INVALID_ARG;
+  RotateArgs a{};
+  a.x[0] = p->q, a.x[1] = p->k, a.out[0] = p->q_out, a.out[1] = p->k_out;
+  a.weight[0] = p->q_weight, a.weight[1] = p->k_weight;
+  a.stride[0] = p->q_stride, a.stride[1] = p->k_stride, a.out_stride[0] = p->q_out_stride, a.out_stride[1] = p->k_out_stride;
+  a.heads[0] = p->H_q, a.heads[1] = p->H_k;
+  a.positions = p->positions, a.inv_freq = p->inv_freq, a.tokens = T;
+  a.d = p->d, a.half = half, a.norm = int(p->norm), a.pos64 = p->position_bytes == 8, a.eps = p->eps;
+  for (int i = 0; i < half; ++i) a.axis[i] = p->pair_axis[i];
+  const cudaError_t err = launch_norm_rotate(a, p->in_dtype == KDA_BF16, p->out_dtype == KDA_BF16, p->interleaved != 0,
+                                             static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

@@ -82,21 +82,6 @@ __global__ void __launch_bounds__(kThr, 3) linear_recurrent_kernel(const LinearA
     }
     if (tid < kTok) rg_ = t + tid < s.t1 ? a.log_decay[a.per_token ? (t + tid) * a.H + h : h] : 0.f;
   };
-  // The factor of a token's decay, e^g in fp32. Simply rounded, the factors of a constant decay would
-  // all be off the same way, which a memory of thousands of tokens adds up. So the token takes a whole
-  // ulp more or less where `rest`, what one rounding loses in ulps, times the tokens so far passes a
-  // half: factors of a constant decay stay within an ulp of e to the sum, others round either way
-  // without a bias. (Decay's choice between two forms, made in the loop over rows, costs 2.07 ms at
-  // T = 4096, 96 heads of 128 in fp32; this 1.57.)
-  auto factor = [&](float g, int64_t t) {
-    const Decay d = decay_of(g);
-    if (!d.keep) return d.c;  // e^g below one half: no memory to drift
-    const float e = 1.f + d.c;
-    const uint32_t exponent = __float_as_uint(e) & 0x7f800000u;  // an ulp is 2^-23 of its power of two
-    const float rest = (d.c - (e - 1.f)) * __uint_as_float(0x8a800000u - exponent);
-    const float n = float((t - s.t0) & 4095);
-    return fmaf(rintf((n + 1.f) * rest) - rintf(n * rest), __uint_as_float(exponent - 0x0b800000u), e);
-  };
   auto stage = [&](int b, int64_t t) {
     if (tid < 4 * kRows) {
 #pragma unroll
@@ -108,7 +93,7 @@ __global__ void __launch_bounds__(kThr, 3) linear_recurrent_kernel(const LinearA
 #pragma unroll
     for (int i = 0; i < kTok * kCols / kThr; ++i) s_v[b][2 * i + (tid >> 6)][tid & 63] = value(rv[i]);
     if (tid < kTok) {
-      s_e[b][tid] = factor(rg_, t + tid);
+      s_e[b][tid] = unbiased_decay(rg_, t + tid - s.t0);
       if constexpr (kStateOnly) s_g[b][tid] = rg_;
     }
   };

@@ -25,6 +25,8 @@ Notes, section 1.1 "Kimi Delta Attention"):
   L2 norm of q and k), with per-sequence convolution states, in numpy fp64.
 * ``linear``   -- linear attention with one decay per head (the recurrence without
   the delta rule) and the residual block norm, in numpy fp64.
+* ``delta``    -- the gated delta rule with one decay per head, and the norm and rotation of
+  queries and keys, in numpy fp64.
 
 Parity status: every function here is pinned by the ``-m "not gpu"`` tests
 (exact brute force, closed forms, invariants, recurrent/chunked agreement and
@@ -39,3 +41,4 @@ from .exact import kda_exact  # noqa: F401
 from .epilogue import output_gate_rmsnorm, EPILOGUE_MUTATIONS  # noqa: F401
 from .prologue import kda_prologue, short_conv, PROLOGUE_MUTATIONS  # noqa: F401
 from .linear import linear_recurrent, block_norm  # noqa: F401
+from .delta import delta_recurrent, norm_rotate  # noqa: F401
