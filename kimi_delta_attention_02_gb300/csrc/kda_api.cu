@@ -723,6 +723,7 @@ kda_status kda_norm_rotate(const kda_norm_rotate_params *p, void *stream) {
   a.heads[0] = p->H_q, a.heads[1] = p->H_k;
   a.positions = p->positions, a.inv_freq = p->inv_freq, a.tokens = T;
   a.d = p->d, a.half = half, a.norm = int(p->norm), a.pos64 = p->position_bytes == 8, a.eps = p->eps;
+  a.per = p->norm == KDA_NORM_RMS ? 1.f / float(p->d) : 1.f;
   for (int i = 0; i < half; ++i) a.axis[i] = p->pair_axis[i];
   const cudaError_t err = launch_norm_rotate(a, p->in_dtype == KDA_BF16, p->out_dtype == KDA_BF16, p->interleaved != 0,
                                              static_cast<cudaStream_t>(stream));

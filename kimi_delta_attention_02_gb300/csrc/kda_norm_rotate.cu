@@ -3,14 +3,16 @@
 // one), a = w cos p and b = -+ w_partner sin p of the token's angles, which all heads share.
 //
 // Reads and writes q and k once at about 7 flops per element: bound by HBM bandwidth. The angles of a
-// token are formed once per CTA, in shared memory; a row's lanes then keep a and b of their channels
-// in registers while they go through the token's heads.
+// token are formed once per CTA, in shared memory. A head row takes as many lanes as it has pieces of 8
+// channels (the next power of two), so that a warp works on up to 32 rows at once, and a lane keeps the
+// angles of its channels in registers while it goes through the token's heads, two at a time. A turned
+// channel's partner is in the same lane (neighbours) or comes by a second load, which finds its line in L1.
 //
 // Angles. p = position * f can be millions of radians, where fp32 is off by tenths. A turn is a number
-// modulo one: F = f / (2 pi) modulo one as a 64-bit fraction (formed in fp64, off by 2^-53 of itself, so
-// the angle is off by 2^-53 of itself too), and the wrapping 64-bit product position * F is the angle's
-// fraction of a turn whatever the position, negative ones among them. Its top 32 bits, as a signed number
-// of half turns, go to sincospi: off by 2^-32 of a turn.
+// modulo one: F = f / (2 pi) modulo one as a 64-bit fraction (off by 2^-63 while f is below 2^24), and the
+// wrapping 64-bit product position * F is the angle's fraction of a turn whatever the position, negative
+// ones among them (off by position 2^-63). Its top 32 bits, as a signed number of half turns, go to
+// sincospi: off by 2^-32 of a turn.
 #include "kda_common.cuh"
 #include "kda_norm_rotate.h"
 
@@ -19,6 +21,202 @@ namespace {
 
 constexpr int kThr = 256;
 
+// The angle of pair i at token t as (cos, sin); `turns` is the pair's F.
+__device__ __forceinline__ uint64_t turns_per_position(float inv_freq) {
+  // |f| = m 2^-s with a whole m, times 1 / (2 pi) as 128 bits behind the point; all in integers
+  const uint32_t bits = __float_as_uint(inv_freq) & 0x7fffffffu, exponent = bits >> 23;
+  const uint64_t m = (bits & 0x7fffffu) | (exponent != 0 ? 0x800000u : 0u);
+  const int s = 150 - int(exponent != 0 ? exponent : 1);
+  constexpr uint64_t k1 = 0x28be60db9391054aull, k0 = 0x7f09d5f47d4d3770ull;  // 1 / (2 pi)
+  const uint64_t low = m * k1 + __umul64hi(m, k0), high = __umul64hi(m, k1) + (low < m * k1);  // m / (2 pi) 2^64
+  uint64_t f = s <= 0 ? (s > -64 ? low << -s : 0) : s < 64 ? (low >> s) | (high << (64 - s)) : s < 128 ? high >> (s - 64) : 0;
+  return inv_freq < 0.f ? uint64_t(0) - f : f;
+}
+__device__ __forceinline__ float2 angle(const RotateArgs &a, int i, int64_t t, uint64_t turns) {
+  const int64_t at = a.axis[i] * a.tokens + t;
+  const int64_t pos = a.pos64 ? static_cast<const int64_t *>(a.positions)[at]
+                              : int64_t(static_cast<const int32_t *>(a.positions)[at]);
+  const int32_t turn = int32_t((uint64_t(pos) * turns) >> 32);
+  float s, c;
+  sincospif(float(turn) * 0x1p-31f, &s, &c);
+  if (!isfinite(a.inv_freq[i])) s = c = __int_as_float(0x7fc00000);
+  return make_float2(c, s);
+}
+__device__ __forceinline__ float norm_factor(const RotateArgs &a, float sum) {
+  return a.norm == KDA_NORM_NONE ? 1.f : rsqrtf(fmaf(sum, a.per, a.eps));
+}
+
+// 8 channels as stored: N 16-byte words
+template <bool kBF16>
+struct Piece {
+  uint4 w[kBF16 ? 1 : 2];
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (kBF16) {
+      const float2 p[4] = {unpack_bf16x2(w[0].x), unpack_bf16x2(w[0].y), unpack_bf16x2(w[0].z), unpack_bf16x2(w[0].w)};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[2 * e] = p[e].x, x[2 * e + 1] = p[e].y;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        x[4 * e] = __uint_as_float(w[e].x), x[4 * e + 1] = __uint_as_float(w[e].y);
+        x[4 * e + 2] = __uint_as_float(w[e].z), x[4 * e + 3] = __uint_as_float(w[e].w);
+      }
+    }
+  }
+};
+// kN neighbouring elements at an address aligned to them
+template <bool kBF16, int kN>
+__device__ __forceinline__ void load_part(const void *base, int64_t at, float *x) {
+  if constexpr (kBF16 && kN == 8) {
+    Piece<true> p;
+    p.w[0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
+    float y[8];
+    p.get(y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = y[e];
+  } else if constexpr (!kBF16 && kN == 8) {
+    load_part<false, 4>(base, at, x);
+    load_part<false, 4>(base, at + 4, x + 4);
+  } else if constexpr (kBF16 && kN == 4) {
+    const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(base) + at);
+    const float2 a = unpack_bf16x2(w.x), b = unpack_bf16x2(w.y);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+  } else if constexpr (!kBF16 && kN == 4) {
+    const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
+    x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+  } else if constexpr (kBF16 && kN == 2) {
+    const float2 a = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + at));
+    x[0] = a.x, x[1] = a.y;
+  } else if constexpr (!kBF16 && kN == 2) {
+    const float2 w = *reinterpret_cast<const float2 *>(static_cast<const float *>(base) + at);
+    x[0] = w.x, x[1] = w.y;
+  } else {
+    x[0] = load_elem<kBF16>(base, at);
+  }
+}
+
+// Rows of whole pieces of 8 channels on 16-byte boundaries, each of which turns as a whole or not at all.
+// kPart: partners are neighbours (0), or lie rot / 2 channels away: whole pieces (8) come from their lane,
+// half pieces (4) by a load. `lanes` threads per row, `group` rows of a token side by side, so
+// kThr / (lanes group) tokens at a time; `pairs` threads form a token's angles.
+template <bool kInBF16, bool kOutBF16, int kPart>
+__global__ void __launch_bounds__(kThr, kInBF16 ? 4 : 3) rotate_kernel(const RotateArgs a, int lanes, int group, int pairs) {
+  constexpr int kEi = kInBF16 ? 2 : 4, kEo = kOutBF16 ? 2 : 4;
+  __shared__ uint64_t s_turn[kRotateMaxD / 2];
+  __shared__ __align__(16) float2 s_cs[2][kThr * 4];  // tokens x rot / 2: a row has at most 8 channels per lane
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int slot = tid / lanes, tokens = kThr / (lanes * group), token = slot / group;
+  const int c0 = 8 * (tid % lanes), first = slot % group + group * blockIdx.y, stride = group * gridDim.y;
+  const bool turns = c0 < 2 * a.half, upper = c0 >= a.half;
+  const int partner = turns ? (upper ? c0 - a.half : c0 + a.half) : c0;  // of a whole piece, and its lane
+  const int from_lane = lane + (partner - c0) / 8;
+  for (int i = tid; i < a.half; i += kThr) s_turn[i] = turns_per_position(a.inv_freq[i]);
+  __syncthreads();
+  int buf = 0;
+#pragma unroll 1
+  for (int64_t t0 = int64_t(blockIdx.x) * tokens; t0 < a.tokens; t0 += int64_t(gridDim.x) * tokens, buf ^= 1) {
+    const int here = a.tokens - t0 < tokens ? int(a.tokens - t0) : tokens;
+    const int64_t t = t0 + token;
+    const bool mine = c0 < a.d && token < here;
+    // the first row is on its way while the angles are formed
+    const uint8_t *src;
+    Piece<kInBF16> next{};
+    auto fetch = [&](bool ok) {
+      if (ok) {
+#pragma unroll
+        for (int e = 0; e < kEi / 2; ++e) next.w[e] = reinterpret_cast<const uint4 *>(src + c0 * kEi)[e];
+      }
+    };
+    src = static_cast<const uint8_t *>(a.x[0]) + (t * a.stride[0] + int64_t(first) * a.d) * kEi;
+    fetch(mine && first < a.heads[0]);
+    const int p = tid & (pairs - 1);
+#pragma unroll 1
+    for (int i = tid / pairs; i < here; i += kThr / pairs)
+      if (p < a.half) s_cs[buf][i * a.half + p] = angle(a, p, t0 + i, s_turn[p]);
+    __syncthreads();  // (the other buffer's readers are past it when this one is written again)
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const int rows = a.heads[which];
+      if (which == 1) {
+        src = static_cast<const uint8_t *>(a.x[1]) + (t * a.stride[1] + int64_t(first) * a.d) * kEi;
+        fetch(mine && first < rows);
+      }
+      // the factors of this lane's channels and of their partners
+      const float *w = a.weight[which];
+      float2 ca[4], cb[4];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = c0 + e;
+        const bool up = kPart == 0 ? (e & 1) != 0 : c >= a.half;
+        const int p = kPart == 0 ? c ^ 1 : up ? c - a.half : c + a.half;
+        float x = 1.f, y = 0.f;
+        if (mine && turns) {
+          const float2 cs = s_cs[buf][token * a.half + (kPart == 0 ? c >> 1 : up ? p : c)];
+          x = cs.x, y = up ? cs.y : -cs.y;
+          if (w != nullptr) y *= w[p];
+        }
+        if (mine && w != nullptr) x *= w[c];
+        if (e & 1) ca[e >> 1].y = x, cb[e >> 1].y = y;
+        else ca[e >> 1].x = x, cb[e >> 1].x = y;
+      }
+      uint8_t *dst = static_cast<uint8_t *>(a.out[which]) + (t * a.out_stride[which] + int64_t(first) * a.d + c0) * kEo;
+      const uint32_t row_in = uint32_t(stride) * a.d * kEi, row_out = uint32_t(stride) * a.d * kEo;
+#pragma unroll 1
+      for (int h = first; h - first < rows; h += stride, dst += row_out) {  // (all rows of a warp go round together)
+        const Piece<kInBF16> raw = next;
+        const uint8_t *row = src;
+        src += row_in;
+        fetch(mine && h + stride < rows);
+        const bool ok = mine && h < rows;
+        float x[8], xp[8];
+        raw.get(x);
+        float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) s2 = f2_fma(make_float2(x[e], x[e + 1]), make_float2(x[e], x[e + 1]), s2);
+        float sum = s2.x + s2.y;
+        if constexpr (kPart == 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) xp[e] = x[e ^ 1];
+        } else if constexpr (kPart == 8) {
+          Piece<kInBF16> p;
+#pragma unroll
+          for (int e = 0; e < kEi / 2; ++e) {
+            p.w[e].x = __shfl_sync(0xffffffffu, raw.w[e].x, from_lane), p.w[e].y = __shfl_sync(0xffffffffu, raw.w[e].y, from_lane);
+            p.w[e].z = __shfl_sync(0xffffffffu, raw.w[e].z, from_lane), p.w[e].w = __shfl_sync(0xffffffffu, raw.w[e].w, from_lane);
+          }
+          p.get(xp);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; e += 4) {
+            if (ok && turns) load_part<kInBF16, 4>(row, c0 + e < a.half ? c0 + e + a.half : c0 + e - a.half, &xp[e]);
+          }
+        }
+#pragma unroll 1
+        for (int off = lanes >> 1; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        __syncwarp();  // in place: every lane of the row has read it
+        const float r = norm_factor(a, sum);
+        float2 y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] = f2_mul(make_float2(x[2 * e], x[2 * e + 1]), ca[e]);
+          // (left out, not multiplied by zero, where nothing turns: the partner may be infinite)
+          if (turns) y[e] = f2_fma(make_float2(xp[2 * e], xp[2 * e + 1]), cb[e], y[e]);
+          y[e] = f2_mul(y[e], make_float2(r, r));
+        }
+        if (ok) {
+          if constexpr (kOutBF16) {
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y),
+                                                         pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
+          } else {
+            reinterpret_cast<float4 *>(dst)[0] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+            reinterpret_cast<float4 *>(dst)[1] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
+          }
+        }
+      }
+    }
+  }
+}
+
 // One channel per lane and step: rows that start anywhere, head sizes that are no multiple of 8.
 template <bool kInBF16, bool kOutBF16, bool kNeighbours>
 __global__ void __launch_bounds__(kThr) rotate_any_kernel(const RotateArgs a) {
@@ -26,22 +224,10 @@ __global__ void __launch_bounds__(kThr) rotate_any_kernel(const RotateArgs a) {
   __shared__ uint64_t s_turn[kRotateMaxD / 2];
   __shared__ float2 s_cs[kRotateMaxD / 2];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  for (int i = tid; i < a.half; i += kThr) {
-    const double f = double(a.inv_freq[i]) * 0.15915494309189533577;  // turns per position
-    s_turn[i] = __double2ull_rz((f - floor(f)) * 18446744073709551616.);
-  }
+  for (int i = tid; i < a.half; i += kThr) s_turn[i] = turns_per_position(a.inv_freq[i]);
   for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
     __syncthreads();
-    for (int i = tid; i < a.half; i += kThr) {
-      const int64_t at = a.axis[i] * a.tokens + t;
-      const int64_t pos = a.pos64 ? static_cast<const int64_t *>(a.positions)[at]
-                                  : int64_t(static_cast<const int32_t *>(a.positions)[at]);
-      const int32_t turn = int32_t((uint64_t(pos) * s_turn[i]) >> 32);
-      float s, c;
-      sincospif(float(turn) * 0x1p-31f, &s, &c);
-      if (!isfinite(a.inv_freq[i])) s = c = __int_as_float(0x7fc00000);
-      s_cs[i] = make_float2(c, s);
-    }
+    for (int i = tid; i < a.half; i += kThr) s_cs[i] = angle(a, i, t, s_turn[i]);
     __syncthreads();
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
@@ -71,12 +257,11 @@ __global__ void __launch_bounds__(kThr) rotate_any_kernel(const RotateArgs a) {
           xp[j] = c < 2 * a.half ? load_elem<kInBF16>(a.x[which], row + partner[j]) : 0.f;
           sum = fmaf(x[j], x[j], sum);
         }
-        float r = 1.f;
         if (a.norm != KDA_NORM_NONE) {
 #pragma unroll
           for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-          r = 1.f / sqrtf((a.norm == KDA_NORM_RMS ? sum / float(a.d) : sum) + a.eps);
         }
+        const float r = norm_factor(a, sum);
         __syncwarp();  // in place: every lane has read the row
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
@@ -92,6 +277,32 @@ __global__ void __launch_bounds__(kThr) rotate_any_kernel(const RotateArgs a) {
 }  // namespace
 
 cudaError_t launch_norm_rotate(const RotateArgs &a, bool in_bf16, bool out_bf16, bool interleaved, cudaStream_t stream) {
+  const auto whole = [&](const void *p, int64_t stride, int size) {
+    return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.tokens == 1 || stride * size % 16 == 0));
+  };
+  const int si = in_bf16 ? 2 : 4, so = out_bf16 ? 2 : 4;
+  if (a.d % 8 == 0 && a.half % 4 == 0 && whole(a.x[0], a.stride[0], si) && whole(a.x[1], a.stride[1], si) &&
+      whole(a.out[0], a.out_stride[0], so) && whole(a.out[1], a.out_stride[1], so)) {
+    using Kern = void (*)(const RotateArgs, int, int, int);
+#define KDA_ROT(ib, ob) {rotate_kernel<ib, ob, 0>, rotate_kernel<ib, ob, 4>, rotate_kernel<ib, ob, 8>}
+    static const Kern kernels[4][3] = {KDA_ROT(false, false), KDA_ROT(false, true), KDA_ROT(true, false), KDA_ROT(true, true)};
+#undef KDA_ROT
+    int lanes = 1, pairs = 1, group = 1;
+    while (8 * lanes < a.d) lanes *= 2;
+    while (pairs < a.half) pairs *= 2;
+    const int rows = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1], slots = kThr / lanes;
+    const int64_t fit = 152 * (in_bf16 ? 4 : 3);
+    // a lane's factors serve some six rows of a token, unless there are too few tokens for that
+    const int64_t per = a.tokens * rows / (fit * slots);
+    while (group < slots && group * (per < 1 ? 1 : per < 6 ? per : 6) < rows) group *= 2;
+    const int64_t passes = (a.tokens + slots / group - 1) / (slots / group);
+    // few tokens: their heads over several CTAs
+    const int64_t most = (rows + group - 1) / group, spare = fit / passes;
+    const unsigned parts = unsigned(spare < 1 ? 1 : spare < most ? spare : most);
+    kernels[2 * int(in_bf16) + int(out_bf16)][interleaved ? 0 : a.half % 8 == 0 ? 2 : 1]<<<
+        dim3(unsigned(passes < fit ? passes : fit), parts), kThr, 0, stream>>>(a, lanes, group, pairs);
+    return cudaGetLastError();
+  }
   using Kern = void (*)(const RotateArgs);
 #define KDA_ROT(ib, ob) {rotate_any_kernel<ib, ob, false>, rotate_any_kernel<ib, ob, true>}
   static const Kern any[4][2] = {KDA_ROT(false, false), KDA_ROT(false, true), KDA_ROT(true, false), KDA_ROT(true, true)};

@@ -18,7 +18,7 @@ struct RotateArgs {
   const float *inv_freq;
   int64_t tokens;
   int32_t d, half, norm, pos64;
-  float eps;
+  float eps, per;  // the norm's factor is 1 / sqrt(per sum(x^2) + eps)
   uint8_t axis[kRotateMaxD / 2];
 };
 
