@@ -4,9 +4,12 @@
 //
 // One read and one write of the d_k x d_v fp32 state per (sequence, head) against 1.2 flops per byte:
 // bound by HBM bandwidth, and by latency when few states are in flight. A new entry needs its whole old
-// column (S'^T k), so a CTA holds all key rows of its value columns in registers, 32 entries per
-// thread: kRows rows of kVec neighbouring columns, every load issued before the first is used. The two
-// row sums meet once, by shuffles and through shared memory, and every thread forms its own columns' u.
+// column (S'^T k), so a CTA holds all key rows of its value columns, 32 entries per thread: kRows rows of
+// kVec neighbouring columns, every load issued before the first is used. Where rows of the state start on
+// 16-byte boundaries the entries come to shared memory by cp.async (each thread reads back only what it
+// copied), so that they take no registers and six CTAs of 32 KB share an SM; single columns are held in
+// registers. The two row sums meet once, by shuffles and through shared memory, and every thread forms its
+// own columns' u.
 #include "kda_delta.cuh"
 
 namespace kda {
@@ -14,7 +17,7 @@ namespace {
 
 // kTX threads side by side along the value columns, kVec columns each; kThr / kTX key rows at a time.
 template <bool kInBF16, bool kOutBF16, int kVec, int kTX, int kThr>
-__global__ void __launch_bounds__(kThr)
+__global__ void __launch_bounds__(kThr, kVec == 4 ? 1536 / kThr : 512 / kThr)
     delta_decode_kernel(const void *__restrict__ q, const void *__restrict__ k, const void *__restrict__ v,
                         const float *__restrict__ log_decay, int per_token, const float *__restrict__ beta,
                         float *__restrict__ state, void *__restrict__ out, int H, int H_k, int d_k, int d_v,
@@ -37,22 +40,26 @@ __global__ void __launch_bounds__(kThr)
   const bool ok = col < d_v;                        // kVec divides d_v
   float *S = state + bh * int64_t(d_k) * d_v + col;
 
-  float st[kRows][kVec];
+  __shared__ __align__(16) float s_st[kVec == 4 ? kRG * kRows * kCols : 4];
+  float st[kVec == 4 ? 1 : kRows];
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
     const int r = ty + kRG * j;
-    if (ok && r < d_k) {
-      if constexpr (kVec == 4) {
-        const float4 x = __ldcs(reinterpret_cast<const float4 *>(S + int64_t(r) * d_v));
-        st[j][0] = x.x, st[j][1] = x.y, st[j][2] = x.z, st[j][3] = x.w;
-      } else {
-        st[j][0] = __ldcs(S + int64_t(r) * d_v);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) st[j][e] = 0.f;
-    }
+    const bool on = ok && r < d_k;
+    if constexpr (kVec == 4) cp_async_16_zfill(&s_st[(kThr * j + tid) * 4], on ? S + int64_t(r) * d_v : state, on);
+    else st[j] = on ? __ldcs(S + int64_t(r) * d_v) : 0.f;
   }
+  // the decayed entries of row j
+  auto get = [&](int j, Decay decay, float (&x)[kVec]) {
+    if constexpr (kVec == 4) {
+      const float4 v = *reinterpret_cast<const float4 *>(&s_st[(kThr * j + tid) * 4]);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      x[0] = st[j];
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) x[e] = decay_step(x[e], decay);
+  };
   const Decay decay = decay_of(log_decay[per_token ? bh : h]);
   const float b = beta[bh];
   float vv[kVec];
@@ -66,15 +73,17 @@ __global__ void __launch_bounds__(kThr)
   __syncthreads();
 
   float y[kVec] = {}, z[kVec] = {}, kq = 0.f;
+  if constexpr (kVec == 4) cp_async_wait_all();
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
     const float kr = s_k[ty + kRG * j], qr = s_q[ty + kRG * j];
     kq = fmaf(kr, qr, kq);
+    float x[kVec];
+    get(j, decay, x);
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
-      st[j][e] = decay_step(st[j][e], decay);
-      y[e] = fmaf(kr, st[j][e], y[e]);
-      z[e] = fmaf(qr, st[j][e], z[e]);
+      y[e] = fmaf(kr, x[e], y[e]);
+      z[e] = fmaf(qr, x[e], z[e]);
     }
   }
 #pragma unroll
@@ -105,12 +114,13 @@ __global__ void __launch_bounds__(kThr)
   for (int j = 0; j < kRows; ++j) {
     const int r = ty + kRG * j;
     const float kr = s_k[r];
+    float x[kVec];
+    get(j, decay, x);
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) st[j][e] = fmaf(kr, u[e], st[j][e]);
+    for (int e = 0; e < kVec; ++e) x[e] = fmaf(kr, u[e], x[e]);
     if (ok && r < d_k) {
-      if constexpr (kVec == 4)
-        __stcs(reinterpret_cast<float4 *>(S + int64_t(r) * d_v), make_float4(st[j][0], st[j][1], st[j][2], st[j][3]));
-      else __stcs(S + int64_t(r) * d_v, st[j][0]);
+      if constexpr (kVec == 4) __stcs(reinterpret_cast<float4 *>(S + int64_t(r) * d_v), make_float4(x[0], x[1], x[2], x[3]));
+      else __stcs(S + int64_t(r) * d_v, x[0]);
     }
   }
   if (ty == 0 && ok) {

@@ -100,8 +100,9 @@ __device__ __forceinline__ void load_part(const void *base, int64_t at, float *x
 // half pieces (4) by a load. `lanes` threads per row, `group` rows of a token side by side, so
 // kThr / (lanes group) tokens at a time; `pairs` threads form a token's angles.
 template <bool kInBF16, bool kOutBF16, int kPart>
-__global__ void __launch_bounds__(kThr, kInBF16 ? 4 : 3) rotate_kernel(const RotateArgs a, int lanes, int group, int pairs) {
+__global__ void __launch_bounds__(kThr, 3) rotate_kernel(const RotateArgs a, int lanes, int group, int pairs) {
   constexpr int kEi = kInBF16 ? 2 : 4, kEo = kOutBF16 ? 2 : 4;
+  constexpr int kU = kInBF16 ? 2 : 1;  // rows at a time, and as many on their way
   __shared__ uint64_t s_turn[kRotateMaxD / 2];
   __shared__ __align__(16) float2 s_cs[2][kThr * 4];  // tokens x rot / 2: a row has at most 8 channels per lane
   const int tid = threadIdx.x, lane = tid & 31;
@@ -120,15 +121,18 @@ __global__ void __launch_bounds__(kThr, kInBF16 ? 4 : 3) rotate_kernel(const Rot
     const bool mine = c0 < a.d && token < here;
     // the first row is on its way while the angles are formed
     const uint8_t *src;
-    Piece<kInBF16> next{};
-    auto fetch = [&](bool ok) {
-      if (ok) {
+    Piece<kInBF16> next[kU] = {};
+    auto fetch = [&](int h, int rows) {
 #pragma unroll
-        for (int e = 0; e < kEi / 2; ++e) next.w[e] = reinterpret_cast<const uint4 *>(src + c0 * kEi)[e];
-      }
+      for (int u = 0; u < kU; ++u)
+        if (mine && h + u * stride < rows) {
+#pragma unroll
+          for (int e = 0; e < kEi / 2; ++e)
+            next[u].w[e] = reinterpret_cast<const uint4 *>(src + uint32_t(u * stride) * a.d * kEi + c0 * kEi)[e];
+        }
     };
     src = static_cast<const uint8_t *>(a.x[0]) + (t * a.stride[0] + int64_t(first) * a.d) * kEi;
-    fetch(mine && first < a.heads[0]);
+    fetch(first, a.heads[0]);
     const int p = tid & (pairs - 1);
 #pragma unroll 1
     for (int i = tid / pairs; i < here; i += kThr / pairs)
@@ -139,7 +143,7 @@ __global__ void __launch_bounds__(kThr, kInBF16 ? 4 : 3) rotate_kernel(const Rot
       const int rows = a.heads[which];
       if (which == 1) {
         src = static_cast<const uint8_t *>(a.x[1]) + (t * a.stride[1] + int64_t(first) * a.d) * kEi;
-        fetch(mine && first < rows);
+        fetch(first, rows);
       }
       // the factors of this lane's channels and of their partners
       const float *w = a.weight[which];
@@ -162,54 +166,70 @@ __global__ void __launch_bounds__(kThr, kInBF16 ? 4 : 3) rotate_kernel(const Rot
       uint8_t *dst = static_cast<uint8_t *>(a.out[which]) + (t * a.out_stride[which] + int64_t(first) * a.d + c0) * kEo;
       const uint32_t row_in = uint32_t(stride) * a.d * kEi, row_out = uint32_t(stride) * a.d * kEo;
 #pragma unroll 1
-      for (int h = first; h - first < rows; h += stride, dst += row_out) {  // (all rows of a warp go round together)
-        const Piece<kInBF16> raw = next;
+      for (int h = first; h - first < rows; h += kU * stride, dst += kU * row_out) {  // (all rows of a warp go round together)
+        Piece<kInBF16> raw[kU];
         const uint8_t *row = src;
-        src += row_in;
-        fetch(mine && h + stride < rows);
-        const bool ok = mine && h < rows;
-        float x[8], xp[8];
-        raw.get(x);
-        float2 s2 = make_float2(0.f, 0.f);
+        src += kU * row_in;
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) s2 = f2_fma(make_float2(x[e], x[e + 1]), make_float2(x[e], x[e + 1]), s2);
-        float sum = s2.x + s2.y;
-        if constexpr (kPart == 0) {
+        for (int u = 0; u < kU; ++u) raw[u] = next[u];
+        fetch(h + kU * stride, rows);
+        float sum[kU];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) xp[e] = x[e ^ 1];
-        } else if constexpr (kPart == 8) {
-          Piece<kInBF16> p;
+        for (int u = 0; u < kU; ++u) {
+          float x[8];
+          raw[u].get(x);
+          float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int e = 0; e < kEi / 2; ++e) {
-            p.w[e].x = __shfl_sync(0xffffffffu, raw.w[e].x, from_lane), p.w[e].y = __shfl_sync(0xffffffffu, raw.w[e].y, from_lane);
-            p.w[e].z = __shfl_sync(0xffffffffu, raw.w[e].z, from_lane), p.w[e].w = __shfl_sync(0xffffffffu, raw.w[e].w, from_lane);
-          }
-          p.get(xp);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; e += 4) {
-            if (ok && turns) load_part<kInBF16, 4>(row, c0 + e < a.half ? c0 + e + a.half : c0 + e - a.half, &xp[e]);
-          }
+          for (int e = 0; e < 8; e += 2) s2 = f2_fma(make_float2(x[e], x[e + 1]), make_float2(x[e], x[e + 1]), s2);
+          sum[u] = s2.x + s2.y;
         }
 #pragma unroll 1
-        for (int off = lanes >> 1; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        __syncwarp();  // in place: every lane of the row has read it
-        const float r = norm_factor(a, sum);
-        float2 y[4];
+        for (int off = lanes >> 1; off > 0; off >>= 1) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[e] = f2_mul(make_float2(x[2 * e], x[2 * e + 1]), ca[e]);
-          // (left out, not multiplied by zero, where nothing turns: the partner may be infinite)
-          if (turns) y[e] = f2_fma(make_float2(xp[2 * e], xp[2 * e + 1]), cb[e], y[e]);
-          y[e] = f2_mul(y[e], make_float2(r, r));
+          for (int u = 0; u < kU; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], off);
         }
-        if (ok) {
-          if constexpr (kOutBF16) {
-            *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y),
-                                                         pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const bool ok = mine && h + u * stride < rows;
+          float x[8], xp[8];
+          raw[u].get(x);
+          if constexpr (kPart == 0) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) xp[e] = x[e ^ 1];
+          } else if constexpr (kPart == 8) {
+            Piece<kInBF16> p;
+#pragma unroll
+            for (int e = 0; e < kEi / 2; ++e) {
+              p.w[e].x = __shfl_sync(0xffffffffu, raw[u].w[e].x, from_lane), p.w[e].y = __shfl_sync(0xffffffffu, raw[u].w[e].y, from_lane);
+              p.w[e].z = __shfl_sync(0xffffffffu, raw[u].w[e].z, from_lane), p.w[e].w = __shfl_sync(0xffffffffu, raw[u].w[e].w, from_lane);
+            }
+            p.get(xp);
           } else {
-            reinterpret_cast<float4 *>(dst)[0] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
-            reinterpret_cast<float4 *>(dst)[1] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+              if (ok && turns)
+                load_part<kInBF16, 4>(row + u * row_in, c0 + e < a.half ? c0 + e + a.half : c0 + e - a.half, &xp[e]);
+            }
+          }
+          __syncwarp();  // in place: every lane of the row has read it
+          const float r = norm_factor(a, sum[u]);
+          float2 y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[e] = f2_mul(make_float2(x[2 * e], x[2 * e + 1]), ca[e]);
+            // (left out, not multiplied by zero, where nothing turns: the partner may be infinite)
+            if (turns) y[e] = f2_fma(make_float2(xp[2 * e], xp[2 * e + 1]), cb[e], y[e]);
+            y[e] = f2_mul(y[e], make_float2(r, r));
+          }
+          if (ok) {
+            uint8_t *to = dst + u * row_out;
+            if constexpr (kOutBF16) {
+              *reinterpret_cast<uint4 *>(to) = make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y),
+                                                          pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
+            } else {
+              reinterpret_cast<float4 *>(to)[0] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+              reinterpret_cast<float4 *>(to)[1] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
+            }
           }
         }
       }
@@ -291,7 +311,7 @@ cudaError_t launch_norm_rotate(const RotateArgs &a, bool in_bf16, bool out_bf16,
     while (8 * lanes < a.d) lanes *= 2;
     while (pairs < a.half) pairs *= 2;
     const int rows = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1], slots = kThr / lanes;
-    const int64_t fit = 152 * (in_bf16 ? 4 : 3);
+    const int64_t fit = 152 * 3;
     // a lane's factors serve some six rows of a token, unless there are too few tokens for that
     const int64_t per = a.tokens * rows / (fit * slots);
     while (group < slots && group * (per < 1 ? 1 : per < 6 ? per : 6) < rows) group *= 2;
