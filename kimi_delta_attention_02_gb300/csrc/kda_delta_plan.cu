@@ -79,7 +79,7 @@ DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool 
                      size_t workspace_bytes) {
   DeltaPlan p;
   // TMA addresses rows of a multiple of 16 bytes
-  const int64_t least = 24;
+  const int64_t least = d_k <= 64 && d_v <= 64 ? 44 : d_k <= 64 || d_v <= 64 ? 16 : 6;
   p.tensor = in_bf16 && !recurrent && d_k % 8 == 0 && d_v % 8 == 0 && total >= least * num_seqs &&
              int64_t(H) * d_v <= 1 << 25;  // (its output addresses)
   if (!p.tensor) return p;

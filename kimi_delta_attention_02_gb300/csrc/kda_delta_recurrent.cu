@@ -11,9 +11,11 @@
 // multiply-adds per entry for four tokens (16 one by one) and a quarter of the waits. No decay is the
 // difference of two sums.
 //
-// A warp holds 4 kNC value columns: lane (cl, rl) owns kNC of them and the key rows 32 j + 4 rl + 0..3,
-// two rows to a packed fp32 instruction. q, k, v pass through shared memory 16 tokens at a time, the
-// next 16 waiting in registers; warp w forms the products k.k and q.k of the stage's block w.
+// kLanes lanes share a column's key rows, so a warp holds 32 / kLanes kNC value columns: lane (cl, rl) owns
+// kNC of them and the key rows 4 kLanes j + 4 rl + 0..3, two rows to a packed fp32 instruction. Four warps do
+// this. Four others go ahead of them: they bring q, k, v to shared memory 16 tokens at a time (the next 16
+// waiting in registers) and form the products k.k and q.k and the decays of the next 16 tokens' blocks.
+#include <atomic>
 #include <type_traits>
 
 #include "kda_delta.cuh"
@@ -22,7 +24,7 @@ namespace kda {
 namespace {
 
 constexpr int kTok = 16;  // tokens per stage
-constexpr int kThr = 128;
+constexpr int kThr = 128;  // of each half: those that keep the state, those that go ahead
 
 struct Block {  // of four tokens
   float E[4];       // from the block's start
@@ -34,59 +36,66 @@ struct Block {  // of four tokens
   float qk[4][4];   // D_ti (q_t . k_i), i <= t
 };
 
-template <bool kInBF16, bool kOutBF16, int kRows, int kNC>
-__global__ void __launch_bounds__(kThr) delta_recurrent_kernel(const DeltaArgs a) {
-  constexpr int kDK = 8 * kRows, kCols = 16 * kNC;
-  __shared__ __align__(16) float s_k[2][kTok][kDK], s_q[2][kTok][kDK];
-  __shared__ __align__(16) float s_v[2][kTok][kCols];
-  __shared__ __align__(16) Block s_block[kTok / 4];
-  __shared__ float s_g[2][kTok], s_beta[2][kTok];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int rl = lane & 7, cl = lane >> 3;
+template <int kDK, int kCols>
+struct Shared {
+  float k[3][kTok][kDK], q[3][kTok][kDK], v[3][kTok][kCols];
+  Block block[2][kTok / 4];
+  float g[3][kTok], beta[3][kTok];
+};
+
+template <bool kInBF16, bool kOutBF16, int kLanes, int kRows, int kNC>
+__global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const DeltaArgs a) {
+  constexpr int kDK = kLanes * kRows, kCols = kThr / kLanes * kNC;
+  constexpr int kEach = kLanes / 8;  // lanes that end with the same one of a block's eight sums
+  extern __shared__ __align__(16) uint8_t smem[];
+  Shared<kDK, kCols> &sh = *reinterpret_cast<Shared<kDK, kCols> *>(smem);
+  const int tid = threadIdx.x % kThr, lane = tid & 31, w = tid >> 5;
+  const int rl = lane % kLanes, cl = lane / kLanes;
   const int h = blockIdx.x % a.H, n = blockIdx.x / a.H, hk = h / (a.H / a.H_k);
-  const int col0 = blockIdx.y * kCols, cw = 4 * kNC * w + kNC * cl, col = col0 + cw;
+  const int col0 = blockIdx.y * kCols, cw = 32 / kLanes * kNC * w + kNC * cl, col = col0 + cw;
   const int64_t t0 = a.cu[n], t1 = a.cu[n + 1];
 
-  // the state: S[c][2 j + p] holds rows 32 j + 4 rl + 2 p, + 1 of column col + c
-  float2 S[kNC][kRows / 2];
-  const int64_t at_state = (int64_t(n) * a.H + h) * a.d_k * a.d_v;
-#pragma unroll
-  for (int p = 0; p < kRows / 2; ++p) {
-    const int r = 32 * (p >> 1) + 4 * rl + 2 * (p & 1);
-    auto at = [&](int row, int c) {
-      return a.init_state != nullptr && row < a.d_k && col + c < a.d_v
-                 ? a.init_state[at_state + int64_t(row) * a.d_v + col + c] : 0.f;
-    };
-#pragma unroll
-    for (int c = 0; c < kNC; ++c) S[c][p] = make_float2(at(r, c), at(r + 1, c));
-  }
-
-  // global -> registers -> shared memory, a stage of kTok tokens at a time (as stored: a conversion
-  // here would wait for the load)
+  // global -> registers -> shared memory, a stage of kTok tokens at a time (as stored: a conversion here
+  // would wait for the load). Rows of q and k that are whole 16-byte pieces take 16-byte loads: a load
+  // per element and its address are half of a stage's instructions where a warp has one column.
   using Elem = std::conditional_t<kInBF16, uint16_t, float>;
-  auto raw = [](const void *p, int64_t at) { return static_cast<const Elem *>(p)[at]; };
   auto value = [](Elem x) {
     if constexpr (kInBF16) return bf16_to_f32(x);
     else return x;
   };
-  constexpr int kKeys = kTok * kDK / kThr, kVals = kTok * kCols / kThr;
-  Elem rk[kKeys], rq[kKeys], rv[kVals];
+  constexpr int kPer = 16 / int(sizeof(Elem)), kPieces = kTok * kDK / kPer / kThr, kRowPieces = kDK / kPer;
+  constexpr int kVals = (kTok * kCols + kThr - 1) / kThr;
+  union Raw {
+    uint4 w;
+    Elem e[kPer];
+  };
+  Raw rk[kPieces], rq[kPieces];
+  Elem rv[kVals];
+  const bool whole = a.d_k % kPer == 0;
   float r_g = 0.f, r_beta = 0.f;
   auto fetch = [&](int64_t t) {  // tokens t .. t + kTok - 1; zeros past the sequence
 #pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-      const int64_t tt = t + i * (kThr / kDK) + tid / kDK;
-      const int c = tid % kDK;
-      const bool ok = tt < t1 && c < a.d_k;
+    for (int i = 0; i < kPieces; ++i) {
+      const int64_t tt = t + (i * kThr + tid) / kRowPieces;
+      const int c = tid % kRowPieces * kPer;
       const int64_t at = (tt * a.H_k + hk) * a.d_k + c;
-      rk[i] = ok ? raw(a.k, at) : Elem(0);
-      rq[i] = ok ? raw(a.q, at) : Elem(0);
+      const Elem *k = static_cast<const Elem *>(a.k) + at, *q = static_cast<const Elem *>(a.q) + at;
+      rk[i].w = rq[i].w = make_uint4(0, 0, 0, 0);
+      if (tt >= t1 || c >= a.d_k) continue;
+      if (whole) {
+        rk[i].w = *reinterpret_cast<const uint4 *>(k), rq[i].w = *reinterpret_cast<const uint4 *>(q);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+          if (c + e < a.d_k) rk[i].e[e] = k[e], rq[i].e[e] = q[e];
+      }
     }
 #pragma unroll
     for (int i = 0; i < kVals; ++i) {
       const int64_t tt = t + (i * kThr + tid) / kCols;
       const int c = col0 + tid % kCols;
-      rv[i] = tt < t1 && c < a.d_v ? raw(a.v, (tt * a.H + h) * a.d_v + c) : Elem(0);
+      rv[i] = i * kThr + tid < kTok * kCols && tt < t1 && c < a.d_v
+                  ? static_cast<const Elem *>(a.v)[(tt * a.H + h) * a.d_v + c] : Elem(0);
     }
     if (tid < kTok) {
       const bool ok = t + tid < t1;
@@ -96,23 +105,29 @@ __global__ void __launch_bounds__(kThr) delta_recurrent_kernel(const DeltaArgs a
   };
   auto stage = [&](int b) {
 #pragma unroll
-    for (int i = 0; i < kKeys; ++i) {
-      s_k[b][i * (kThr / kDK) + tid / kDK][tid % kDK] = value(rk[i]);
-      s_q[b][i * (kThr / kDK) + tid / kDK][tid % kDK] = value(rq[i]);
+    for (int i = 0; i < kPieces; ++i) {
+      const int row = (i * kThr + tid) / kRowPieces, c = tid % kRowPieces * kPer;
+#pragma unroll
+      for (int e = 0; e < kPer; e += 4) {
+        *reinterpret_cast<float4 *>(&sh.k[b][row][c + e]) =
+            make_float4(value(rk[i].e[e]), value(rk[i].e[e + 1]), value(rk[i].e[e + 2]), value(rk[i].e[e + 3]));
+        *reinterpret_cast<float4 *>(&sh.q[b][row][c + e]) =
+            make_float4(value(rq[i].e[e]), value(rq[i].e[e + 1]), value(rq[i].e[e + 2]), value(rq[i].e[e + 3]));
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kVals; ++i) s_v[b][(i * kThr + tid) / kCols][tid % kCols] = value(rv[i]);
-    if (tid < kTok) s_g[b][tid] = r_g, s_beta[b][tid] = r_beta;
+    for (int i = 0; i < kVals; ++i)
+      if (i * kThr + tid < kTok * kCols) sh.v[b][(i * kThr + tid) / kCols][tid % kCols] = value(rv[i]);
+    if (tid < kTok) sh.g[b][tid] = r_g, sh.beta[b][tid] = r_beta;
   };
   // warp w: the products and decays of the stage's block w
-  auto form_block = [&](int b, int64_t step) {
-    Block &B = s_block[w];
+  auto form_block = [&](int b, Block &B, int64_t step) {
     float4 k4[4], q4[4];
     const bool on = 4 * lane < kDK;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      k4[t] = on ? *reinterpret_cast<const float4 *>(&s_k[b][4 * w + t][4 * lane]) : make_float4(0.f, 0.f, 0.f, 0.f);
-      q4[t] = on ? *reinterpret_cast<const float4 *>(&s_q[b][4 * w + t][4 * lane]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      k4[t] = on ? *reinterpret_cast<const float4 *>(&sh.k[b][4 * w + t][4 * lane]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      q4[t] = on ? *reinterpret_cast<const float4 *>(&sh.q[b][4 * w + t][4 * lane]) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     auto dot = [](float4 x, float4 y) { return fmaf(x.x, y.x, x.y * y.y) + fmaf(x.z, y.z, x.w * y.w); };
     float sums[16];  // 10 of q.k (row t from t (t + 1) / 2), then 6 of k.k (row t from t (t - 1) / 2)
@@ -132,7 +147,7 @@ __global__ void __launch_bounds__(kThr) delta_recurrent_kernel(const DeltaArgs a
     float g[4], decay = 0.f, from = 0.f, rest = 0.f, whole = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      g[j] = s_g[b][4 * w + j];
+      g[j] = sh.g[b][4 * w + j];
       if (j > i && j <= t) decay += g[j];
       if (j <= (lane & 3)) from += g[j];
       if (j > (lane & 3)) rest += g[j];
@@ -140,31 +155,59 @@ __global__ void __launch_bounds__(kThr) delta_recurrent_kernel(const DeltaArgs a
     }
     if ((lane & 1) == 0) {
       if (is_qk) B.qk[t][i] = expf(decay) * sum;
-      else B.kk[t][i] = s_beta[b][4 * w + t] * expf(decay) * sum;
+      else B.kk[t][i] = sh.beta[b][4 * w + t] * expf(decay) * sum;
     }
     if (lane < 4) {
       B.E[lane] = expf(from);
       B.rest[lane] = expf(rest);
-      B.beta[lane] = s_beta[b][4 * w + lane];
+      B.beta[lane] = sh.beta[b][4 * w + lane];
     }
     if (lane == 4) B.whole = unbiased_decay(whole, step);
   };
 
-  if (t0 < t1) {
+  if (threadIdx.x >= kThr) {
+    // stage i + 2 comes to shared memory and the blocks of stage i + 1 are formed while stage i is worked on
+    if (t0 >= t1) return;
     fetch(t0);
     stage(0);
+    fetch(t0 + kTok);
+    stage(1);
+    fetch(t0 + 2 * kTok);
+    named_bar_sync(1, kThr);
+    form_block(0, sh.block[0][w], w);
+    int b1 = 1, b2 = 2;
+    for (int64_t t = t0, i = 1; t < t1; t += kTok, ++i) {
+      __syncthreads();
+      stage(b2);
+      fetch(t + 3 * kTok);
+      form_block(b1, sh.block[i & 1][w], i * (kTok / 4) + w);
+      b1 = b2;
+      if (++b2 == 3) b2 = 0;
+    }
+    return;
   }
-  int b = 0;
-  for (int64_t t = t0; t < t1; t += kTok, b ^= 1) {
-    __syncthreads();  // stage b is written; every thread is done with stage b ^ 1 and the blocks
-    const bool more = t + kTok < t1;
-    if (more) fetch(t + kTok);
-    form_block(b, (t - t0) / 4 + w);
+
+  // the state: S[c][2 j + p] holds rows 4 kLanes j + 4 rl + 2 p, + 1 of column col + c
+  float2 S[kNC][kRows / 2];
+  const int64_t at_state = (int64_t(n) * a.H + h) * a.d_k * a.d_v;
+#pragma unroll
+  for (int p = 0; p < kRows / 2; ++p) {
+    const int r = 4 * kLanes * (p >> 1) + 4 * rl + 2 * (p & 1);
+    auto at = [&](int row, int c) {
+      return a.init_state != nullptr && row < a.d_k && col + c < a.d_v
+                 ? a.init_state[at_state + int64_t(row) * a.d_v + col + c] : 0.f;
+    };
+#pragma unroll
+    for (int c = 0; c < kNC; ++c) S[c][p] = make_float2(at(r, c), at(r + 1, c));
+  }
+
+  int b = 0, turn = 0;
+  for (int64_t t = t0; t < t1; t += kTok, turn ^= 1) {
     __syncthreads();
     const int len = t1 - t < kTok ? int(t1 - t) : kTok;
 #pragma unroll 1
     for (int i0 = 0; i0 < len; i0 += 4) {
-      const Block &B = s_block[i0 >> 2];
+      const Block &B = sh.block[turn][i0 >> 2];
       float2 acc[kNC][8];
 #pragma unroll
       for (int c = 0; c < kNC; ++c)
@@ -174,7 +217,7 @@ __global__ void __launch_bounds__(kThr) delta_recurrent_kernel(const DeltaArgs a
       for (int j = 0; j < kRows / 4; ++j) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float4 x = *reinterpret_cast<const float4 *>(&(e < 4 ? s_k : s_q)[b][i0 + (e & 3)][32 * j + 4 * rl]);
+          const float4 x = *reinterpret_cast<const float4 *>(&(e < 4 ? sh.k : sh.q)[b][i0 + (e & 3)][4 * kLanes * j + 4 * rl]);
 #pragma unroll
           for (int c = 0; c < kNC; ++c)
             acc[c][e] = f2_fma(make_float2(x.z, x.w), S[c][2 * j + 1],
@@ -184,32 +227,34 @@ __global__ void __launch_bounds__(kThr) delta_recurrent_kernel(const DeltaArgs a
       float u[kNC][4];
 #pragma unroll
       for (int c = 0; c < kNC; ++c) {
-        // the sums over the eight lanes rl: lane rl ends with y_rl, or z_{rl - 4}
+        // the sums over the lanes rl: lane rl ends with y_{rl / kEach}, or z_{rl / kEach - 4}
         float x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = acc[c][e].x + acc[c][e].y;
 #pragma unroll
         for (int half = 4; half >= 1; half >>= 1) {
-          const bool up = (rl & half) != 0;
+          const bool up = (rl & half * kEach) != 0;
 #pragma unroll
           for (int e = 0; e < half; ++e)
-            x[e] = (up ? x[e + half] : x[e]) + __shfl_xor_sync(0xffffffffu, up ? x[e] : x[e + half], half);
+            x[e] = (up ? x[e + half] : x[e]) + __shfl_xor_sync(0xffffffffu, up ? x[e] : x[e + half], half * kEach);
         }
-        const float mine = x[0];
+        float mine = x[0];
+#pragma unroll
+        for (int off = kEach >> 1; off >= 1; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float y = __shfl_sync(0xffffffffu, mine, e, 8);
-          float r = B.beta[e] * (s_v[b][i0 + e][cw + c] - B.E[e] * y);
+          const float y = __shfl_sync(0xffffffffu, mine, e * kEach, kLanes);
+          float r = B.beta[e] * (sh.v[b][i0 + e][cw + c] - B.E[e] * y);
 #pragma unroll
           for (int i = 0; i < e; ++i) r = fmaf(-B.kk[e][i], u[c][i], r);
           u[c][e] = i0 + e < len ? r : 0.f;
         }
-        const int e = rl & 3;
+        const int e = rl / kEach & 3;
         float o = B.E[e] * mine;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (i <= e) o = fmaf(B.qk[e][i], u[c][i], o);
-        if (rl >= 4 && i0 + e < len && col + c < a.d_v)
+        if (rl >= 4 * kEach && rl % kEach == 0 && i0 + e < len && col + c < a.d_v)
           store_elem<kOutBF16>(a.out, ((t + i0 + e) * a.H + h) * a.d_v + col + c, a.scale * o);
       }
       const float2 whole = make_float2(B.whole, B.whole);
@@ -226,7 +271,7 @@ __global__ void __launch_bounds__(kThr) delta_recurrent_kernel(const DeltaArgs a
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float4 x = *reinterpret_cast<const float4 *>(&s_k[b][i0 + e][32 * j + 4 * rl]);
+          const float4 x = *reinterpret_cast<const float4 *>(&sh.k[b][i0 + e][4 * kLanes * j + 4 * rl]);
 #pragma unroll
           for (int c = 0; c < kNC; ++c) {
             const float2 uu = make_float2(u[c][e], u[c][e]);
@@ -236,13 +281,13 @@ __global__ void __launch_bounds__(kThr) delta_recurrent_kernel(const DeltaArgs a
         }
       }
     }
-    if (more) stage(b ^ 1);
+    if (++b == 3) b = 0;
   }
 
   if (a.final_state != nullptr) {
 #pragma unroll
     for (int p = 0; p < kRows / 2; ++p) {
-      const int r = 32 * (p >> 1) + 4 * rl + 2 * (p & 1);
+      const int r = 4 * kLanes * (p >> 1) + 4 * rl + 2 * (p & 1);
 #pragma unroll
       for (int c = 0; c < kNC; ++c) {
         float *dst = a.final_state + at_state + int64_t(r) * a.d_v + col + c;
@@ -253,23 +298,45 @@ __global__ void __launch_bounds__(kThr) delta_recurrent_kernel(const DeltaArgs a
   }
 }
 
+template <bool kInBF16, bool kOutBF16, int kLanes, int kRows, int kNC>
+cudaError_t launch_one(const DeltaArgs &a, cudaStream_t stream) {
+  constexpr int kCols = kThr / kLanes * kNC;
+  constexpr int smem = int(sizeof(Shared<kLanes * kRows, kCols>));
+  const auto kern = delta_recurrent_kernel<kInBF16, kOutBF16, kLanes, kRows, kNC>;
+  if (smem > 49152) {  // granted once per device (bit d for device d; past 63 at every launch)
+    static std::atomic<uint64_t> granted;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (bit == 0 || (granted.load(std::memory_order_acquire) & bit) == 0) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      granted.fetch_or(bit, std::memory_order_release);
+    }
+  }
+  const dim3 grid(unsigned(int64_t(a.num_seqs) * a.H), unsigned((a.d_v + kCols - 1) / kCols));
+  kern<<<grid, 2 * kThr, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream) {
-  using Kern = void (*)(const DeltaArgs);
+  // Few chains take a warp per column, so that a block's way is shorter; many take 16 columns per CTA, or 32 while
+  // that leaves two CTAs for every SM.
   const int64_t chains = int64_t(a.num_seqs) * a.H;
-  int nc = 4;
-  while (nc > 1 && chains * ((a.d_v + 16 * nc - 1) / (16 * nc)) < 2 * kLinearSMs) nc >>= 1;
-  const bool wide = a.d_k > 64;
-#define KDA_DELTA(ib, ob)                                                                                     \
-  {delta_recurrent_kernel<ib, ob, 8, 1>, delta_recurrent_kernel<ib, ob, 8, 2>, delta_recurrent_kernel<ib, ob, 8, 4>, \
-   delta_recurrent_kernel<ib, ob, 16, 1>, delta_recurrent_kernel<ib, ob, 16, 2>, delta_recurrent_kernel<ib, ob, 16, 4>}
-  static const Kern kernels[4][6] = {KDA_DELTA(false, false), KDA_DELTA(false, true), KDA_DELTA(true, false),
-                                     KDA_DELTA(true, true)};
-#undef KDA_DELTA
-  const dim3 grid(unsigned(chains), unsigned((a.d_v + 16 * nc - 1) / (16 * nc)));
-  kernels[2 * int(in_bf16) + int(out_bf16)][3 * int(wide) + (nc == 4 ? 2 : nc - 1)]<<<grid, kThr, 0, stream>>>(a);
-  return cudaGetLastError();
+  const auto ctas = [&](int cols) { return chains * ((a.d_v + cols - 1) / cols); };
+  const auto run = [&](auto in, auto out) {
+    constexpr bool ib = decltype(in)::value, ob = decltype(out)::value;
+    if (ctas(4) <= 6 * kLinearSMs) return launch_one<ib, ob, 32, 4, 1>(a, stream);
+    const bool wide = a.d_k > 64, two = ctas(32) >= 2 * kLinearSMs;
+    if (wide) return two ? launch_one<ib, ob, 8, 16, 2>(a, stream) : launch_one<ib, ob, 8, 16, 1>(a, stream);
+    return two ? launch_one<ib, ob, 8, 8, 2>(a, stream) : launch_one<ib, ob, 8, 8, 1>(a, stream);
+  };
+  const std::true_type yes;
+  const std::false_type no;
+  return in_bf16 ? (out_bf16 ? run(yes, yes) : run(yes, no)) : (out_bf16 ? run(no, yes) : run(no, no));
 }
 
 }  // namespace kda
