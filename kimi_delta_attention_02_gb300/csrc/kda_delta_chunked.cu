@@ -15,18 +15,18 @@
 //
 // Roundings. The operands of what reaches the state (S, R, T', U') are pairs of bf16, hi + lo, each
 // pair off by at most 2^-17 of the value, and the products take hi hi + hi lo + lo hi (K and Q are bf16
-// as given). The read-out's own operands P and U are single bf16 for a bf16 output (2^-9, like the
-// output's own rounding), pairs for an fp32 one. A and its inverse are formed in fp32 on the CUDA
+// as given). The read-out's own operand P is a single bf16 for a bf16 output (2^-9, like the output's own
+// rounding), a pair for an fp32 one. A and its inverse are formed in fp32 on the CUDA
 // cores: the inverse of the diagonal blocks of 16 by forward substitution, the rest by products of blocks
 // (no power of A is formed, which with keys alike would grow like binomials).
 //
 // Decays. G is summed in fp64 and kept as a pair of floats, so that no entry of D loses to long sums.
 // A log-decay below -88 counts as -88 (2^-127), as in linear attention.
 //
-// Warps (20): 0 loads (TMA), 1 issues the chain's products X, U, S, 2 makes the decay tables, 3 issues
+// Warps (24): 0 loads (TMA), 1 issues the chain's products X, U, S, 2 makes the decay tables, 3 issues
 // the others (K K^T with Q K^T, Q S, P U) into the gaps of the chain; 4-7 and 8-11 make A, its inverse and P of
-// every other chunk each, one to two chunks ahead; 12-19 keep the state (a value channel and half of the
-// key rows per thread), form the chain's operands and write the output while X and U are on their way.
+// every other chunk each, one to two chunks ahead; 12-15 write the output; 16-23 keep the state (a value
+// channel and half of the key rows per thread) and form the chain's operands.
 #include <atomic>
 
 #include "kda_delta.cuh"
@@ -37,11 +37,12 @@ namespace kda {
 namespace {
 
 constexpr int kC = 64;             // tokens per chunk
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
 constexpr int kKQ = 3, kTabs = 4;          // buffers
 constexpr uint32_t kTileKQ = 32768;        // 64 rows of K, then 64 of Q, x 128 channels, two 64-channel blocks
 constexpr uint32_t kTileV = 16384, kTileT = 8192;  // 64 x 64 bf16
 constexpr int kStrideA = 68;       // floats per row of A
+constexpr uint32_t kProbes = 2000000;
 constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453, kMinLog2 = -127.;
 
 struct Table {  // decays of one chunk; sums in log2 units
@@ -70,7 +71,7 @@ struct Control {
 
 template <bool kOutBF16>
 struct Cfg {
-  static constexpr bool kPair = !kOutBF16;  // P and U of the read-out as pairs
+  static constexpr bool kPair = !kOutBF16;  // P as a pair
   static constexpr int kV = kPair ? 1 : 2, kP = kPair ? 2 : 3;  // buffers
   static constexpr uint32_t kTileP = (kPair ? 2 : 1) * kTileT;
   static constexpr uint32_t oV = kKQ * kTileKQ, oT = oV + kV * kTileV, oP = oT + 4 * kTileT,
@@ -89,17 +90,17 @@ struct Run {
   int width;           // columns of `from` and `to`: d_v, or d_k of a map
 };
 
-// Probes (each suspends for up to kSleepNs) until the phase of this parity is complete; false, and `gave_up`
-// set, after kSleepLimit of them (2 s).
+// Probes (a failing one takes about 1 us) until the phase of this parity is complete; false, and `gave_up`
+// set, after kProbes of them.
 __device__ __forceinline__ bool bounded_wait(uint64_t &bar, uint32_t parity, volatile uint32_t &gave_up) {
   uint32_t ok;
   asm volatile(
       "{\n .reg .pred p, q;\n .reg .b32 i;\n mov.b32 i, %4;\n"
-      "PROBE:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %5;\n @p bra DONE;\n"
+      "PROBE:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra DONE;\n"
       " sub.u32 i, i, 1;\n setp.ne.u32 q, i, 0;\n @q bra PROBE;\n st.volatile.shared.b32 [%3], 1;\n"
       "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(smem_u32(&bar)), "r"(parity), "r"(smem_u32(const_cast<const uint32_t *>(&gave_up))), "n"(kSleepLimit), "n"(kSleepNs)
+      : "r"(smem_u32(&bar)), "r"(parity), "r"(smem_u32(const_cast<const uint32_t *>(&gave_up))), "n"(kProbes)
       : "memory");
   return ok != 0;
 }
@@ -116,35 +117,44 @@ __device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sy
 template <int kRegs>
 __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
-// D (+)= A B of 16 x 8 x 8 in tf32 (fp32 bits, of which the product takes the upper 19)
-__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+// D (+)= A B of 16 x 8 x 16 in fp16 with fp32 sums
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-// One warp: to = +- x m for 16 rows and 8 kN columns, over 8 kK inner entries, of fp32 blocks in rows of
-// kStrideA. Each operand is a pair of tf32 whose low parts' product (2^-22) is left out.
+// One warp: to = +- x m for 16 rows and 8 kN columns, over 16 kK inner entries, of fp32 blocks in rows of
+// kStrideA. Each operand is a pair of fp16 (2^-22; the entries are at most about one, since keys are unit
+// vectors) whose low parts' product is left out.
 template <int kK, int kN>
 __device__ __forceinline__ void block_product(const float *x, const float *m, float *to, bool negate, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  auto split = [](float v, uint32_t &hi, uint32_t &lo) {
-    hi = __float_as_uint(v) & 0xffffe000u;
-    lo = __float_as_uint(v - __uint_as_float(hi));
+  auto split = [](float2 v, uint32_t &hi, uint32_t &lo) {
+    hi = pack_f16x2(v.x, v.y);
+    float2 h;
+    asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, u;\n}\n" : "=f"(h.x), "=f"(h.y) : "r"(hi));
+    const float2 rest = f2_fma(h, make_float2(-1.f, -1.f), v);
+    lo = pack_f16x2(rest.x, rest.y);
   };
   float d[kN][3][4] = {};
-  const float *xr = x + g * kStrideA + t, *mr = m + t * kStrideA + g;
-#pragma unroll 1
-  for (int k = 0; k < kK; ++k, xr += 8, mr += 8 * kStrideA) {
+  const float *xr = x + g * kStrideA + 2 * t, *mr = m + 2 * t * kStrideA + g;
+#pragma unroll
+  for (int k = 0; k < kK; ++k, xr += 16, mr += 16 * kStrideA) {
     uint32_t ah[4], al[4];
-    split(xr[0], ah[0], al[0]), split(xr[8 * kStrideA], ah[1], al[1]);
-    split(xr[4], ah[2], al[2]), split(xr[8 * kStrideA + 4], ah[3], al[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      split(*reinterpret_cast<const float2 *>(xr + (e & 1) * 8 * kStrideA + (e >> 1) * 8), ah[e], al[e]);
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       uint32_t bh[2], bl[2];
-      split(mr[8 * j], bh[0], bl[0]), split(mr[4 * kStrideA + 8 * j], bh[1], bl[1]);
-      mma_tf32(d[j][0], ah, bh);
-      mma_tf32(d[j][1], ah, bl);
-      mma_tf32(d[j][2], al, bh);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float *p = mr + e * 8 * kStrideA + 8 * j;
+        split(make_float2(p[0], p[kStrideA]), bh[e], bl[e]);
+      }
+      mma_f16(d[j][0], ah, bh);
+      mma_f16(d[j][1], ah, bl);
+      mma_f16(d[j][2], al, bh);
     }
   }
   const float sign = negate ? -1.f : 1.f;
@@ -210,11 +220,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kV; ++i) mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_free[i], 1);
     for (int i = 0; i < kP; ++i) mbar_init(&ctl->p_free[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&ctl->gram_done[i], 1), mbar_init(&ctl->t_free[i], 1);
-    for (int i = 0; i < kTabs; ++i) mbar_init(&ctl->tab_full[i], 1), mbar_init(&ctl->tab_free[i], 12);
+    for (int i = 0; i < kTabs; ++i) mbar_init(&ctl->tab_full[i], 1), mbar_init(&ctl->tab_free[i], run.emit ? 16 : 12);
     mbar_init(&ctl->t_full, 4), mbar_init(&ctl->gram_read, 4), mbar_init(&ctl->zeroed, 4);
     for (int i = 0; i < 2; ++i) mbar_init(&ctl->s_full[i], 8), mbar_init(&ctl->r_full[i], 8), mbar_init(&ctl->up_full[i], 8);
     mbar_init(&ctl->x_done, 1), mbar_init(&ctl->xq_done, 1), mbar_init(&ctl->u_done, 1), mbar_init(&ctl->d_done, 1);
-    mbar_init(&ctl->o_done, 1), mbar_init(&ctl->o_read, 8), mbar_init(&ctl->drain, 2);
+    mbar_init(&ctl->o_done, 1), mbar_init(&ctl->o_read, 4), mbar_init(&ctl->drain, 2);
     ctl->gave_up = 0;
     fence_mbarrier_init();
   }
@@ -234,9 +244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_warp = [&](uint64_t &bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
   const bool partial = len % kC != 0;  // the last chunk's rows behind the run are zeroed in K and V
 
-  // registers by warpgroup, out of the 96 each that the launch holds: 64 + 2 x 80 + 2 x 128 = 5 x 96
+  // registers by warpgroup, out of the 80 each that the launch holds: 56 + 2 x 72 + 40 + 2 x 120 = 6 x 80
   if (warp < 4) {
-  registers_down<64>();
+  registers_down<56>();
   if (warp == 0) {
     // ---- loads
     if (lane == 0) {
@@ -380,39 +390,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       mma_commit(leader, ctl->gram_done[n & 1]);
       return true;
     };
-    bool ok = true;
+    // K K^T and Q K^T two chunks ahead, while X becomes R; Q S while U becomes U'; P U while S is made
 #pragma unroll 1
-    for (int n = -2; ok && n < chunks; ++n) {  // K K^T and Q K^T two chunks ahead
-      if (run.emit && n >= 0) {
-        if (!wait_warp(ctl->x_done, n)) break;
-        if (n > 0 && !wait_warp(ctl->o_read, n - 1)) break;
-        tc_fence_after();
-        const uint64_t d = dKQ + ((n % kKQ) * (kTileKQ >> 4) + (8192 >> 4));
+    for (int n = -2; n < chunks; ++n) {
+      const bool here = run.emit && n >= 0;
+      if (here && !wait_warp(ctl->x_done, n)) break;
+      if (n + 2 < chunks && !gram(n + 2)) break;
+      if (!here) continue;
+      if (!wait_warp(ctl->u_done, n)) break;
+      if (n > 0 && !wait_warp(ctl->o_read, n - 1)) break;
+      tc_fence_after();
+      const uint64_t d = dKQ + ((n % kKQ) * (kTileKQ >> 4) + (8192 >> 4));
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          if (ks >= nk) break;
-          const uint64_t b = d + ((ks >> 2) * 1024 + (ks & 3) * 2);
-          mma_ts(leader, tXQ, tS + 16 * ks, b, i64, ks > 0);
-          if constexpr (kPair) mma_ts(leader, tXQ, tS + 16 * ks + 8, b, i64, 1);
-        }
-        mma_commit(leader, ctl->xq_done);
+      for (int ks = 0; ks < 8; ++ks) {
+        if (ks >= nk) break;
+        const uint64_t b = d + ((ks >> 2) * 1024 + (ks & 3) * 2);
+        mma_ts(leader, tXQ, tS + 16 * ks, b, i64, ks > 0);
+        mma_ts(leader, tXQ, tS + 16 * ks + 8, b, i64, 1);
       }
-      if (n + 2 < chunks) ok = gram(n + 2);
-      if (ok && run.emit && n >= 0) {
-        const uint64_t dPn = desc_k(base + F::oP) + n % kP * (F::kTileP >> 4);
-        if (!wait_warp(ctl->up_full[1], n)) break;  // (and the first half, and t_full, which U waited for)
-        tc_fence_after();
+      mma_commit(leader, ctl->xq_done);
+      const uint64_t dPn = desc_k(base + F::oP) + n % kP * (F::kTileP >> 4);
+      if (!wait_warp(ctl->d_done, n)) break;  // (U for the read-out came before)
+      tc_fence_after();
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          mma_ts(leader, tO, tUH + 8 * ks, dPn + 2 * ks, i64, ks > 0);
-          if constexpr (kPair) {
-            mma_ts(leader, tO, tUH + 8 * ks, dPn + (kTileT >> 4) + 2 * ks, i64, 1);
-            mma_ts(leader, tO, tUH + 32 + 8 * ks, dPn + 2 * ks, i64, 1);
-          }
-        }
-        mma_commit(leader, ctl->o_done);
-        mma_commit(leader, ctl->p_free[n % kP]);
+      for (int ks = 0; ks < 4; ++ks) {
+        mma_ts(leader, tO, tUH + 8 * ks, dPn + 2 * ks, i64, ks > 0);
+        mma_ts(leader, tO, tUH + 32 + 8 * ks, dPn + 2 * ks, i64, 1);
+        if constexpr (kPair) mma_ts(leader, tO, tUH + 8 * ks, dPn + (kTileT >> 4) + 2 * ks, i64, 1);
       }
+      mma_commit(leader, ctl->o_done);
+      mma_commit(leader, ctl->p_free[n % kP]);
     }
     mma_commit(leader, ctl->drain);
     if (leader) mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
@@ -462,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   } else if (warp < 12) {
-    registers_down<80>();
+    registers_down<72>();
     // ---- A, its inverse and P: warps 4 to 7 of the even chunks, 8 to 11 of the odd ones
     const int w = warp & 3, group = (warp >> 2) - 1, wt = tid & 127;
     float *const sA = reinterpret_cast<float *>(smem + F::oA) + group * (kC * kStrideA);
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c = 8 * (w & 1);
 #pragma unroll 1
         for (int p = 0; p < 2; ++p) {
-          block_product<2, 1>(D + 16 * kStrideA + 16 * p, (p == 0 ? D : y16) + c, (p == 0 ? y16 : D + 16 * kStrideA) + c,
+          block_product<1, 1>(D + 16 * kStrideA + 16 * p, (p == 0 ? D : y16) + c, (p == 0 ? y16 : D + 16 * kStrideA) + c,
                               p != 0, lane);
           if (p == 0) sync_pair();
         }
@@ -615,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = 16 * (w & 1), c = 16 * (w >> 1);
 #pragma unroll 1
         for (int p = 0; p < 2; ++p) {
-          block_product<4, 2>(sA + (32 + r) * kStrideA + 32 * p, (p == 0 ? sA : Y) + c,
+          block_product<2, 2>(sA + (32 + r) * kStrideA + 32 * p, (p == 0 ? sA : Y) + c,
                               (p == 0 ? Y + r * kStrideA : sA + (32 + r) * kStrideA) + c, p != 0, lane);
           if (p == 0) sync();
         }
@@ -655,10 +662,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&ctl->tab_free[n % kTabs]);
       }
     }
+  } else if (warp < 16) {
+    registers_down<40>();
+    // ---- the output: value channel c, O = scale (Q S) + P U
+    if (run.emit) {
+      const int w = warp & 3, c = 32 * w + lane;
+      const uint32_t row = uint32_t(32 * w) << 16;
+      constexpr int kEs = kOutBF16 ? 2 : 4;
+      const uint32_t step = uint32_t(a.H) * uint32_t(a.d_v) * kEs;  // from token to token; 16 of them are below 2^32 (see delta_plan)
+      uint8_t *out = static_cast<uint8_t *>(a.out) + ((run.t0 * a.H + h) * a.d_v + c) * kEs;
+#pragma unroll 1
+      for (int n = 0; n < chunks; ++n) {
+        const Table &tb = tab[n % kTabs];
+        if (!wait_warp(ctl->tab_full[n % kTabs], n / kTabs)) break;
+        if (!wait_warp(ctl->o_done, n)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int t = 0; t < kC; t += 8, out += uint64_t(step) * 8) {
+          const int part = c < a.d_v ? len - n * kC - t : 0;
+          float x[8], o[8];
+          tmem_ld8(tXQ + row + t, x);
+          tmem_ld8(tO + row + t, o);
+          tmem_ld_wait(x, o);
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(&tb.out[t + j]);
+            const float2 y0 = f2_fma(make_float2(f.x, f.y), make_float2(x[j], x[j + 1]), make_float2(o[j], o[j + 1]));
+            const float2 y1 = f2_fma(make_float2(f.z, f.w), make_float2(x[j + 2], x[j + 3]), make_float2(o[j + 2], o[j + 3]));
+            x[j] = y0.x, x[j + 1] = y0.y, x[j + 2] = y1.x, x[j + 3] = y1.y;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < part) store_elem<kOutBF16>(out + uint64_t(uint32_t(j) * step), 0, x[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctl->o_read);
+          mbar_arrive(&ctl->tab_free[n % kTabs]);
+        }
+      }
+    }
   } else {
-    registers_up<128>();
+    registers_up<120>();
     // ---- the state: value channel c, key rows 64 half .. + 63; tokens 32 half .. + 31 of R and U'
-    const int w = warp & 3, half = (warp - 12) >> 2, c = 32 * w + lane;
+    const int w = warp & 3, half = (warp - 16) >> 2, c = 32 * w + lane;
     const uint32_t row = uint32_t(32 * w) << 16;
     const uint32_t rS = tS + row + 64 * half, rX = tX + row + 32 * half, rU = tU + row + 32 * half;
     const uint32_t rUH = tUH + row + 16 * half;
@@ -696,9 +744,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_st8(at, hi);
       tmem_st8(at + 8, lo);
     };
-    constexpr int kEs = kOutBF16 ? 2 : 4;
-    const uint32_t step = uint32_t(a.H) * uint32_t(a.d_v) * kEs;  // from token to token; 16 of them are below 2^32 (see delta_plan)
-    uint8_t *out = static_cast<uint8_t *>(a.out) + (((run.t0 + 32 * half) * a.H + h) * a.d_v + c) * kEs;
     auto give = [&](uint64_t &bar) {  // what this warp wrote to tensor memory is there for the MMAs
       tmem_st_wait();
       tc_fence_before();
@@ -709,37 +754,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = -1;; ++n) {
       const Table &tb = tab[n & (kTabs - 1)];
       if (n >= 0) {
-      if (n < chunks && !wait_warp(ctl->tab_full[n % kTabs], n / kTabs)) break;
-      if (run.emit && n > 0) {  // the read-out of chunk n - 1, while X is on its way: O = scale (Q S) + P U
-        if (!wait_warp(ctl->o_done, n - 1)) break;
-        tc_fence_after();
-        const Table &was = tab[(n - 1) % kTabs];
-#pragma unroll 1
-        for (int p = 0; p < 32; p += 16, out += uint64_t(step) * 16) {
-          const int part = c < a.d_v ? len - (n - 1) * kC - 32 * half - p : 0;
-          float x[16], o[16];
-          tmem_ld16(tXQ + row + 32 * half + p, x);
-          tmem_ld16(tO + row + 32 * half + p, o);
-          tmem_ld_wait(x, o);
-#pragma unroll
-          for (int j = 0; j < 16; j += 2) {
-            const float2 y = f2_fma(*reinterpret_cast<const float2 *>(&was.out[32 * half + p + j]), make_float2(x[j], x[j + 1]),
-                                    make_float2(o[j], o[j + 1]));
-            x[j] = y.x, x[j + 1] = y.y;
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (j < part) store_elem<kOutBF16>(out + uint64_t(uint32_t(j) * step), 0, x[j]);
-        }
-        out += uint64_t(step) * 32;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl->o_read);
-          mbar_arrive(&ctl->tab_free[(n - 1) % kTabs]);
-        }
-      }
       if (n >= chunks) break;
+      if (!wait_warp(ctl->tab_full[n % kTabs], n / kTabs)) break;
+      if (run.emit && n > 0 && !wait_warp(ctl->o_done, n - 1)) break;  // the read-out's U of chunk n - 1 is read
       // X = K S, split where it stands
       if (!wait_warp(ctl->x_done, n)) break;
       tc_fence_after();
@@ -758,20 +775,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         float x[16];
         tmem_ld16_wait(rU + 16 * p, x);
         if (run.emit) {
-          float hi[8];
+          float hi[8], lo[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) hi[j] = __uint_as_float(pack_bf16x2(x[2 * j], x[2 * j + 1]));
-          tmem_st8(rUH + 8 * p, hi);
-          if constexpr (kPair) {
-            float lo[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              uint32_t h, l;
-              split_pair(x[2 * j], x[2 * j + 1], h, l);
-              lo[j] = __uint_as_float(l);
-            }
-            tmem_st8(rUH + 32 + 8 * p, lo);
+          for (int j = 0; j < 8; ++j) {
+            uint32_t h, l;
+            split_pair(x[2 * j], x[2 * j + 1], h, l);
+            hi[j] = __uint_as_float(h), lo[j] = __uint_as_float(l);
           }
+          tmem_st8(rUH + 8 * p, hi);
+          tmem_st8(rUH + 32 + 8 * p, lo);
         }
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
@@ -802,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (n + 1 < chunks) give(ctl->s_full[i >> 5]);
       }
-      if (!run.emit && n >= 0) {
+      if (n >= 0) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->tab_free[n % kTabs]);
       }
