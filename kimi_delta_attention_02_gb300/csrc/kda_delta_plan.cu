@@ -1,5 +1,7 @@
 // kda_delta_plan.cu -- how a prefill of the gated delta rule is cut (host), and the kernel that chains the
 // segments' states.
+#include <atomic>
+
 #include "kda_delta.cuh"
 
 namespace kda {
@@ -7,73 +9,100 @@ namespace {
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-constexpr int kChainCols = 32, kChainThreads = 256;
+constexpr int kChainCols = 16, kChainThreads = 256, kChainStride = 132;  // (floats per row of M: conflict-free)
+constexpr int kChainBytes = (2 * 128 * kChainStride + 128 * kChainCols) * 4;
 
 // Pass 2: E_{j+1} = M_j E_j + B_j for the segments between a sequence's first and last, in fp32. The
 // first segment's end state is E_1; B_j gives way to E_{j+1}. The CTAs of a sequence's first segment
-// (blockIdx.y is the piece) walk its segments, 32 value columns each: thread (rg, cg) forms rows
-// 4 rg .. + 3 of columns 4 cg .. + 3, E in shared memory, M through L1.
+// (blockIdx.y is the piece) walk its segments, 16 value columns each: thread (rg, cg) forms rows rg, rg + 32,
+// .. of columns 2 cg, + 1, with E and M in shared memory and the next M on its way (5 us a step; 13 us with
+// M read through L1 as it is used).
 __global__ void __launch_bounds__(kChainThreads) delta_chain_kernel(const DeltaArgs a) {
-  __shared__ __align__(16) float E[128][kChainCols];
+  extern __shared__ __align__(16) float chain_smem[];
+  float *const E = chain_smem + 2 * 128 * kChainStride;  // [128][16]
   LinearSlot s;
   if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, blockIdx.y, s) || !s.first) return;
   const int segs = (a.cu[s.n + 1] - a.cu[s.n] - 1) / a.plan.seg_len + 1;
-  const int h = blockIdx.x % a.H, c = int(blockIdx.x) / a.H * kChainCols + 4 * (threadIdx.x & 7);
-  const int rg = threadIdx.x >> 3, r0 = 4 * rg, cs = 4 * (threadIdx.x & 7);
-  const bool ok = c < a.d_v && r0 < a.d_k;  // (d_k and d_v are multiples of 8)
+  const int h = blockIdx.x % a.H, cg = threadIdx.x & 7, rg = threadIdx.x >> 3;
+  const int c = int(blockIdx.x) / a.H * kChainCols + 2 * cg;
   const int64_t place = delta_place(a, s);
   float *ends = reinterpret_cast<float *>(a.workspace + a.plan.ends);
   const float *maps = reinterpret_cast<const float *>(a.workspace + a.plan.maps);
   auto at = [&](int64_t p, int r) { return ends + ((p * a.H + h) * a.d_k + r) * a.d_v + c; };
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (ok) *reinterpret_cast<float4 *>(&E[r0 + i][cs]) = *reinterpret_cast<const float4 *>(at(place, r0 + i));
-  for (int j = 1; j + 1 < segs; ++j) {
-    __syncthreads();
-    const float *M = maps + ((place + j) * a.H + h) * int64_t(a.d_k) * a.d_k + r0 * a.d_k;
-    float4 acc[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      acc[i] = ok ? *reinterpret_cast<const float4 *>(at(place + j, r0 + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < a.d_k; k += 4) {
-      float4 m[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        m[i] = ok ? *reinterpret_cast<const float4 *>(M + i * a.d_k + k) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float4 x = *reinterpret_cast<const float4 *>(&E[k + e][cs]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float y = e == 0 ? m[i].x : e == 1 ? m[i].y : e == 2 ? m[i].z : m[i].w;
-          acc[i].x = fmaf(y, x.x, acc[i].x), acc[i].y = fmaf(y, x.y, acc[i].y);
-          acc[i].z = fmaf(y, x.z, acc[i].z), acc[i].w = fmaf(y, x.w, acc[i].w);
-        }
+  auto fetch = [&](int j) {  // M_j (d_k is a multiple of 8); one group of copies per call, also where there is none
+    if (j + 1 < segs) {
+      const float *M = maps + ((place + j) * a.H + h) * int64_t(a.d_k) * a.d_k;
+      const int per_row = a.d_k >> 2;
+      for (int i = threadIdx.x; i < a.d_k * per_row; i += kChainThreads) {
+        const int r = i / per_row, k = i % per_row * 4;
+        cp_async_16_zfill(&chain_smem[(j & 1) * 128 * kChainStride + r * kChainStride + k], M + i * 4, true);
       }
     }
-    __syncthreads();  // every thread is past E before it is overwritten
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto on = [&](int i) { return rg + 32 * i < a.d_k && c < a.d_v; };  // (d_v is a multiple of 8)
+  fetch(1);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = on(i) ? *reinterpret_cast<const float2 *>(at(place, rg + 32 * i)) : make_float2(0.f, 0.f);
+    *reinterpret_cast<float2 *>(&E[(rg + 32 * i) * kChainCols + 2 * cg]) = x;
+  }
+  for (int j = 1; j + 1 < segs; ++j) {
+    fetch(j + 1);
+    float2 acc[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (ok) {
-        *reinterpret_cast<float4 *>(&E[r0 + i][cs]) = acc[i];
-        *reinterpret_cast<float4 *>(at(place + j, r0 + i)) = acc[i];
+      acc[i] = on(i) ? *reinterpret_cast<const float2 *>(at(place + j, rg + 32 * i)) : make_float2(0.f, 0.f);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    const float *M = chain_smem + (j & 1) * 128 * kChainStride + rg * kChainStride;
+#pragma unroll 4
+    for (int k = 0; k < a.d_k; k += 4) {
+      float2 x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = *reinterpret_cast<const float2 *>(&E[(k + e) * kChainCols + 2 * cg]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (rg + 32 * i >= a.d_k) break;
+        const float4 m = *reinterpret_cast<const float4 *>(&M[32 * i * kChainStride + k]);
+        acc[i] = f2_fma(make_float2(m.x, m.x), x[0], acc[i]);
+        acc[i] = f2_fma(make_float2(m.y, m.y), x[1], acc[i]);
+        acc[i] = f2_fma(make_float2(m.z, m.z), x[2], acc[i]);
+        acc[i] = f2_fma(make_float2(m.w, m.w), x[3], acc[i]);
       }
+    }
+    __syncthreads();  // every thread is past E and M before they are overwritten
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      *reinterpret_cast<float2 *>(&E[(rg + 32 * i) * kChainCols + 2 * cg]) = acc[i];
+      if (on(i)) *reinterpret_cast<float2 *>(at(place + j, rg + 32 * i)) = acc[i];
+    }
   }
 }
 
 }  // namespace
 
 cudaError_t launch_delta_chain(const DeltaArgs &a, cudaStream_t stream) {
+  static std::atomic<uint64_t> granted;  // as in the other kernels
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (bit == 0 || (granted.load(std::memory_order_acquire) & bit) == 0) {
+    e = cudaFuncSetAttribute(delta_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kChainBytes);
+    if (e != cudaSuccess) return e;
+    granted.fetch_or(bit, std::memory_order_release);
+  }
   const dim3 grid(unsigned(a.H * ((a.d_v + kChainCols - 1) / kChainCols)), unsigned(a.plan.inner));
-  delta_chain_kernel<<<grid, kChainThreads, 0, stream>>>(a);
+  delta_chain_kernel<<<grid, kChainThreads, kChainBytes, stream>>>(a);
   return cudaGetLastError();
 }
 
 // A CTA of the tensor-core kernel holds one (sequence, head) from end to end, one CTA per SM, so few long
 // sequences leave SMs idle. A sequence cut into m segments runs 2 m - 3 of them side by side in pass 1 and
 // m - 1 in pass 3: two segments' time instead of m, for up to three times the work. Of a single sequence
-// m is the largest that fits; of several the lengths are not known here, and cuts lie so far apart that
+// m is that of the least time by waves of CTAs (a chunk of 64 tokens takes some 4 us, a step of pass 2 five,
+// a pass ten to begin and end; T = 65536, 16 heads: m = 10); of several the lengths are not known here, and cuts lie so far apart that
 // pass 1 fills the SMs at most twice. Sequences in more chains than SMs run longest first.
 DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool in_bf16, bool out_bf16, bool recurrent,
                      size_t workspace_bytes) {
@@ -86,14 +115,19 @@ DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool 
   (void)out_bf16;
   int64_t len = 0;
   if (num_seqs == 1) {
-    const int64_t m = (kLinearSMs / H + 3) / 2;
-    if (m >= 3) len = (total + m - 1) / m;
+    const auto waves = [&](int64_t pieces) { return (pieces * H + kLinearSMs - 1) / kLinearSMs; };
+    int64_t best = total / 64 * 4 * waves(1);
+    for (int64_t m = 3; m <= 64 && total >= m * 512; ++m) {
+      const int64_t us = (waves(2 * m - 3) + waves(m - 1)) * (total / (m * 64) * 4 + 10) + 5 * m;
+      if (us < best) best = us, len = (total + m - 1) / m;
+    }
   } else {
     len = (2 * total * H + kLinearSMs - 1) / kLinearSMs;
   }
   len = (len + 63) / 64 * 64;
   if (len > 0 && len < 512) len = 512;
-  if (len > 0 && total >= 3 * len - 63 * 3 && 8 * total >= len * num_seqs) {
+  // (cuts that most sequences are far too short for would only cost the order of the others)
+  if (len > 0 && total > 2 * len && 8 * total >= len * num_seqs) {
     const int64_t inner = total / len;
     const size_t ends = align256(size_t(inner) * H * d_k * d_v * 4), maps = align256(size_t(inner) * H * d_k * d_k * 4);
     if (ends + maps <= workspace_bytes) {
