@@ -47,7 +47,7 @@ __device__ __forceinline__ int64_t delta_place(const DeltaArgs &a, const LinearS
 }
 
 // The plan for a call that has this much workspace (SIZE_MAX: what it would like to have).
-DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool in_bf16, bool out_bf16, bool recurrent,
+DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool in_bf16, bool recurrent,
                      size_t workspace_bytes);
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream);
 cudaError_t launch_delta_chunked(const DeltaArgs &a, bool out_bf16, cudaStream_t stream);

@@ -2,23 +2,25 @@
 // inputs, head sizes in multiples of 8), in chunks of 64 tokens.
 //
 // With G the cumulative log-decay inside a chunk, D_ti = e^{G_t - G_i}, and S the state that enters it,
-//     A_ti = beta_t D_ti (k_t . k_i), i < t;      T' = (I + A)^-1 diag(beta)
-//     U    = T' (V - diag(e^G) K S)
-//     O    = scale (diag(e^G) Q S + P U),         P_ti = D_ti (q_t . k_i), i <= t
+//     A_ti = beta_t D_ti (k_t . k_i), i < t;      T' = (I + A)^-1 diag(beta),   T'' = -T' diag(e^G)
+//     U    = T' V + T'' X,                        X = K S
+//     O    = scale diag(e^G) Q S + P U,           P_ti = scale D_ti (q_t . k_i), i <= t
 //     S   <- e^{G_C} S + K^T U',                  U'_i = e^{G_C - G_i} u_i .
 // Everything that touches the state is formed transposed, with the value channels as the 128 rows of
-// the MMA: X^T = S^T K^T, U^T = R^T T'^T, S^T += U'^T K, O^T = U^T P^T. So the state's way from one
-// chunk to the next (S -> X -> R -> U -> U' -> S) stays in one lane of tensor memory per value
-// channel: each product's accumulator is read by the thread that owns its lane, turned into the next
-// product's A operand and written back over the same columns. Shared memory only holds B operands: K and
-// Q as they come, T' and P. The state itself stays in fp32 registers.
+// the MMA: X^T = S^T K^T, U^T = V^T T'^T + X^T T''^T, S^T += U'^T K, O^T = U^T P^T. So the state's way from
+// one chunk to the next (S -> X -> U -> U' -> S) stays in one lane of tensor memory per value channel: each
+// product's accumulator is read by a thread that owns its lane, split into the next product's A operand
+// and written back over the same columns. Shared memory only holds B operands (K and Q as they come, T', T''
+// and P) and V, the A operand of T' V, which runs ahead of the chain. The state itself stays in fp32 registers.
 //
-// Roundings. The operands of what reaches the state (S, R, T', U') are pairs of bf16, hi + lo, each
-// pair off by at most 2^-17 of the value, and the products take hi hi + hi lo + lo hi (K and Q are bf16
-// as given). The read-out's own operand P is a single bf16 for a bf16 output (2^-9, like the output's own
-// rounding), a pair for an fp32 one. A and its inverse are formed in fp32 on the CUDA
-// cores: the inverse of the diagonal blocks of 16 by forward substitution, the rest by products of blocks
-// (no power of A is formed, which with keys alike would grow like binomials).
+// Roundings. The operands of what reaches the state (S, X, T', T'', U') are pairs of bf16, hi + lo, each
+// pair off by at most 2^-17 of the value, and the products take hi hi + hi lo + lo hi (K, Q and V are bf16
+// as given). The read-out takes S and U as the same kind of pairs; its P is a single bf16 for a bf16 output
+// (2^-9, the size of the output's own rounding), a pair for an fp32 one. A is formed in fp32. Its inverse
+// starts from blocks of 8 by forward substitution in fp32, joined to 16 in fp32, and to 32 and 64 by
+// products of blocks in pairs of tf32 (2^-20) on the tensor cores. No power of A is formed, which with keys
+// alike would grow like binomials. At T = 4096, 96 heads of 128: bf16 output off by 0.0023 in the 2-norm (its
+// rounding alone: 0.0017), fp32 output by 7e-6, state by 5e-6.
 //
 // Decays. G is summed in fp64 and kept as a pair of floats, so that no entry of D loses to long sums.
 // A log-decay below -88 counts as -88 (2^-127), as in linear attention.
@@ -27,6 +29,12 @@
 // the others (K K^T with Q K^T, Q S, P U) into the gaps of the chain; 4-7 and 8-11 make A, its inverse and P of
 // every other chunk each, one to two chunks ahead; 12-15 write the output; 16-23 keep the state (a value
 // channel and half of the key rows per thread) and form the chain's operands.
+//
+// What bounds it: the chain's latency. A chunk takes 3.9 us (T = 4096, 96 heads of 128: 250 us for 64 of them,
+// against 63 us to move the bytes and 2.41 ms of the token kernel), of which the three products take 0.8 us
+// and the hand-overs between MMA and warps (six, 0.15 to 0.2 us each) and the splitting of X, U' and S the
+// rest, in competition with warps 4 to 11 for the issue slots: 203 us with those idle. Hence two halves per
+// hand-over, so that a product starts on the first half, and V's product and the read-out off the chain.
 #include <atomic>
 
 #include "kda_delta.cuh"
@@ -117,44 +125,42 @@ __device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sy
 template <int kRegs>
 __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
-// D (+)= A B of 16 x 8 x 16 in fp16 with fp32 sums
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+// D += A B of 16 x 8 x 8 in tf32 with fp32 sums
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 // One warp: to = +- x m for 16 rows and 8 kN columns, over 16 kK inner entries, of fp32 blocks in rows of
-// kStrideA. Each operand is a pair of fp16 (2^-22; the entries are at most about one, since keys are unit
-// vectors) whose low parts' product is left out.
+// kStrideA. Each operand is a pair of tf32, cut off, not rounded (2^-20, with the range of fp32: where keys
+// are not unit vectors or the decay grows, the entries do), whose low parts' product is left out. Unrolled by two: in full it is code enough to slow the whole CTA by 6 %.
 template <int kK, int kN>
 __device__ __forceinline__ void block_product(const float *x, const float *m, float *to, bool negate, int lane) {
   const int g = lane >> 2, t = lane & 3;
-  auto split = [](float2 v, uint32_t &hi, uint32_t &lo) {
-    hi = pack_f16x2(v.x, v.y);
-    float2 h;
-    asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, u;\n}\n" : "=f"(h.x), "=f"(h.y) : "r"(hi));
-    const float2 rest = f2_fma(h, make_float2(-1.f, -1.f), v);
-    lo = pack_f16x2(rest.x, rest.y);
+  auto split = [](float v, uint32_t &hi, uint32_t &lo) {
+    hi = __float_as_uint(v) & 0xffffe000u;
+    lo = __float_as_uint(v - __uint_as_float(hi)) & 0xffffe000u;
   };
   float d[kN][3][4] = {};
+  // (inner entries 2 t and 2 t + 1 stand where the instruction has t and t + 4, in both operands)
   const float *xr = x + g * kStrideA + 2 * t, *mr = m + 2 * t * kStrideA + g;
-#pragma unroll
-  for (int k = 0; k < kK; ++k, xr += 16, mr += 16 * kStrideA) {
+#pragma unroll 2
+  for (int k = 0; k < 2 * kK; ++k, xr += 8, mr += 8 * kStrideA) {
     uint32_t ah[4], al[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      split(*reinterpret_cast<const float2 *>(xr + (e & 1) * 8 * kStrideA + (e >> 1) * 8), ah[e], al[e]);
+    for (int e = 0; e < 2; ++e) {
+      const float2 v = *reinterpret_cast<const float2 *>(xr + e * 8 * kStrideA);
+      split(v.x, ah[e], al[e]);
+      split(v.y, ah[e + 2], al[e + 2]);
+    }
 #pragma unroll
     for (int j = 0; j < kN; ++j) {
       uint32_t bh[2], bl[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float *p = mr + e * 8 * kStrideA + 8 * j;
-        split(make_float2(p[0], p[kStrideA]), bh[e], bl[e]);
-      }
-      mma_f16(d[j][0], ah, bh);
-      mma_f16(d[j][1], ah, bl);
-      mma_f16(d[j][2], al, bh);
+      split(mr[8 * j], bh[0], bl[0]);
+      split(mr[kStrideA + 8 * j], bh[1], bl[1]);
+      mma_tf32(d[j][0], ah, bh);
+      mma_tf32(d[j][1], ah, bl);
+      mma_tf32(d[j][2], al, bh);
     }
   }
   const float sign = negate ? -1.f : 1.f;
@@ -233,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-  // S and K^T U' (128 columns), X and R, U and U', Q S, O, K K^T and Q K^T, U for the read-out (hi, lo)
+  // S and K^T U' (128 columns), X, U and U', Q S, O, K K^T and Q K^T, U for the read-out (hi, lo)
   const uint32_t tS = tmem, tX = tmem + 128, tU = tmem + 192, tXQ = tmem + 256, tO = tmem + 320, tG = tmem + 384,
                  tUH = tmem + 448;
 
@@ -246,228 +252,228 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // registers by warpgroup, out of the 80 each that the launch holds: 56 + 2 x 72 + 40 + 2 x 120 = 6 x 80
   if (warp < 4) {
-  registers_down<56>();
-  if (warp == 0) {
-    // ---- loads
-    if (lane == 0) {
-      int kq = 0, vs = 0;  // issued
-      uint32_t ks = 0, vs_ = 0, ks_turn = 1, vs_turn = 1;  // buffers, and the parity of the use before
-      const uint32_t kq_bytes = kb * (run.emit ? 16384 : 8192);
-#pragma unroll 1
-      for (int32_t t = int32_t(run.t0), n = 0; n < chunks; ++n, t += kC) {
-        if (!wait(ctl->kq_free[ks], ks_turn)) break;
-        uint8_t *dst = smem + ks * kTileKQ;
-        uint64_t &full = ctl->kq_full[ks];
-        mbar_arrive_expect_tx(&full, kq_bytes);
-#pragma unroll 1
-        for (int b = 0; b < kb; ++b) {
-          tma_load_3d(dst + b * 16384, &mk, &full, 64 * b, hk, t);
-          if (run.emit) tma_load_3d(dst + b * 16384 + 8192, &mq, &full, 64 * b, hk, t);
+    registers_down<56>();
+    if (warp == 0) {
+      // ---- loads
+      if (lane == 0) {
+        int kq = 0, vs = 0;  // issued
+        uint32_t ks = 0, vs_ = 0, ks_turn = 1, vs_turn = 1;  // buffers, and the parity of the use before
+        const uint32_t kq_bytes = kb * (run.emit ? 16384 : 8192);
+  #pragma unroll 1
+        for (int32_t t = int32_t(run.t0), n = 0; n < chunks; ++n, t += kC) {
+          if (!wait(ctl->kq_free[ks], ks_turn)) break;
+          uint8_t *dst = smem + ks * kTileKQ;
+          uint64_t &full = ctl->kq_full[ks];
+          mbar_arrive_expect_tx(&full, kq_bytes);
+  #pragma unroll 1
+          for (int b = 0; b < kb; ++b) {
+            tma_load_3d(dst + b * 16384, &mk, &full, 64 * b, hk, t);
+            if (run.emit) tma_load_3d(dst + b * 16384 + 8192, &mq, &full, 64 * b, hk, t);
+          }
+          ++kq;
+          if (++ks == kKQ) ks = 0, ks_turn ^= 1;
+          if (run.identity) continue;
+          if (!wait(ctl->v_free[vs_], vs_turn)) break;
+          mbar_arrive_expect_tx(&ctl->v_full[vs_], vb * 8192);
+  #pragma unroll 1
+          for (int b = 0; b < vb; ++b)
+            tma_load_3d(smem + F::oV + vs_ * kTileV + b * 8192, &mv, &ctl->v_full[vs_], 64 * b, h, t);
+          ++vs;
+          if (++vs_ == kV) vs_ = 0, vs_turn ^= 1;
         }
-        ++kq;
-        if (++ks == kKQ) ks = 0, ks_turn ^= 1;
-        if (run.identity) continue;
-        if (!wait(ctl->v_free[vs_], vs_turn)) break;
-        mbar_arrive_expect_tx(&ctl->v_full[vs_], vb * 8192);
-#pragma unroll 1
-        for (int b = 0; b < vb; ++b)
-          tma_load_3d(smem + F::oV + vs_ * kTileV + b * 8192, &mv, &ctl->v_full[vs_], 64 * b, h, t);
-        ++vs;
-        if (++vs_ == kV) vs_ = 0, vs_turn ^= 1;
+        // every load issued has landed before the CTA may end
+  #pragma unroll 1
+        for (int i = kq > kKQ ? kq - kKQ : 0; i < kq; ++i) wait(ctl->kq_full[i % kKQ], i / kKQ);
+  #pragma unroll 1
+        for (int i = vs > kV ? vs - kV : 0; i < vs; ++i) wait(ctl->v_full[i % kV], i / kV);
       }
-      // every load issued has landed before the CTA may end
-#pragma unroll 1
-      for (int i = kq > kKQ ? kq - kKQ : 0; i < kq; ++i) wait(ctl->kq_full[i % kKQ], i / kKQ);
-#pragma unroll 1
-      for (int i = vs > kV ? vs - kV : 0; i < vs; ++i) wait(ctl->v_full[i % kV], i / kV);
-    }
-  } else if (warp == 1) {
-    // ---- the chain: X = K S, U = T' R, K^T U'
-    const bool leader = elect_lane();
-    const uint32_t base = smem_u32(smem);
-    constexpr uint32_t i64 = umma_idesc_bf16(128, 64, false, false, false);
-    const uint32_t iD = umma_idesc_bf16(128, a.d_k > 64 ? 128 : 64, false, true, false);
-    constexpr uint32_t iV = umma_idesc_bf16(128, 64, true, false, false);
-    uint32_t stage = 0;
-#pragma unroll 1
-    for (int n = 0; n < chunks; ++n) {
-      // nothing, as the compiler does not see: addresses made with it are not kept in registers over the loop,
-      // forty of them
-      const uint32_t none = uint32_t(n) >> 28;
-      const uint32_t tS = tmem + none, tX = tS + 128, tU = tS + 192;
-      const uint64_t dT = desc_k(base + none + F::oT), dTW = dT + (2 * kTileT >> 4);  // T', then -T' diag(e^G), each hi and lo
-      const uint32_t tile = base + stage * kTileKQ;
-      const uint64_t dK = desc_k(tile), dKT = desc_mn(tile, 16384);
-      uint64_t &kq_full = ctl->kq_full[stage], &kq_free = ctl->kq_free[stage];
-      if (!wait_warp(kq_full, n / kKQ)) break;
-      if (++stage == kKQ) stage = 0;
-      if (partial && n + 1 == chunks && !wait_warp(ctl->zeroed, 0)) break;
-      // T' V, while S is made
-      if (!wait_warp(ctl->t_full, n)) break;
-      if (!run.identity && !wait_warp(ctl->v_full[n % kV], n / kV)) break;
-      if (n > 0 && !wait_warp(ctl->d_done, n - 1)) break;  // U' of chunk n - 1 is read
-      if (!run.identity) {
-        tc_fence_after();
-        const uint64_t dV = desc_mn(base + F::oV + n % kV * kTileV, 8192);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          mma_ss(leader, tU, dV + 128 * ks, dT + 2 * ks, iV, ks > 0);
-          mma_ss(leader, tU, dV + 128 * ks, dT + (kTileT >> 4) + 2 * ks, iV, 1);
+    } else if (warp == 1) {
+      // ---- the chain: X = K S, U = T' V + T'' X, K^T U'
+      const bool leader = elect_lane();
+      const uint32_t base = smem_u32(smem);
+      constexpr uint32_t i64 = umma_idesc_bf16(128, 64, false, false, false);
+      const uint32_t iD = umma_idesc_bf16(128, a.d_k > 64 ? 128 : 64, false, true, false);
+      constexpr uint32_t iV = umma_idesc_bf16(128, 64, true, false, false);
+      uint32_t stage = 0;
+  #pragma unroll 1
+      for (int n = 0; n < chunks; ++n) {
+        // nothing, as the compiler does not see: addresses made with it are not kept in registers over the loop,
+        // forty of them
+        const uint32_t none = uint32_t(n) >> 28;
+        const uint32_t tS = tmem + none, tX = tS + 128, tU = tS + 192;
+        const uint64_t dT = desc_k(base + none + F::oT), dTW = dT + (2 * kTileT >> 4);  // T', then T'', each hi and lo
+        const uint32_t tile = base + stage * kTileKQ;
+        const uint64_t dK = desc_k(tile), dKT = desc_mn(tile, 16384);
+        uint64_t &kq_full = ctl->kq_full[stage], &kq_free = ctl->kq_free[stage];
+        if (!wait_warp(kq_full, n / kKQ)) break;
+        if (++stage == kKQ) stage = 0;
+        if (partial && n + 1 == chunks && !wait_warp(ctl->zeroed, 0)) break;
+        // T' V, while S is made
+        if (!wait_warp(ctl->t_full, n)) break;
+        if (!run.identity && !wait_warp(ctl->v_full[n % kV], n / kV)) break;
+        if (n > 0 && !wait_warp(ctl->d_done, n - 1)) break;  // U' of chunk n - 1 is read
+        if (!run.identity) {
+          tc_fence_after();
+          const uint64_t dV = desc_mn(base + F::oV + n % kV * kTileV, 8192);
+  #pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            mma_ss(leader, tU, dV + 128 * ks, dT + 2 * ks, iV, ks > 0);
+            mma_ss(leader, tU, dV + 128 * ks, dT + (kTileT >> 4) + 2 * ks, iV, 1);
+          }
+          mma_commit(leader, ctl->v_free[n % kV]);
         }
-        mma_commit(leader, ctl->v_free[n % kV]);
-      }
-      // Each product begins with the steps whose operands come first: S, X and U' by halves of each thread's
-      // columns (steps 0, 1, 4, 5 of S, then 2, 3, 6, 7; steps 0, 2, then 1, 3 of the tokens).
-      bool ok = true;
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        ok = ok && wait_warp(ctl->s_full[p], n);
+        // Each product begins with the steps whose operands come first: S, X and U' by halves of each thread's
+        // columns (steps 0, 1, 4, 5 of S, then 2, 3, 6, 7; steps 0, 2, then 1, 3 of the tokens).
+        bool ok = true;
+  #pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          ok = ok && wait_warp(ctl->s_full[p], n);
+          if (!ok) break;
+          tc_fence_after();
+  #pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int ks = 4 * (m >> 1) + 2 * p + (m & 1);
+            if (ks >= nk) break;
+            const uint64_t b = dK + ((ks >> 2) * 1024 + (ks & 3) * 2);
+            mma_ts(leader, tX, tS + 16 * ks, b, i64, ks > 0);
+            mma_ts(leader, tX, tS + 16 * ks + 8, b, i64, 1);
+          }
+        }
         if (!ok) break;
+        mma_commit(leader, ctl->x_done);
+  #pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          ok = ok && wait_warp(ctl->r_full[p], n);
+          if (!ok) break;
+          tc_fence_after();
+  #pragma unroll
+          for (int ks = p; ks < 4; ks += 2) {
+            mma_ts(leader, tU, tX + 16 * ks, dTW + 2 * ks, i64, ks > 0 || !run.identity);
+            mma_ts(leader, tU, tX + 16 * ks, dTW + (kTileT >> 4) + 2 * ks, i64, 1);
+            mma_ts(leader, tU, tX + 16 * ks + 8, dTW + 2 * ks, i64, 1);
+          }
+        }
+        if (!ok) break;
+        mma_commit(leader, ctl->u_done);
+        mma_commit(leader, ctl->t_free[n & 1]);
+        if (run.emit && !wait_warp(ctl->xq_done, n)) break;  // Q S has read S
+  #pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          ok = ok && wait_warp(ctl->up_full[p], n);
+          if (!ok) break;
+          tc_fence_after();
+  #pragma unroll
+          for (int ks = p; ks < 4; ks += 2) {
+            mma_ts(leader, tS, tU + 16 * ks, dKT + 128 * ks, iD, ks > 0);
+            mma_ts(leader, tS, tU + 16 * ks + 8, dKT + 128 * ks, iD, 1);
+          }
+        }
+        if (!ok) break;
+        mma_commit(leader, ctl->d_done);
+        mma_commit(leader, kq_free);  // (K K^T, Q K^T and Q S were done before)
+      }
+      // no MMA is in flight when tensor memory is freed
+      mma_commit(leader, ctl->drain);
+      if (leader) mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
+    } else if (warp == 3) {
+      // ---- the other products
+      const bool leader = elect_lane();
+      const uint32_t base = smem_u32(smem);
+      constexpr uint32_t i64 = umma_idesc_bf16(128, 64, false, false, false);
+      const uint64_t dKQ = desc_k(base);
+      auto gram = [&](int n) -> bool {  // rows 0 .. 63: K K^T, 64 .. 127: Q K^T
+        if (!wait_warp(ctl->kq_full[n % kKQ], n / kKQ)) return false;
+        if (partial && n + 1 == chunks && !wait_warp(ctl->zeroed, 0)) return false;
+        if (n > 0 && !wait_warp(ctl->gram_read, n - 1)) return false;
         tc_fence_after();
-#pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const int ks = 4 * (m >> 1) + 2 * p + (m & 1);
+        const uint64_t d = dKQ + (n % kKQ) * (kTileKQ >> 4);
+  #pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
           if (ks >= nk) break;
-          const uint64_t b = dK + ((ks >> 2) * 1024 + (ks & 3) * 2);
-          mma_ts(leader, tX, tS + 16 * ks, b, i64, ks > 0);
-          mma_ts(leader, tX, tS + 16 * ks + 8, b, i64, 1);
+          const uint64_t b = d + ((ks >> 2) * 1024 + (ks & 3) * 2);
+          mma_ss(leader, tG, b, b, i64, ks > 0);
         }
-      }
-      if (!ok) break;
-      mma_commit(leader, ctl->x_done);
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        ok = ok && wait_warp(ctl->r_full[p], n);
-        if (!ok) break;
+        mma_commit(leader, ctl->gram_done[n & 1]);
+        return true;
+      };
+      // K K^T and Q K^T two chunks ahead, while X is split; Q S while U becomes U'; P U while S is made
+  #pragma unroll 1
+      for (int n = -2; n < chunks; ++n) {
+        const bool here = run.emit && n >= 0;
+        if (here && !wait_warp(ctl->x_done, n)) break;
+        if (n + 2 < chunks && !gram(n + 2)) break;
+        if (!here) continue;
+        if (!wait_warp(ctl->u_done, n)) break;
+        if (n > 0 && !wait_warp(ctl->o_read, n - 1)) break;
         tc_fence_after();
-#pragma unroll
-        for (int ks = p; ks < 4; ks += 2) {
-          mma_ts(leader, tU, tX + 16 * ks, dTW + 2 * ks, i64, ks > 0 || !run.identity);
-          mma_ts(leader, tU, tX + 16 * ks, dTW + (kTileT >> 4) + 2 * ks, i64, 1);
-          mma_ts(leader, tU, tX + 16 * ks + 8, dTW + 2 * ks, i64, 1);
+        const uint64_t d = dKQ + ((n % kKQ) * (kTileKQ >> 4) + (8192 >> 4));
+  #pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          if (ks >= nk) break;
+          const uint64_t b = d + ((ks >> 2) * 1024 + (ks & 3) * 2);
+          mma_ts(leader, tXQ, tS + 16 * ks, b, i64, ks > 0);
+          mma_ts(leader, tXQ, tS + 16 * ks + 8, b, i64, 1);
         }
-      }
-      if (!ok) break;
-      mma_commit(leader, ctl->u_done);
-      mma_commit(leader, ctl->t_free[n & 1]);
-      if (run.emit && !wait_warp(ctl->xq_done, n)) break;  // Q S has read S
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        ok = ok && wait_warp(ctl->up_full[p], n);
-        if (!ok) break;
+        mma_commit(leader, ctl->xq_done);
+        const uint64_t dPn = desc_k(base + F::oP) + n % kP * (F::kTileP >> 4);
+        if (!wait_warp(ctl->d_done, n)) break;  // (U for the read-out came before)
         tc_fence_after();
-#pragma unroll
-        for (int ks = p; ks < 4; ks += 2) {
-          mma_ts(leader, tS, tU + 16 * ks, dKT + 128 * ks, iD, ks > 0);
-          mma_ts(leader, tS, tU + 16 * ks + 8, dKT + 128 * ks, iD, 1);
+  #pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+          mma_ts(leader, tO, tUH + 8 * ks, dPn + 2 * ks, i64, ks > 0);
+          mma_ts(leader, tO, tUH + 32 + 8 * ks, dPn + 2 * ks, i64, 1);
+          if constexpr (kPair) mma_ts(leader, tO, tUH + 8 * ks, dPn + (kTileT >> 4) + 2 * ks, i64, 1);
         }
+        mma_commit(leader, ctl->o_done);
+        mma_commit(leader, ctl->p_free[n % kP]);
       }
-      if (!ok) break;
-      mma_commit(leader, ctl->d_done);
-      mma_commit(leader, kq_free);  // (K K^T, Q K^T and Q S were done before)
+      mma_commit(leader, ctl->drain);
+      if (leader) mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
+    } else if (warp == 2) {
+      // ---- decay tables: tokens 2 lane and 2 lane + 1
+      const bool per_token = a.per_token != 0;
+      const float constant = per_token ? 0.f : a.log_decay[h];
+      float g[2] = {}, b[2] = {};
+  #pragma unroll 1
+      for (int n = -1; n < chunks; ++n) {
+        double G[2];
+        const float beta[2] = {b[0], b[1]};
+  #pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const double x = double(g[e]) * kLog2e;
+          G[e] = x < kMinLog2 ? kMinLog2 : x;  // a NaN stays
+          const int i = (n + 1) * kC + 2 * lane + e;  // the next chunk's
+          g[e] = i < len ? (per_token ? a.log_decay[(run.t0 + i) * a.H + h] : constant) : 0.f;
+          b[e] = i < len ? a.beta[(run.t0 + i) * a.H + h] : 0.f;
+        }
+        if (n < 0) continue;
+        double sum = G[0] + G[1];
+  #pragma unroll 1
+        for (int o = 1; o < 32; o <<= 1) {
+          const double up = __shfl_up_sync(0xffffffffu, sum, o);
+          if (lane >= o) sum += up;
+        }
+        const double end = __shfl_sync(0xffffffffu, sum, 31), middle = __shfl_sync(0xffffffffu, sum, 15);
+        G[0] = sum - G[1], G[1] = sum;
+        Table &w = tab[n % kTabs];
+        if (!wait_warp(ctl->tab_free[n % kTabs], (n / kTabs) ^ 1)) break;
+  #pragma unroll 1
+        for (int e = 0; e < 2; ++e) {
+          const int i = 2 * lane + e;
+          const double x = e == 0 ? G[0] : G[1];
+          const float hi = float(x), f = ex2(hi);
+          w.g[i] = hi, w.g_lo[i] = float(x - double(hi));
+          w.f[i] = -f;
+          w.out[i] = a.scale * f;
+          w.cross[i] = ex2(float(lane < 16 ? middle - x : x - middle));
+          w.w[i] = ex2(float(end - x));
+          w.beta[i] = e == 0 ? beta[0] : beta[1];
+        }
+        if (lane == 0) w.whole = unbiased_decay(float(end * kLn2), n);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->tab_full[n % kTabs]);
+      }
     }
-    // no MMA is in flight when tensor memory is freed
-    mma_commit(leader, ctl->drain);
-    if (leader) mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
-  } else if (warp == 3) {
-    // ---- the other products
-    const bool leader = elect_lane();
-    const uint32_t base = smem_u32(smem);
-    constexpr uint32_t i64 = umma_idesc_bf16(128, 64, false, false, false);
-    const uint64_t dKQ = desc_k(base);
-    auto gram = [&](int n) -> bool {  // rows 0 .. 63: K K^T, 64 .. 127: Q K^T
-      if (!wait_warp(ctl->kq_full[n % kKQ], n / kKQ)) return false;
-      if (partial && n + 1 == chunks && !wait_warp(ctl->zeroed, 0)) return false;
-      if (n > 0 && !wait_warp(ctl->gram_read, n - 1)) return false;
-      tc_fence_after();
-      const uint64_t d = dKQ + (n % kKQ) * (kTileKQ >> 4);
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        if (ks >= nk) break;
-        const uint64_t b = d + ((ks >> 2) * 1024 + (ks & 3) * 2);
-        mma_ss(leader, tG, b, b, i64, ks > 0);
-      }
-      mma_commit(leader, ctl->gram_done[n & 1]);
-      return true;
-    };
-    // K K^T and Q K^T two chunks ahead, while X becomes R; Q S while U becomes U'; P U while S is made
-#pragma unroll 1
-    for (int n = -2; n < chunks; ++n) {
-      const bool here = run.emit && n >= 0;
-      if (here && !wait_warp(ctl->x_done, n)) break;
-      if (n + 2 < chunks && !gram(n + 2)) break;
-      if (!here) continue;
-      if (!wait_warp(ctl->u_done, n)) break;
-      if (n > 0 && !wait_warp(ctl->o_read, n - 1)) break;
-      tc_fence_after();
-      const uint64_t d = dKQ + ((n % kKQ) * (kTileKQ >> 4) + (8192 >> 4));
-#pragma unroll
-      for (int ks = 0; ks < 8; ++ks) {
-        if (ks >= nk) break;
-        const uint64_t b = d + ((ks >> 2) * 1024 + (ks & 3) * 2);
-        mma_ts(leader, tXQ, tS + 16 * ks, b, i64, ks > 0);
-        mma_ts(leader, tXQ, tS + 16 * ks + 8, b, i64, 1);
-      }
-      mma_commit(leader, ctl->xq_done);
-      const uint64_t dPn = desc_k(base + F::oP) + n % kP * (F::kTileP >> 4);
-      if (!wait_warp(ctl->d_done, n)) break;  // (U for the read-out came before)
-      tc_fence_after();
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
-        mma_ts(leader, tO, tUH + 8 * ks, dPn + 2 * ks, i64, ks > 0);
-        mma_ts(leader, tO, tUH + 32 + 8 * ks, dPn + 2 * ks, i64, 1);
-        if constexpr (kPair) mma_ts(leader, tO, tUH + 8 * ks, dPn + (kTileT >> 4) + 2 * ks, i64, 1);
-      }
-      mma_commit(leader, ctl->o_done);
-      mma_commit(leader, ctl->p_free[n % kP]);
-    }
-    mma_commit(leader, ctl->drain);
-    if (leader) mbar_wait(&ctl->drain, 0, err_word, DEVERR_MMA_TIMEOUT);
-  } else if (warp == 2) {
-    // ---- decay tables: tokens 2 lane and 2 lane + 1
-    const bool per_token = a.per_token != 0;
-    const float constant = per_token ? 0.f : a.log_decay[h];
-    float g[2] = {}, b[2] = {};
-#pragma unroll 1
-    for (int n = -1; n < chunks; ++n) {
-      double G[2];
-      const float beta[2] = {b[0], b[1]};
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const double x = double(g[e]) * kLog2e;
-        G[e] = x < kMinLog2 ? kMinLog2 : x;  // a NaN stays
-        const int i = (n + 1) * kC + 2 * lane + e;  // the next chunk's
-        g[e] = i < len ? (per_token ? a.log_decay[(run.t0 + i) * a.H + h] : constant) : 0.f;
-        b[e] = i < len ? a.beta[(run.t0 + i) * a.H + h] : 0.f;
-      }
-      if (n < 0) continue;
-      double sum = G[0] + G[1];
-#pragma unroll 1
-      for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += up;
-      }
-      const double end = __shfl_sync(0xffffffffu, sum, 31), middle = __shfl_sync(0xffffffffu, sum, 15);
-      G[0] = sum - G[1], G[1] = sum;
-      Table &w = tab[n % kTabs];
-      if (!wait_warp(ctl->tab_free[n % kTabs], (n / kTabs) ^ 1)) break;
-#pragma unroll 1
-      for (int e = 0; e < 2; ++e) {
-        const int i = 2 * lane + e;
-        const double x = e == 0 ? G[0] : G[1];
-        const float hi = float(x), f = ex2(hi);
-        w.g[i] = hi, w.g_lo[i] = float(x - double(hi));
-        w.f[i] = -f;
-        w.out[i] = a.scale * f;
-        w.cross[i] = ex2(float(lane < 16 ? middle - x : x - middle));
-        w.w[i] = ex2(float(end - x));
-        w.beta[i] = e == 0 ? beta[0] : beta[1];
-      }
-      if (lane == 0) w.whole = unbiased_decay(float(end * kLn2), n);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->tab_full[n % kTabs]);
-    }
-  }
   } else if (warp < 12) {
     registers_down<72>();
     // ---- A, its inverse and P: warps 4 to 7 of the even chunks, 8 to 11 of the odd ones
@@ -627,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p == 0) sync();
         }
       }
-      // T' = T diag(beta) and -T' diag(e^G) as pairs, 8 columns at a time: 4 pieces of each upper row, 8 of
+      // T' = T diag(beta) and T'' = -T' diag(e^G) as pairs, 8 columns at a time: 4 pieces of each upper row, 8 of
       // each lower one. Their buffers: the products of chunk n - 1 are done.
       ok = n == 0 || wait_warp(ctl->t_free[(n - 1) & 1], (n - 1) >> 1);
       if (clear && !run.identity) {
@@ -705,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     registers_up<120>();
-    // ---- the state: value channel c, key rows 64 half .. + 63; tokens 32 half .. + 31 of R and U'
+    // ---- the state: value channel c, key rows 64 half .. + 63; tokens 32 half .. + 31 of X and U'
     const int w = warp & 3, half = (warp - 16) >> 2, c = 32 * w + lane;
     const uint32_t row = uint32_t(32 * w) << 16;
     const uint32_t rS = tS + row + 64 * half, rX = tX + row + 32 * half, rU = tU + row + 32 * half;
@@ -754,47 +760,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = -1;; ++n) {
       const Table &tb = tab[n & (kTabs - 1)];
       if (n >= 0) {
-      if (n >= chunks) break;
-      if (!wait_warp(ctl->tab_full[n % kTabs], n / kTabs)) break;
-      if (run.emit && n > 0 && !wait_warp(ctl->o_done, n - 1)) break;  // the read-out's U of chunk n - 1 is read
-      // X = K S, split where it stands
-      if (!wait_warp(ctl->x_done, n)) break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int p = 0; p < 2; ++p) {
-        float x[16];
-        tmem_ld16_wait(rX + 16 * p, x);
-        put_pair(rX + 16 * p, x);
-        give(ctl->r_full[p]);
-      }
-      // U, and U' over it
-      if (!wait_warp(ctl->u_done, n)) break;
-      tc_fence_after();
-#pragma unroll 1
-      for (int p = 0; p < 2; ++p) {
-        float x[16];
-        tmem_ld16_wait(rU + 16 * p, x);
-        if (run.emit) {
-          float hi[8], lo[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint32_t h, l;
-            split_pair(x[2 * j], x[2 * j + 1], h, l);
-            hi[j] = __uint_as_float(h), lo[j] = __uint_as_float(l);
+        if (n >= chunks) break;
+        if (!wait_warp(ctl->tab_full[n % kTabs], n / kTabs)) break;
+        if (run.emit && n > 0 && !wait_warp(ctl->o_done, n - 1)) break;  // the read-out's U of chunk n - 1 is read
+        // X = K S, split where it stands
+        if (!wait_warp(ctl->x_done, n)) break;
+        tc_fence_after();
+  #pragma unroll 1
+        for (int p = 0; p < 2; ++p) {
+          float x[16];
+          tmem_ld16_wait(rX + 16 * p, x);
+          put_pair(rX + 16 * p, x);
+          give(ctl->r_full[p]);
+        }
+        // U, and U' over it
+        if (!wait_warp(ctl->u_done, n)) break;
+        tc_fence_after();
+  #pragma unroll 1
+        for (int p = 0; p < 2; ++p) {
+          float x[16];
+          tmem_ld16_wait(rU + 16 * p, x);
+          if (run.emit) {
+            float hi[8], lo[8];
+  #pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t h, l;
+              split_pair(x[2 * j], x[2 * j + 1], h, l);
+              hi[j] = __uint_as_float(h), lo[j] = __uint_as_float(l);
+            }
+            tmem_st8(rUH + 8 * p, hi);
+            tmem_st8(rUH + 32 + 8 * p, lo);
           }
-          tmem_st8(rUH + 8 * p, hi);
-          tmem_st8(rUH + 32 + 8 * p, lo);
+  #pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float2 y = f2_mul(make_float2(x[j], x[j + 1]), *reinterpret_cast<const float2 *>(&tb.w[32 * half + 16 * p + j]));
+            x[j] = y.x, x[j + 1] = y.y;
+          }
+          put_pair(rU + 16 * p, x);
+          give(ctl->up_full[p]);
         }
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float2 y = f2_mul(make_float2(x[j], x[j + 1]), *reinterpret_cast<const float2 *>(&tb.w[32 * half + 16 * p + j]));
-          x[j] = y.x, x[j + 1] = y.y;
-        }
-        put_pair(rU + 16 * p, x);
-        give(ctl->up_full[p]);
-      }
-      if (!wait_warp(ctl->d_done, n)) break;
-      tc_fence_after();
+        if (!wait_warp(ctl->d_done, n)) break;
+        tc_fence_after();
       }
       // S <- e^{G_C} S + K^T U'
       const float2 whole = make_float2(n < 0 ? 0.f : tb.whole, n < 0 ? 0.f : tb.whole);

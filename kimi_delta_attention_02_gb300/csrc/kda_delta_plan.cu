@@ -98,21 +98,26 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// A CTA of the tensor-core kernel holds one (sequence, head) from end to end, one CTA per SM, so few long
-// sequences leave SMs idle. A sequence cut into m segments runs 2 m - 3 of them side by side in pass 1 and
-// m - 1 in pass 3: two segments' time instead of m, for up to three times the work. Of a single sequence
-// m is that of the least time by waves of CTAs (a chunk of 64 tokens takes some 4 us, a step of pass 2 five,
-// a pass ten to begin and end; T = 65536, 16 heads: m = 10); of several the lengths are not known here, and cuts lie so far apart that
-// pass 1 fills the SMs at most twice. Sequences in more chains than SMs run longest first.
-DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool in_bf16, bool out_bf16, bool recurrent,
+// The tensor-core kernel needs head sizes whose rows TMA can address (16 bytes) and takes a chunk of 64
+// tokens' time for the shortest sequence, so calls of short ones go to the token kernel: below `least` tokens a
+// sequence on average (16 sequences, 64 heads of 128, us by the token kernel / this one: 4 tokens 93 / 97,
+// 8 107 / 97, 24 176 / 98; 128 sequences: 4 767 / 667, 16 1021 / 671; 64 heads of 64, where a warp holds
+// a whole state: 8 tokens 38 / 87, 32 68 / 88; between the two where one size is above 64).
+//
+// A CTA holds one (sequence, head) from end to end, one CTA per SM, so few long sequences leave SMs idle. A
+// sequence cut into m segments runs 2 m - 3 of them side by side in pass 1 and m - 1 in pass 3: two segments'
+// time instead of m, for up to three times the work. Of a single sequence m is that of the least time by
+// waves of CTAs: a chunk of 64 tokens takes some 4 us, a step of pass 2 five, a pass ten to begin and end (T =
+// 65536, 16 heads: m = 10, 1335 us; m = 6: 1378 us; not cut: some 3100). Of several the lengths are not known
+// here, and cuts lie so far apart that pass 1 fills the SMs at most twice. Sequences in more chains than SMs run
+// longest first.
+DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool in_bf16, bool recurrent,
                      size_t workspace_bytes) {
   DeltaPlan p;
-  // TMA addresses rows of a multiple of 16 bytes
   const int64_t least = d_k <= 64 && d_v <= 64 ? 44 : d_k <= 64 || d_v <= 64 ? 16 : 6;
   p.tensor = in_bf16 && !recurrent && d_k % 8 == 0 && d_v % 8 == 0 && total >= least * num_seqs &&
              int64_t(H) * d_v <= 1 << 25;  // (its output addresses)
   if (!p.tensor) return p;
-  (void)out_bf16;
   int64_t len = 0;
   if (num_seqs == 1) {
     const auto waves = [&](int64_t pieces) { return (pieces * H + kLinearSMs - 1) / kLinearSMs; };

@@ -62,6 +62,26 @@ def test_decays(decay, out_dtype):
 
 
 @pytest.mark.parametrize("out_dtype", [B16, F32])
+@pytest.mark.parametrize("lens,first,g", [([64], 3, 0.6), ([150], 5, 0.3)])
+def test_growth(lens, first, g, out_dtype):
+    """Positive log-decays while no run of tokens sums above 40: entries of the inverse reach e^36. With
+    G_t the sums from the start, e^{-G_t} S_t follows the recurrence without a decay and with e^{-G_t} v_t,
+    and every rounding is relative to its entry, so the bound is that of this one times e^{G_t}. (An
+    entry's decay is off by 2^-19 of it more, a sum of up to 58 in units of ln 2 held in fp32; the bound counts
+    each pair, at most 2^-17 off, as 2^-16.)"""
+    c = make(lens, decay=0.0, seed=9)
+    c["log_decay"][first:first + int(36 / g)] = g
+    out, fin = run(c, out_dtype=out_dtype)
+    o, f = reference(c)
+    G = torch.cumsum(c["log_decay"].double(), 0)[:, :, None]
+    still = {**c, "v": c["v"].double() * torch.exp(-G), "log_decay": torch.zeros_like(c["log_decay"])}
+    bo, bf, _ = bounds(still, pairs=True, read=2.0 ** -8 * 2 if out_dtype == B16 else 0.0)
+    grown = f64(torch.exp(G))
+    check(out, o, bo * grown + half_step(o, out_dtype), "out")
+    check(fin, f, bf * grown[-1][None, :, None], "final")
+
+
+@pytest.mark.parametrize("out_dtype", [B16, F32])
 def test_keys_alike(out_dtype):
     """Keys with a common direction, and one key over and over: the inverse of I + A is then far from
     I - A, and powers of A would grow like binomials."""
