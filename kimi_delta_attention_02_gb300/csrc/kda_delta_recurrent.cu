@@ -15,6 +15,11 @@
 // kNC of them and the key rows 4 kLanes j + 4 rl + 0..3, two rows to a packed fp32 instruction. Four warps do
 // this. Four others go ahead of them: they bring q, k, v to shared memory 16 tokens at a time (the next 16
 // waiting in registers) and form the products k.k and q.k and the decays of the next 16 tokens' blocks.
+//
+// What bounds it: the latency of a block of four tokens where chains are few (0.13 us a token: 700 and 333
+// tokens, 6 heads of 100 x 72, fp32: 97 us, 137 without warps that go ahead), issue where they are many
+// (4096 tokens, 96 heads of 128: 1.98 ms, 2.41 without; the 21 G multiply-adds are a quarter of the fp32
+// rate, beside the reads of k and q from shared memory and the exchange of the sums).
 #include <atomic>
 #include <type_traits>
 
@@ -323,14 +328,17 @@ cudaError_t launch_one(const DeltaArgs &a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream) {
-  // Few chains take a warp per column, so that a block's way is shorter; many take 16 columns per CTA, or 32 while
-  // that leaves two CTAs for every SM.
+  // A warp per column while that leaves at most two CTAs for an SM: a block's way is shorter, but 16 columns per
+  // CTA are less work. Two columns per thread once 16 per CTA are more CTAs than SMs: a CTA's block takes half
+  // as long again, and one SM's two CTAs twice as long. 1000 tokens in fp32, us by 4 / 16 / 32 columns per
+  // CTA: 8 heads of 128 134 / 144 / 205, 16 heads 261 / 146 / 205, 28 heads 388 / 231 / 205, 48 heads 756 / 455 / 315,
+  // 96 heads 1432 / 682 / 497; 48 heads of 64 383 / 152 / 122.
   const int64_t chains = int64_t(a.num_seqs) * a.H;
   const auto ctas = [&](int cols) { return chains * ((a.d_v + cols - 1) / cols); };
   const auto run = [&](auto in, auto out) {
     constexpr bool ib = decltype(in)::value, ob = decltype(out)::value;
-    if (ctas(4) <= 6 * kLinearSMs) return launch_one<ib, ob, 32, 4, 1>(a, stream);
-    const bool wide = a.d_k > 64, two = ctas(32) >= 2 * kLinearSMs;
+    if (ctas(4) <= 2 * kLinearSMs) return launch_one<ib, ob, 32, 4, 1>(a, stream);
+    const bool wide = a.d_k > 64, two = ctas(16) > kLinearSMs;
     if (wide) return two ? launch_one<ib, ob, 8, 16, 2>(a, stream) : launch_one<ib, ob, 8, 16, 1>(a, stream);
     return two ? launch_one<ib, ob, 8, 8, 2>(a, stream) : launch_one<ib, ob, 8, 8, 1>(a, stream);
   };

@@ -2,8 +2,9 @@
 // y = r (a (*) x + b (*) x_partner) per head row, with r = 1 / sqrt(mean(x^2) + eps) (or of the sum, or
 // one), a = w cos p and b = -+ w_partner sin p of the token's angles, which all heads share.
 //
-// Reads and writes q and k once at about 7 flops per element: bound by HBM bandwidth. The angles of a
-// token are formed once per CTA, in shared memory. A head row takes as many lanes as it has pieces of 8
+// Reads and writes q and k once at about 7 flops per element: bound by HBM bandwidth (4096 tokens, 192 heads
+// of 128, bf16: 403 MB in 79 us, 5.1 TB/s; the copy rate would be 60 us), by latency for a few tokens (one token:
+// 6 us). The angles of a token are formed once per CTA, in shared memory. A head row takes as many lanes as it has pieces of 8
 // channels (the next power of two), so that a warp works on up to 32 rows at once, and a lane keeps the
 // angles of its channels in registers while it goes through the token's heads, two at a time. A turned
 // channel's partner is in the same lane (neighbours) or comes by a second load, which finds its line in L1.
@@ -64,34 +65,16 @@ struct Piece {
     }
   }
 };
-// kN neighbouring elements at an address aligned to them
-template <bool kBF16, int kN>
-__device__ __forceinline__ void load_part(const void *base, int64_t at, float *x) {
-  if constexpr (kBF16 && kN == 8) {
-    Piece<true> p;
-    p.w[0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
-    float y[8];
-    p.get(y);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = y[e];
-  } else if constexpr (!kBF16 && kN == 8) {
-    load_part<false, 4>(base, at, x);
-    load_part<false, 4>(base, at + 4, x + 4);
-  } else if constexpr (kBF16 && kN == 4) {
+// four neighbouring elements
+template <bool kBF16>
+__device__ __forceinline__ void load4(const void *base, int64_t at, float *x) {
+  if constexpr (kBF16) {
     const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(base) + at);
     const float2 a = unpack_bf16x2(w.x), b = unpack_bf16x2(w.y);
     x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
-  } else if constexpr (!kBF16 && kN == 4) {
+  } else {
     const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
     x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
-  } else if constexpr (kBF16 && kN == 2) {
-    const float2 a = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + at));
-    x[0] = a.x, x[1] = a.y;
-  } else if constexpr (!kBF16 && kN == 2) {
-    const float2 w = *reinterpret_cast<const float2 *>(static_cast<const float *>(base) + at);
-    x[0] = w.x, x[1] = w.y;
-  } else {
-    x[0] = load_elem<kBF16>(base, at);
   }
 }
 
@@ -208,7 +191,7 @@ __global__ void __launch_bounds__(kThr, 3) rotate_kernel(const RotateArgs a, int
 #pragma unroll
             for (int e = 0; e < 8; e += 4) {
               if (ok && turns)
-                load_part<kInBF16, 4>(row + u * row_in, c0 + e < a.half ? c0 + e + a.half : c0 + e - a.half, &xp[e]);
+                load4<kInBF16>(row + u * row_in, c0 + e < a.half ? c0 + e + a.half : c0 + e - a.half, &xp[e]);
             }
           }
           __syncwarp();  // in place: every lane of the row has read it
@@ -237,46 +220,54 @@ __global__ void __launch_bounds__(kThr, 3) rotate_kernel(const RotateArgs a, int
   }
 }
 
-// One channel per lane and step: rows that start anywhere, head sizes that are no multiple of 8.
-template <bool kInBF16, bool kOutBF16, bool kNeighbours>
-__global__ void __launch_bounds__(kThr) rotate_any_kernel(const RotateArgs a) {
-  constexpr int kPer = kRotateMaxD / 32;
-  __shared__ uint64_t s_turn[kRotateMaxD / 2];
-  __shared__ float2 s_cs[kRotateMaxD / 2];
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  for (int i = tid; i < a.half; i += kThr) s_turn[i] = turns_per_position(a.inv_freq[i]);
-  for (int64_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
-    __syncthreads();
-    for (int i = tid; i < a.half; i += kThr) s_cs[i] = angle(a, i, t, s_turn[i]);
-    __syncthreads();
+// Rows that start anywhere, head sizes that are no multiple of 8: a warp per row, a pair of channels per lane
+// and step (kPer of them: the pairs that turn, then neighbours of those that do not), element by element. A
+// warp keeps a token's factors in registers while it goes through its share of the token's heads (blockIdx.y).
+// Bound by its 2-byte accesses: the sizes above take 189 us here, and 10007 tokens of 20 heads of 72 take 45 us
+// (31 us by whole pieces), so rows that allow it go there.
+template <bool kInBF16, bool kOutBF16, int kPer>
+__global__ void __launch_bounds__(kThr) rotate_any_kernel(const RotateArgs a, int interleaved) {
+  const int lane = threadIdx.x & 31;
+  uint64_t turns[kPer];
+  int ch[kPer], ph[kPer];  // the pair's channels, or the row's end
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int p = lane + 32 * j;
+    const bool turned = p < a.half;
+    turns[j] = turned ? turns_per_position(a.inv_freq[p]) : 0;
+    ch[j] = turned && interleaved == 0 ? p : 2 * p;
+    ph[j] = turned && interleaved == 0 ? p + a.half : 2 * p + 1;
+    if (ch[j] > a.d) ch[j] = a.d;
+    if (ph[j] > a.d) ph[j] = a.d;
+  }
+#pragma unroll 1
+  for (int64_t t = blockIdx.x * int64_t(kThr / 32) + (threadIdx.x >> 5); t < a.tokens; t += gridDim.x * int64_t(kThr / 32)) {
+    float2 cs[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int p = lane + 32 * j;
+      cs[j] = p < a.half ? angle(a, p, t, turns[j]) : make_float2(1.f, 0.f);
+    }
 #pragma unroll 1
     for (int which = 0; which < 2; ++which) {
-      const int64_t from = t * a.stride[which], to = t * a.out_stride[which];
-      float ca[kPer], cb[kPer];
-      int partner[kPer];
+      const float *weight = a.weight[which];
+      float w[kPer], wp[kPer];
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        const int c = lane + 32 * j;
-        const bool turned = c < 2 * a.half;
-        const bool first = kNeighbours ? (c & 1) == 0 : c < a.half;
-        partner[j] = !turned ? c : kNeighbours ? c ^ 1 : first ? c + a.half : c - a.half;
-        const float2 cs = turned ? s_cs[kNeighbours ? c >> 1 : first ? c : c - a.half] : make_float2(1.f, 0.f);
-        const float *weight = a.weight[which];
-        const bool on = c < a.d;
-        ca[j] = (weight != nullptr && on ? weight[c] : 1.f) * cs.x;
-        cb[j] = (weight != nullptr && on ? weight[partner[j]] : 1.f) * (first ? -cs.y : cs.y);
+        w[j] = weight != nullptr && ch[j] < a.d ? weight[ch[j]] : 1.f;
+        wp[j] = weight != nullptr && ph[j] < a.d ? weight[ph[j]] : 1.f;
       }
 #pragma unroll 1
-      for (int h = w; h < a.heads[which]; h += kThr / 32) {
-        const int64_t row = from + int64_t(h) * a.d;
+      for (int h = blockIdx.y; h < a.heads[which]; h += gridDim.y) {
+        const int64_t from = t * a.stride[which] + int64_t(h) * a.d, to = t * a.out_stride[which] + int64_t(h) * a.d;
         float x[kPer], xp[kPer], sum = 0.f;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-          const int c = lane + 32 * j;
-          x[j] = c < a.d ? load_elem<kInBF16>(a.x[which], row + c) : 0.f;
-          xp[j] = c < 2 * a.half ? load_elem<kInBF16>(a.x[which], row + partner[j]) : 0.f;
-          sum = fmaf(x[j], x[j], sum);
+          x[j] = ch[j] < a.d ? load_elem<kInBF16>(a.x[which], from + ch[j]) : 0.f;
+          xp[j] = ph[j] < a.d ? load_elem<kInBF16>(a.x[which], from + ph[j]) : 0.f;
         }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) sum = fmaf(x[j], x[j], fmaf(xp[j], xp[j], sum));
         if (a.norm != KDA_NORM_NONE) {
 #pragma unroll
           for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
@@ -285,9 +276,12 @@ __global__ void __launch_bounds__(kThr) rotate_any_kernel(const RotateArgs a) {
         __syncwarp();  // in place: every lane has read the row
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-          const int c = lane + 32 * j;
-          const float y = c < 2 * a.half ? fmaf(xp[j], cb[j], x[j] * ca[j]) : x[j] * ca[j];
-          if (c < a.d) store_elem<kOutBF16>(a.out[which], to + int64_t(h) * a.d + c, r * y);
+          const bool turned = lane + 32 * j < a.half;
+          const float n = w[j] * x[j], np = wp[j] * xp[j];
+          // (left as they are, not multiplied by zero, where nothing turns: the neighbour may be infinite)
+          const float y = turned ? fmaf(n, cs[j].x, -np * cs[j].y) : n, yp = turned ? fmaf(np, cs[j].x, n * cs[j].y) : np;
+          if (ch[j] < a.d) store_elem<kOutBF16>(a.out[which], to + ch[j], r * y);
+          if (ph[j] < a.d) store_elem<kOutBF16>(a.out[which], to + ph[j], r * yp);
         }
       }
     }
@@ -312,23 +306,26 @@ cudaError_t launch_norm_rotate(const RotateArgs &a, bool in_bf16, bool out_bf16,
     while (pairs < a.half) pairs *= 2;
     const int rows = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1], slots = kThr / lanes;
     const int64_t fit = 152 * 3;
-    // a lane's factors serve some six rows of a token, unless there are too few tokens for that
-    const int64_t per = a.tokens * rows / (fit * slots);
-    while (group < slots && group * (per < 1 ? 1 : per < 6 ? per : 6) < rows) group *= 2;
+    // A lane's factors serve up to twelve rows of a token (us at 1 / 3 / 6 / 12 / 24 rows: 4096 tokens, 192 heads of 128
+    // 82 / 82 / 82 / 79 / 83; 80 heads 59 / 59 / 43 / 40 / 45; 10007 tokens, 20 heads of 72 94 / 39 / 33 / 31 / 31).
+    while (group < slots && group * 12 < rows) group *= 2;
     const int64_t passes = (a.tokens + slots / group - 1) / (slots / group);
-    // few tokens: their heads over several CTAs
+    // Few tokens: their heads over several CTAs.
     const int64_t most = (rows + group - 1) / group, spare = fit / passes;
     const unsigned parts = unsigned(spare < 1 ? 1 : spare < most ? spare : most);
     kernels[2 * int(in_bf16) + int(out_bf16)][interleaved ? 0 : a.half % 8 == 0 ? 2 : 1]<<<
         dim3(unsigned(passes < fit ? passes : fit), parts), kThr, 0, stream>>>(a, lanes, group, pairs);
     return cudaGetLastError();
   }
-  using Kern = void (*)(const RotateArgs);
-#define KDA_ROT(ib, ob) {rotate_any_kernel<ib, ob, false>, rotate_any_kernel<ib, ob, true>}
-  static const Kern any[4][2] = {KDA_ROT(false, false), KDA_ROT(false, true), KDA_ROT(true, false), KDA_ROT(true, true)};
+  using Kern = void (*)(const RotateArgs, int);
+#define KDA_ROT(ib, ob) {rotate_any_kernel<ib, ob, 1>, rotate_any_kernel<ib, ob, 2>, rotate_any_kernel<ib, ob, 4>}
+  static const Kern any[4][3] = {KDA_ROT(false, false), KDA_ROT(false, true), KDA_ROT(true, false), KDA_ROT(true, true)};
 #undef KDA_ROT
-  const int64_t fit = 152 * 8;
-  any[2 * int(in_bf16) + int(out_bf16)][int(interleaved)]<<<unsigned(a.tokens < fit ? a.tokens : fit), kThr, 0, stream>>>(a);
+  const int64_t fit = 152 * 6, passes = (a.tokens + kThr / 32 - 1) / (kThr / 32);
+  const int64_t rows = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1], spare = fit / passes;
+  const unsigned parts = unsigned(spare < 1 ? 1 : spare < rows ? spare : rows);
+  any[2 * int(in_bf16) + int(out_bf16)][a.d <= 64 ? 0 : a.d <= 128 ? 1 : 2]<<<
+      dim3(unsigned(passes < fit ? passes : fit), parts), kThr, 0, stream>>>(a, int(interleaved));
   return cudaGetLastError();
 }
 
