@@ -507,14 +507,29 @@ kda_status kda_block_norm(const kda_block_norm_params *params, void *stream);
  *     S_t = (I - beta_t k_t k_t^T) e^{g_t} S_{t-1} + beta_t k_t v_t^T ,    o_t = scale * S_t^T q_t
  *
  * kda_delta_prefill runs packed variable-length sequences, kda_delta_decode one token for B
- * sequences. Layouts, alignment, aliasing, log_decay, the workspace and error rules are those of
- * kda_linear_prefill and kda_linear_decode; what is added:
+ * sequences. Layouts, alignment, aliasing, log_decay, sizes and error rules are those of
+ * kda_linear_prefill and kda_linear_decode; what is added or differs:
  *
  *   beta         [total_tokens, H] (decode: [B, H]) fp32, any finite value. With beta |k|^2 in
  *                [0, 2] the state's norm only shrinks between writes; outside, the recurrence itself
  *                grows from token to token, and so do the rounding errors of every kernel.
+ *   workspace    (prefill) of kda_delta_prefill_workspace_size() bytes. With it, long sequences of
+ *                calls that would leave SMs idle are cut into segments that run side by side, and
+ *                sequences of unlike lengths start longest first; with less, every (sequence, head)
+ *                runs from end to end in the order given. It may not be shared by calls that run at
+ *                the same time (two captured graphs that may replay together need one each).
  *
- * Sizes: as kda_linear_prefill. Results are accumulated in fp32 and states are fp32.
+ * bf16 prompts with d_k and d_v multiples of 8 run a tensor-core kernel in chunks of 64 tokens,
+ * unless their sequences are short (fewer than 6 tokens on average, 16 where one of d_k and d_v is at most
+ * 64, 44 where both are; empty sequences count) or H d_v is above 2^25. Its products read the state and
+ * what is formed for it as pairs of bf16 (2^-17), so that final states and fp32 outputs are off by
+ * some 1e-5 of themselves (in the 2-norm); the masked products q.k are single bf16 when the output is bf16. A log_decay
+ * below -88 counts as -88. An infinity or NaN in a channel of v reaches that value channel of every
+ * output of its chunk in that (sequence, head), and what follows; one in k, beta or log_decay every
+ * channel of the same; one in q its own token's output. fp32 inputs, short sequences and other head
+ * sizes run the fp32 token-recurrent kernel, where they reach only what depends on them.
+ *
+ * Results are accumulated in fp32 and states are fp32.
  */
 typedef struct kda_delta_prefill_params {
   uint32_t struct_size;       /* sizeof the struct; any other value is KDA_ERR_INVALID_ARG   */
@@ -591,8 +606,11 @@ size_t kda_delta_prefill_workspace_size(int64_t total_tokens, int32_t num_seqs, 
  * excepted) and not each other; rows of a fused buffer that interleave without sharing an element do
  * not overlap. Element alignment is enough for q, k and the outputs (2 or 4 bytes); rows that start
  * on 16-byte boundaries with d a multiple of 8 are faster. Sizes: tokens >= 0, 1 <= d <= 256,
- * rot_dim even and <= d, 1 <= num_axes <= 4, H_q >= 1. eps finite and >= 0; a row of zeros with
- * eps = 0 gives NaN, as the formula does. Squares are summed in fp32.
+ * rot_dim even and <= d, 1 <= num_axes <= 4, 1 <= H_q <= 65535, H_k <= 65535. eps finite and >= 0; a row
+ * of zeros with eps = 0 gives NaN, as the formula does. Squares are summed in fp32, so rows that are
+ * normalised hold values below 1e17 (beyond, the sum may overflow and the row becomes 0), and with eps =
+ * 0 some above 1e-18. An angle is exact to 2^-32 of a turn while |inv_freq| is below 2^24; the result is
+ * rounded once. An infinite or NaN inv_freq gives NaN for its pair.
  */
 typedef enum { KDA_NORM_NONE = 0, KDA_NORM_RMS = 1, KDA_NORM_L2 = 2 } kda_norm_form;
 

@@ -868,7 +868,7 @@ def norm_rotate(q, k, positions, inv_freq, *, norm="rms", q_weight=None, k_weigh
             raise ValueError("pair_axis must name an axis for each pair of inv_freq")
         if half and not 0 <= min(pair_axis) <= max(pair_axis) < min(axes, 256):
             raise ValueError("pair_axis names an axis that positions does not have")
-        axis_of = _PairAxis.from_buffer_copy(bytes(pair_axis).ljust(128, b"\0"))
+        axis_of = _PairAxis.from_buffer_copy(bytes(list(pair_axis)).ljust(128, b"\0"))
     device = _one_device(positions, inv_freq, q_weight, k_weight)
     for t in (q, k, q_out, k_out):
         if t is not None:

@@ -672,7 +672,8 @@ kda_status kda_norm_rotate(const kda_norm_rotate_params *p, void *stream) {
   if (p->tokens < 0 || p->H_q < 1 || p->H_k < 0 || p->d < 1) return KDA_ERR_INVALID_ARG;
   if (p->rot_dim < 0 || p->rot_dim > p->d || p->rot_dim % 2 != 0) return KDA_ERR_INVALID_ARG;
   if ((p->interleaved != 0 && p->interleaved != 1) || !finite_nonneg(p->eps)) return KDA_ERR_INVALID_ARG;
-  if (p->d > kRotateMaxD || p->num_axes > kRotateMaxAxes || p->tokens > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+  if (p->d > kRotateMaxD || p->num_axes > kRotateMaxAxes || p->tokens > INT32_MAX || p->H_q > 65535 || p->H_k > 65535)
+    return KDA_ERR_UNSUPPORTED;
   const int half = p->rot_dim / 2;
   if (half > 0) {
     if (p->num_axes < 1 || (p->position_bytes != 4 && p->position_bytes != 8)) return KDA_ERR_INVALID_ARG;

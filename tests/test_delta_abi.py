@@ -105,6 +105,37 @@ def test_norm_rotate_rejects(over, expect):
     assert _rotate(**over) == expect
 
 
+def test_norm_rotate_head_counts():
+    wide = dict(q_stride=65536 * 64, k_stride=65536 * 64, q_out_stride=65536 * 64, k_out_stride=65536 * 64, d=1, rot_dim=0)
+    assert _rotate(**{**wide, "H_q": 65536}) == UNS and _rotate(**{**wide, "H_k": 65536}) == UNS
+    assert _rotate(**{**wide, "H_q": 65535, "H_k": 65535, "tokens": 0}) == 0
+
+
+def test_workspace_sizes():
+    size = B.delta_workspace_size
+    f32, bf16 = torch.float32, torch.bfloat16
+    for T in (1, 63, 5000, 100000):  # the token kernel
+        assert size(T, 1, 8, dtype=f32) == size(T, 1, 8, recurrent=True) == size(T, 1, 8, d_k=68) == size(T, 1, 8, d_v=4) == 0
+    assert size(0, 0, 8) == size(0, 3, 8) == size(100, 1, 0) == size(-1, 1, 8) == size(100, 1, 8, H_k=3) == 0
+    # one long sequence that leaves SMs idle is cut: an end state and a map for each segment
+    n = size(65536, 1, 16)
+    assert n > 0 and n % (16 * 128 * 128 * 8) == 0
+    assert size(65536, 1, 16, d_v=64) == n * 3 // 4
+    assert size(65536, 1, 152) == 0 and size(600, 1, 4) == 0
+    # more chains than SMs, of lengths that are not known: an order
+    assert size(40 * 200, 40, 32) == 256 and size(40 * 60, 40, 3) == 0
+    # .. or segments, where the tokens would make long ones and SMs are idle
+    assert size(40 * 200, 40, 3) % (3 * 128 * 128 * 8) == 0
+    assert size(9000 * 10, 9000, 32) == 0
+    # short sequences go to the token kernel, by head sizes
+    assert size(40 * 5, 40, 32) == size(40 * 15, 40, 32, d_k=64) == size(40 * 43, 40, 32, d_k=64, d_v=64) == 0
+    assert size(40 * 6, 40, 32) == size(40 * 16, 40, 32, d_k=64) == size(40 * 44, 40, 32, d_k=64, d_v=64) == 256
+    for T in (2**31 - 128, 2**30):  # the largest
+        for N, H in ((1, 1), (1, 64), (7, 3), (1000, 64)):
+            assert size(T, N, H) < 1 << 33
+            assert size(T, N, H) == size(T, N, H)
+
+
 def test_binding_refuses():
     c = make([5, 2], H=4, H_k=2, d_k=16, d_v=8, device="cpu")
     with pytest.raises(ValueError, match="contiguous CUDA tensors"):
