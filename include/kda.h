@@ -515,19 +515,21 @@ kda_status kda_block_norm(const kda_block_norm_params *params, void *stream);
  *                grows from token to token, and so do the rounding errors of every kernel.
  *   workspace    (prefill) of kda_delta_prefill_workspace_size() bytes. With it, long sequences of
  *                calls that would leave SMs idle are cut into segments that run side by side, and
- *                sequences of unlike lengths start longest first; with less, every (sequence, head)
- *                runs from end to end in the order given. It may not be shared by calls that run at
+ *                sequences of unlike lengths start longest first, and bf16 head sizes that are no
+ *                multiple of 8 are padded for the tensor-core kernel; with less, every (sequence,
+ *                head) runs from end to end in the order given, and such head sizes run the
+ *                token-recurrent kernel. It may not be shared by calls that run at
  *                the same time (two captured graphs that may replay together need one each).
  *
- * bf16 prompts with d_k and d_v multiples of 8 run a tensor-core kernel in chunks of 64 tokens,
- * unless their sequences are short (fewer than 6 tokens on average, 16 where one of d_k and d_v is at most
- * 64, 44 where both are; empty sequences count) or H d_v is above 2^25. Its products read the state and
+ * bf16 prompts run a tensor-core kernel in chunks of 64 tokens, unless their sequences are short
+ * (fewer than 6 to 88 tokens on average, by head sizes and the number of sequences and heads; empty
+ * sequences count) or H d_v is above 2^25. Its products read the state and
  * what is formed for it as pairs of bf16 (2^-17), so that final states and fp32 outputs are off by
  * some 1e-5 of themselves (in the 2-norm); the masked products q.k are single bf16 when the output is bf16. A log_decay
  * below -88 counts as -88. An infinity or NaN in a channel of v reaches that value channel of every
  * output of its chunk in that (sequence, head), and what follows; one in k, beta or log_decay every
- * channel of the same; one in q its own token's output. fp32 inputs, short sequences and other head
- * sizes run the fp32 token-recurrent kernel, where they reach only what depends on them.
+ * channel of the same; one in q its own token's output. fp32 inputs and short sequences run
+ * the fp32 token-recurrent kernel, where they reach only what depends on them.
  *
  * Results are accumulated in fp32 and states are fp32.
  */

@@ -17,10 +17,12 @@ namespace kda {
 struct DeltaPlan {
   bool tensor = false;   // tensor-core kernel, else the token kernel
   bool order = false;    // longest sequences first, by a list in the workspace
+  bool pad = false;      // q, k, v by copies whose head sizes are padded to multiples of 8
   int32_t seg_len = 0;   // tokens between cuts (0: none)
   int32_t inner = 0;     // total / seg_len
-  size_t ends = 0;       // in the workspace: [inner, H, d_k, d_v] fp32, the states that segments leave,
-  size_t maps = 0;       // [inner, H, d_k, d_k] fp32, their M; or the list
+  size_t pad_q = 0, pad_k = 0, pad_v = 0;  // in the workspace: the copies;
+  size_t ends = 0;       // [inner, H, d_k, d_v] fp32 (padded sizes), the states that segments leave, or the list,
+  size_t maps = 0;       // [inner, H, d_k, d_k] fp32 (padded sizes), their M
   size_t bytes = 0;      // of the workspace that the plan uses
 };
 
@@ -46,8 +48,10 @@ __device__ __forceinline__ int64_t delta_place(const DeltaArgs &a, const LinearS
   return a.plan.seg_len == 0 ? 0 : bos / a.plan.seg_len + (s.t0 - bos) / a.plan.seg_len;
 }
 
+__host__ __device__ constexpr int delta_up8(int d) { return (d + 7) & ~7; }
+
 // The plan for a call that has this much workspace (SIZE_MAX: what it would like to have).
-DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool in_bf16, bool recurrent,
+DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool recurrent,
                      size_t workspace_bytes);
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream);
 cudaError_t launch_delta_chunked(const DeltaArgs &a, bool out_bf16, cudaStream_t stream);

@@ -1,5 +1,5 @@
 // kda_delta_chunked.cu -- the gated delta rule with one decay per head on the tensor cores (bf16
-// inputs, head sizes in multiples of 8), in chunks of 64 tokens.
+// inputs; head sizes that are no multiple of 8 by padded copies), in chunks of 64 tokens.
 //
 // With G the cumulative log-decay inside a chunk, D_ti = e^{G_t - G_i}, and S the state that enters it,
 //     A_ti = beta_t D_ti (k_t . k_i), i < t;      T' = (I + A)^-1 diag(beta),   T'' = -T' diag(e^G)
@@ -95,7 +95,7 @@ struct Run {
   bool identity;       // from the identity, with v = 0
   const float *from;   // entering state, or null: zero
   float *to;           // or null
-  int width;           // columns of `from` and `to`: d_v, or d_k of a map
+  int from_width, width;  // columns of `from` and `to`: d_v, or padded to a multiple of 8 in the workspace
 };
 
 // Probes (a failing one takes about 1 us) until the phase of this parity is complete; false, and `gave_up`
@@ -197,24 +197,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     int index = blockIdx.x / a.H;
     const bool map = index >= a.plan.inner + a.num_seqs;  // pass 1: the pieces once more, for their M
     if (map) index -= a.plan.inner + a.num_seqs;
-    if (a.plan.order) index = reinterpret_cast<const int32_t *>(a.workspace)[index];
+    if (a.plan.order) index = reinterpret_cast<const int32_t *>(a.workspace + a.plan.ends)[index];
     LinearSlot s;
     if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, index, s)) return;
     if ((pass == 3 || map) ? s.first : s.last && !s.first) return;
-    const int64_t dd = int64_t(a.d_k) * a.d_v;
+    const int pk = delta_up8(a.d_k), pv = delta_up8(a.d_v);
+    const int64_t dd = int64_t(a.d_k) * a.d_v, ee = int64_t(pk) * pv;
     float *ends = reinterpret_cast<float *>(a.workspace + a.plan.ends);
     const int64_t place = delta_place(a, s);
     run.t0 = s.t0, run.len = int(s.t1 - s.t0), run.chunks = (run.len + kC - 1) / kC;
     run.emit = s.first || pass == 3;
     run.identity = map;
-    run.width = a.d_v;
-    run.from = !s.first ? (pass == 3 ? ends + ((place - 1) * a.H + h) * dd : nullptr)
+    run.from_width = s.first ? a.d_v : pv;
+    run.width = pv;
+    run.from = !s.first ? (pass == 3 ? ends + ((place - 1) * a.H + h) * ee : nullptr)
                : a.init_state != nullptr ? a.init_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
-    if (run.emit && s.last) run.to = a.final_state != nullptr ? a.final_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
-    else run.to = pass == 3 ? nullptr : ends + (place * a.H + h) * dd;
+    if (run.emit && s.last) {
+      run.width = a.d_v;
+      run.to = a.final_state != nullptr ? a.final_state + (int64_t(s.n) * a.H + h) * dd : nullptr;
+    } else {
+      run.to = pass == 3 ? nullptr : ends + (place * a.H + h) * ee;
+    }
     if (map) {
-      run.width = a.d_k;
-      run.to = reinterpret_cast<float *>(a.workspace + a.plan.maps) + (place * a.H + h) * int64_t(a.d_k) * a.d_k;
+      run.width = pk;
+      run.to = reinterpret_cast<float *>(a.workspace + a.plan.maps) + (place * a.H + h) * int64_t(pk) * pk;
     }
   }
   const int chunks = run.chunks, len = run.len;
@@ -724,12 +730,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 64; i += 16) {
         float x[16];
         const int r0 = 64 * half + i;
-        const float *from = run.from + int64_t(r0) * a.d_v + c;
+        const float *from = run.from + int64_t(r0) * run.from_width + c;
         const int rows = run.from != nullptr && c < a.d_v ? a.d_k - r0 : 0;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
           x[j] = run.identity && r0 + j == c ? 1.f : 0.f;
-          if (j < rows) x[j] = from[uint32_t(j) * uint32_t(a.d_v)];
+          if (j < rows) x[j] = from[uint32_t(j) * uint32_t(run.from_width)];
         }
         tmem_st16(rS + i, x);
       }
@@ -878,16 +884,26 @@ cudaError_t launch_pass(const CUtensorMap &mq, const CUtensorMap &mk, const CUte
 cudaError_t launch_order_longest_first(const int32_t *cu_seqlens, int num_seqs, int32_t *order, cudaStream_t stream);
 
 cudaError_t launch_delta_chunked(const DeltaArgs &a, bool out_bf16, cudaStream_t stream) {
+  LinearArgs in{};  // q, k, v or their padded copies
+  in.q = a.q, in.k = a.k, in.v = a.v;
+  cudaError_t e = cudaSuccess;
+  if (a.plan.pad) {
+    in.workspace = a.workspace, in.total = a.total;
+    in.H = a.H, in.H_k = a.H_k, in.d_k = a.d_k, in.d_v = a.d_v;
+    in.plan.pad_q = a.plan.pad_q, in.plan.pad_k = a.plan.pad_k, in.plan.pad_v = a.plan.pad_v;
+    e = launch_linear_pad(in, stream);
+    if (e != cudaSuccess) return e;
+  }
+  const int pk = delta_up8(a.d_k), pv = delta_up8(a.d_v);
   CUtensorMap mq, mk, mv;
-  if (!tensor_map_3d(&mq, a.q, true, a.total, a.H_k, a.d_k, 64, kC, true) ||
-      !tensor_map_3d(&mk, a.k, true, a.total, a.H_k, a.d_k, 64, kC, true) ||
-      !tensor_map_3d(&mv, a.v, true, a.total, a.H, a.d_v, 64, kC, true))
+  if (!tensor_map_3d(&mq, in.q, true, a.total, a.H_k, pk, 64, kC, true) ||
+      !tensor_map_3d(&mk, in.k, true, a.total, a.H_k, pk, 64, kC, true) ||
+      !tensor_map_3d(&mv, in.v, true, a.total, a.H, pv, 64, kC, true))
     return cudaErrorInvalidValue;
   const auto pass = [&](int which) {
     return out_bf16 ? launch_pass<true>(mq, mk, mv, a, which, stream) : launch_pass<false>(mq, mk, mv, a, which, stream);
   };
-  cudaError_t e = cudaSuccess;
-  if (a.plan.order) e = launch_order_longest_first(a.cu, a.num_seqs, reinterpret_cast<int32_t *>(a.workspace), stream);
+  if (a.plan.order) e = launch_order_longest_first(a.cu, a.num_seqs, reinterpret_cast<int32_t *>(a.workspace + a.plan.ends), stream);
   if (e == cudaSuccess) e = pass(1);
   if (e != cudaSuccess || a.plan.seg_len == 0) return e;
   e = launch_delta_chain(a, stream);

@@ -28,11 +28,12 @@ __global__ void __launch_bounds__(kChainThreads) delta_chain_kernel(const DeltaA
   const int64_t place = delta_place(a, s);
   float *ends = reinterpret_cast<float *>(a.workspace + a.plan.ends);
   const float *maps = reinterpret_cast<const float *>(a.workspace + a.plan.maps);
-  auto at = [&](int64_t p, int r) { return ends + ((p * a.H + h) * a.d_k + r) * a.d_v + c; };
-  auto fetch = [&](int j) {  // M_j (d_k is a multiple of 8); one group of copies per call, also where there is none
+  const int pk = delta_up8(a.d_k), pv = delta_up8(a.d_v);
+  auto at = [&](int64_t p, int r) { return ends + ((p * a.H + h) * pk + r) * pv + c; };
+  auto fetch = [&](int j) {  // M_j; one group of copies per call, also where there is none
     if (j + 1 < segs) {
-      const float *M = maps + ((place + j) * a.H + h) * int64_t(a.d_k) * a.d_k;
-      const int per_row = a.d_k >> 2;
+      const float *M = maps + ((place + j) * a.H + h) * int64_t(pk) * pk;
+      const int per_row = pk >> 2;
       for (int i = threadIdx.x; i < a.d_k * per_row; i += kChainThreads) {
         const int r = i / per_row, k = i % per_row * 4;
         cp_async_16_zfill(&chain_smem[(j & 1) * 128 * kChainStride + r * kChainStride + k], M + i * 4, true);
@@ -40,7 +41,7 @@ __global__ void __launch_bounds__(kChainThreads) delta_chain_kernel(const DeltaA
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto on = [&](int i) { return rg + 32 * i < a.d_k && c < a.d_v; };  // (d_v is a multiple of 8)
+  auto on = [&](int i) { return rg + 32 * i < a.d_k && c < a.d_v; };  // (an odd d_v's last pair is in the row: pv)
   fetch(1);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(kChainThreads) delta_chain_kernel(const DeltaA
     __syncthreads();
     const float *M = chain_smem + (j & 1) * 128 * kChainStride + rg * kChainStride;
 #pragma unroll 4
-    for (int k = 0; k < a.d_k; k += 4) {
+    for (int k = 0; k < pk; k += 4) {  // (behind d_k, M's columns and E's rows are zero)
       float2 x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = *reinterpret_cast<const float2 *>(&E[(k + e) * kChainCols + 2 * cg]);
@@ -98,11 +99,14 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// The tensor-core kernel needs head sizes whose rows TMA can address (16 bytes) and takes a chunk of 64
-// tokens' time for the shortest sequence, so calls of short ones go to the token kernel: below `least` tokens a
-// sequence on average (16 sequences, 64 heads of 128, us by the token kernel / this one: 4 tokens 93 / 97,
-// 8 107 / 97, 24 176 / 98; 128 sequences: 4 767 / 667, 16 1021 / 671; 64 heads of 64, where a warp holds
-// a whole state: 8 tokens 38 / 87, 32 68 / 88; between the two where one size is above 64).
+// The tensor-core kernel takes a chunk of 64 tokens' time for the shortest sequence, so calls of short ones go
+// to the token kernel: below `least` tokens a sequence on average. us by the token kernel / this one at 8, 16,
+// 32, 64 and 100 tokens; 16 sequences of 64 heads: 128 x 128 103/91, 134/91, 200/93, 329/96; 64 x 128 68/84, 82/84,
+// 125/84; 128 x 64 54/88, 68/88, 105/90, 173/92; 64 x 64, where a warp holds a whole state, 35/82, 43/83,
+// 66/84, 107/83. Fewer chains than SMs (3 sequences of 8 heads): 128 x 128 9/15, 11/15, 13/15, 19/15; 64 x 64
+// 6/13, 7/13, 9/13, 12/13, 16/17. TMA needs rows of whole 16-byte pieces, so other head sizes run on padded
+// copies of q, k and v in the workspace, or without one in the token kernel (4096 tokens, 96 heads of 100: 345 us
+// by copies, 2099 by the token kernel; 32 heads of 68: 209, 835).
 //
 // A CTA holds one (sequence, head) from end to end, one CTA per SM, so few long sequences leave SMs idle. A
 // sequence cut into m segments runs 2 m - 3 of them side by side in pass 1 and m - 1 in pass 3: two segments'
@@ -111,13 +115,21 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, cudaStream_t stream) {
 // 65536, 16 heads: m = 10, 1335 us; m = 6: 1378 us; not cut: some 3100). Of several the lengths are not known
 // here, and cuts lie so far apart that pass 1 fills the SMs at most twice. Sequences in more chains than SMs run
 // longest first.
-DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool in_bf16, bool recurrent,
+DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool recurrent,
                      size_t workspace_bytes) {
   DeltaPlan p;
-  const int64_t least = d_k <= 64 && d_v <= 64 ? 44 : d_k <= 64 || d_v <= 64 ? 16 : 6;
-  p.tensor = in_bf16 && !recurrent && d_k % 8 == 0 && d_v % 8 == 0 && total >= least * num_seqs &&
-             int64_t(H) * d_v <= 1 << 25;  // (its output addresses)
+  const bool few = int64_t(num_seqs) * H <= kLinearSMs;
+  const int64_t least = d_k <= 64 && d_v <= 64 ? (few ? 88 : 44) : few ? 44 : d_v <= 64 ? 24 : d_k <= 64 ? 16 : 6;
+  p.tensor = in_bf16 && !recurrent && total >= least * num_seqs && int64_t(H) * d_v <= 1 << 25;  // (its output addresses)
   if (!p.tensor) return p;
+  const int pk = delta_up8(d_k), pv = delta_up8(d_v);
+  if (pk != d_k || pv != d_v) {
+    const size_t qk = pk != d_k ? align256(size_t(total) * H_k * pk * 2) : 0;
+    p.pad_k = qk, p.pad_v = 2 * qk;
+    p.bytes = p.ends = p.pad_v + (pv != d_v ? align256(size_t(total) * H * pv * 2) : 0);
+    p.pad = p.bytes <= workspace_bytes;
+    if (!p.pad) return DeltaPlan{};
+  }
   int64_t len = 0;
   if (num_seqs == 1) {
     const auto waves = [&](int64_t pieces) { return (pieces * H + kLinearSMs - 1) / kLinearSMs; };
@@ -134,19 +146,19 @@ DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int d_k, int d_v, bool 
   // (cuts that most sequences are far too short for would only cost the order of the others)
   if (len > 0 && total > 2 * len && 8 * total >= len * num_seqs) {
     const int64_t inner = total / len;
-    const size_t ends = align256(size_t(inner) * H * d_k * d_v * 4), maps = align256(size_t(inner) * H * d_k * d_k * 4);
-    if (ends + maps <= workspace_bytes) {
+    const size_t ends = align256(size_t(inner) * H * pk * pv * 4), maps = align256(size_t(inner) * H * pk * pk * 4);
+    if (p.bytes + ends + maps <= workspace_bytes) {
       p.seg_len = int32_t(len);
       p.inner = int32_t(inner);
-      p.maps = ends;
-      p.bytes = ends + maps;
+      p.maps = p.ends + ends;
+      p.bytes += ends + maps;
       return p;
     }
   }
   const size_t list = align256(size_t(num_seqs) * 4);
-  if (num_seqs > 1 && num_seqs <= 8192 && int64_t(num_seqs) * H > kLinearSMs && list <= workspace_bytes) {
+  if (num_seqs > 1 && num_seqs <= 8192 && !few && p.bytes + list <= workspace_bytes) {
     p.order = true;
-    p.bytes = list;
+    p.bytes += list;
   }
   return p;
 }

@@ -115,7 +115,14 @@ def test_workspace_sizes():
     size = B.delta_workspace_size
     f32, bf16 = torch.float32, torch.bfloat16
     for T in (1, 63, 5000, 100000):  # the token kernel
-        assert size(T, 1, 8, dtype=f32) == size(T, 1, 8, recurrent=True) == size(T, 1, 8, d_k=68) == size(T, 1, 8, d_v=4) == 0
+        assert size(T, 1, 8, dtype=f32) == size(T, 1, 8, recurrent=True) == size(T, 1, 8, dtype=f32, d_k=68) == 0
+    # copies of q and k, of v, or of all, with head sizes padded to multiples of 8; segments behind them
+    up = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    assert size(100, 1, 8, d_k=68, H_k=2) == 2 * up(100 * 2 * 72 * 2) and size(100, 1, 8, d_v=5) == up(100 * 8 * 8 * 2)
+    assert size(100, 1, 8, d_k=68, d_v=5, H_k=2) == 2 * up(100 * 2 * 72 * 2) + up(100 * 8 * 8 * 2)
+    assert size(43, 1, 8, d_k=68) == 0
+    cut = size(65536, 1, 16, d_k=128, d_v=120)
+    assert size(65536, 1, 16, d_k=128, d_v=117) == cut + 65536 * 16 * 120 * 2
     assert size(0, 0, 8) == size(0, 3, 8) == size(100, 1, 0) == size(-1, 1, 8) == size(100, 1, 8, H_k=3) == 0
     # one long sequence that leaves SMs idle is cut: an end state and a map for each segment
     n = size(65536, 1, 16)
@@ -128,8 +135,8 @@ def test_workspace_sizes():
     assert size(40 * 200, 40, 3) % (3 * 128 * 128 * 8) == 0
     assert size(9000 * 10, 9000, 32) == 0
     # short sequences go to the token kernel, by head sizes
-    assert size(40 * 5, 40, 32) == size(40 * 15, 40, 32, d_k=64) == size(40 * 43, 40, 32, d_k=64, d_v=64) == 0
-    assert size(40 * 6, 40, 32) == size(40 * 16, 40, 32, d_k=64) == size(40 * 44, 40, 32, d_k=64, d_v=64) == 256
+    for n, d_k, d_v in ((6, 128, 128), (16, 64, 128), (24, 128, 64), (44, 64, 64)):
+        assert size(40 * n - 1, 40, 32, d_k=d_k, d_v=d_v) == 0 and size(40 * n, 40, 32, d_k=d_k, d_v=d_v) == 256
     for T in (2**31 - 128, 2**30):  # the largest
         for N, H in ((1, 1), (1, 64), (7, 3), (1000, 64)):
             assert size(T, N, H) < 1 << 33

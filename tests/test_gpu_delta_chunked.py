@@ -48,6 +48,47 @@ def test_head_sizes(d_k, d_v, out_dtype):
     _check(make([150, 40], H=3, d_k=d_k, d_v=d_v, seed=d_k + d_v), scale=0.25, out_dtype=out_dtype)
 
 
+def _on_tensor_cores(c, out, fin, **kw):
+    """Whether a result is not the token kernel's (they differ in the last bits)."""
+    o, f = run(c, out_dtype=out.dtype, recurrent=True, **kw)
+    return not torch.equal(o, out) and not torch.equal(f, fin)
+
+
+@pytest.mark.parametrize("out_dtype", [B16, F32])
+@pytest.mark.parametrize("d_k,d_v", [(100, 72), (72, 100), (33, 40), (127, 127), (65, 1), (1, 128), (3, 3), (128, 61)])
+def test_padded_head_sizes(d_k, d_v, out_dtype):
+    c = make([150, 0, 140, 1], H=6, H_k=2, d_k=d_k, d_v=d_v, seed=d_k + d_v)
+    c = c if d_k > 64 or d_v > 64 else make([150, 140], H=6, H_k=2, d_k=d_k, d_v=d_v, seed=d_k + d_v)
+    out, fin = _check(c, scale=0.25, out_dtype=out_dtype)
+    assert d_k == 1 or _on_tensor_cores(c, out, fin, scale=0.25)
+    o, f = run(c, scale=0.25, out_dtype=out_dtype, workspace=None)  # no room for the copies
+    assert not _on_tensor_cores(c, o, f, scale=0.25)
+
+
+@pytest.mark.parametrize("d_k,d_v", [(100, 72), (128, 33), (65, 127)])
+def test_padded_segments_and_rows_behind(d_k, d_v):
+    """Cut sequences of odd head sizes, a workspace full of NaN, rows behind the last sequence."""
+    lens = [2600]
+    c = make(lens, H=2, d_k=d_k, d_v=d_v, decay=0.01, seed=13)
+    wide = {n: torch.cat([c[n], torch.full_like(c[n][:40], float("nan"))]) for n in ("q", "k", "v", "log_decay", "beta")}
+    n = binding.delta_workspace_size(2640, 1, 2, d_k, d_v, B16, F32)
+    assert n > 2 * 2640 * 2 * d_v
+    ws = torch.full((n // 4,), float("nan"), device="cuda").view(torch.uint8)
+    for out_dtype in (B16, F32):
+        out = torch.full((2640, 2, d_v), 7.0, device="cuda", dtype=out_dtype)
+        o, fin = run({**c, **wide}, out=out, workspace=ws)
+        assert (out[2600:] == 7).all()
+        _check_against(c, out[:2600].contiguous(), fin)
+
+
+@pytest.mark.parametrize("out_dtype", [B16, F32])
+@pytest.mark.parametrize("lens", [[40, 0], [31, 32, 33], [6, 6, 7], [63, 1, 5], [8, 64, 10]])
+def test_short_sequences_of_many_heads(lens, out_dtype):
+    c = make(lens, H=104, H_k=8, seed=sum(lens))
+    out, fin = _check(c, out_dtype=out_dtype)
+    assert _on_tensor_cores(c, out, fin)
+
+
 @pytest.mark.parametrize("H,H_k", [(6, 1), (6, 3), (8, 2)])
 @pytest.mark.parametrize("per_token", [True, False])
 def test_shared_heads(H, H_k, per_token):
