@@ -143,8 +143,9 @@ DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d
   }
   len = (len + 63) / 64 * 64;
   if (len > 0 && len < 512) len = 512;
-  // (cuts that most sequences are far too short for would only cost the order of the others)
-  if (len > 0 && total > 2 * len && 8 * total >= len * num_seqs) {
+  // (room for three segments; and cuts that most sequences are too short for would only cost the order of the
+  // others: 323 us instead of 280 for prompts of 4096 tokens and less on 32 heads, cut at 4672)
+  if (len > 0 && total >= 3 * len - 63 * 3 && 8 * total >= len * num_seqs) {
     const int64_t inner = total / len;
     const size_t ends = align256(size_t(inner) * H * pk * pv * 4), maps = align256(size_t(inner) * H * pk * pk * 4);
     if (p.bytes + ends + maps <= workspace_bytes) {
