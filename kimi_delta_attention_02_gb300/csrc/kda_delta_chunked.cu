@@ -265,13 +265,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         int kq = 0, vs = 0;  // issued
         uint32_t ks = 0, vs_ = 0, ks_turn = 1, vs_turn = 1;  // buffers, and the parity of the use before
         const uint32_t kq_bytes = kb * (run.emit ? 16384 : 8192);
-  #pragma unroll 1
+#pragma unroll 1
         for (int32_t t = int32_t(run.t0), n = 0; n < chunks; ++n, t += kC) {
           if (!wait(ctl->kq_free[ks], ks_turn)) break;
           uint8_t *dst = smem + ks * kTileKQ;
           uint64_t &full = ctl->kq_full[ks];
           mbar_arrive_expect_tx(&full, kq_bytes);
-  #pragma unroll 1
+#pragma unroll 1
           for (int b = 0; b < kb; ++b) {
             tma_load_3d(dst + b * 16384, &mk, &full, 64 * b, hk, t);
             if (run.emit) tma_load_3d(dst + b * 16384 + 8192, &mq, &full, 64 * b, hk, t);
@@ -281,16 +281,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (run.identity) continue;
           if (!wait(ctl->v_free[vs_], vs_turn)) break;
           mbar_arrive_expect_tx(&ctl->v_full[vs_], vb * 8192);
-  #pragma unroll 1
+#pragma unroll 1
           for (int b = 0; b < vb; ++b)
             tma_load_3d(smem + F::oV + vs_ * kTileV + b * 8192, &mv, &ctl->v_full[vs_], 64 * b, h, t);
           ++vs;
           if (++vs_ == kV) vs_ = 0, vs_turn ^= 1;
         }
         // every load issued has landed before the CTA may end
-  #pragma unroll 1
+#pragma unroll 1
         for (int i = kq > kKQ ? kq - kKQ : 0; i < kq; ++i) wait(ctl->kq_full[i % kKQ], i / kKQ);
-  #pragma unroll 1
+#pragma unroll 1
         for (int i = vs > kV ? vs - kV : 0; i < vs; ++i) wait(ctl->v_full[i % kV], i / kV);
       }
     } else if (warp == 1) {
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t iD = umma_idesc_bf16(128, a.d_k > 64 ? 128 : 64, false, true, false);
       constexpr uint32_t iV = umma_idesc_bf16(128, 64, true, false, false);
       uint32_t stage = 0;
-  #pragma unroll 1
+#pragma unroll 1
       for (int n = 0; n < chunks; ++n) {
         // nothing, as the compiler does not see: addresses made with it are not kept in registers over the loop,
         // forty of them
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!run.identity) {
           tc_fence_after();
           const uint64_t dV = desc_mn(base + F::oV + n % kV * kTileV, 8192);
-  #pragma unroll
+#pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
             mma_ss(leader, tU, dV + 128 * ks, dT + 2 * ks, iV, ks > 0);
             mma_ss(leader, tU, dV + 128 * ks, dT + (kTileT >> 4) + 2 * ks, iV, 1);
@@ -331,12 +331,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Each product begins with the steps whose operands come first: S, X and U' by halves of each thread's
         // columns (steps 0, 1, 4, 5 of S, then 2, 3, 6, 7; steps 0, 2, then 1, 3 of the tokens).
         bool ok = true;
-  #pragma unroll
+#pragma unroll
         for (int p = 0; p < 2; ++p) {
           ok = ok && wait_warp(ctl->s_full[p], n);
           if (!ok) break;
           tc_fence_after();
-  #pragma unroll
+#pragma unroll
           for (int m = 0; m < 4; ++m) {
             const int ks = 4 * (m >> 1) + 2 * p + (m & 1);
             if (ks >= nk) break;
@@ -347,12 +347,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         mma_commit(leader, ctl->x_done);
-  #pragma unroll
+#pragma unroll
         for (int p = 0; p < 2; ++p) {
           ok = ok && wait_warp(ctl->r_full[p], n);
           if (!ok) break;
           tc_fence_after();
-  #pragma unroll
+#pragma unroll
           for (int ks = p; ks < 4; ks += 2) {
             mma_ts(leader, tU, tX + 16 * ks, dTW + 2 * ks, i64, ks > 0 || !run.identity);
             mma_ts(leader, tU, tX + 16 * ks, dTW + (kTileT >> 4) + 2 * ks, i64, 1);
@@ -363,12 +363,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_commit(leader, ctl->u_done);
         mma_commit(leader, ctl->t_free[n & 1]);
         if (run.emit && !wait_warp(ctl->xq_done, n)) break;  // Q S has read S
-  #pragma unroll
+#pragma unroll
         for (int p = 0; p < 2; ++p) {
           ok = ok && wait_warp(ctl->up_full[p], n);
           if (!ok) break;
           tc_fence_after();
-  #pragma unroll
+#pragma unroll
           for (int ks = p; ks < 4; ks += 2) {
             mma_ts(leader, tS, tU + 16 * ks, dKT + 128 * ks, iD, ks > 0);
             mma_ts(leader, tS, tU + 16 * ks + 8, dKT + 128 * ks, iD, 1);
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0 && !wait_warp(ctl->gram_read, n - 1)) return false;
         tc_fence_after();
         const uint64_t d = dKQ + (n % kKQ) * (kTileKQ >> 4);
-  #pragma unroll
+#pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           if (ks >= nk) break;
           const uint64_t b = d + ((ks >> 2) * 1024 + (ks & 3) * 2);
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       // K K^T and Q K^T two chunks ahead, while X is split; Q S while U becomes U'; P U while S is made
-  #pragma unroll 1
+#pragma unroll 1
       for (int n = -2; n < chunks; ++n) {
         const bool here = run.emit && n >= 0;
         if (here && !wait_warp(ctl->x_done, n)) break;
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0 && !wait_warp(ctl->o_read, n - 1)) break;
         tc_fence_after();
         const uint64_t d = dKQ + ((n % kKQ) * (kTileKQ >> 4) + (8192 >> 4));
-  #pragma unroll
+#pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           if (ks >= nk) break;
           const uint64_t b = d + ((ks >> 2) * 1024 + (ks & 3) * 2);
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dPn = desc_k(base + F::oP) + n % kP * (F::kTileP >> 4);
         if (!wait_warp(ctl->d_done, n)) break;  // (U for the read-out came before)
         tc_fence_after();
-  #pragma unroll
+#pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
           mma_ts(leader, tO, tUH + 8 * ks, dPn + 2 * ks, i64, ks > 0);
           mma_ts(leader, tO, tUH + 32 + 8 * ks, dPn + 2 * ks, i64, 1);
@@ -440,11 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool per_token = a.per_token != 0;
       const float constant = per_token ? 0.f : a.log_decay[h];
       float g[2] = {}, b[2] = {};
-  #pragma unroll 1
+#pragma unroll 1
       for (int n = -1; n < chunks; ++n) {
         double G[2];
         const float beta[2] = {b[0], b[1]};
-  #pragma unroll
+#pragma unroll
         for (int e = 0; e < 2; ++e) {
           const double x = double(g[e]) * kLog2e;
           G[e] = x < kMinLog2 ? kMinLog2 : x;  // a NaN stays
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (n < 0) continue;
         double sum = G[0] + G[1];
-  #pragma unroll 1
+#pragma unroll 1
         for (int o = 1; o < 32; o <<= 1) {
           const double up = __shfl_up_sync(0xffffffffu, sum, o);
           if (lane >= o) sum += up;
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         G[0] = sum - G[1], G[1] = sum;
         Table &w = tab[n % kTabs];
         if (!wait_warp(ctl->tab_free[n % kTabs], (n / kTabs) ^ 1)) break;
-  #pragma unroll 1
+#pragma unroll 1
         for (int e = 0; e < 2; ++e) {
           const int i = 2 * lane + e;
           const double x = e == 0 ? G[0] : G[1];
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // X = K S, split where it stands
         if (!wait_warp(ctl->x_done, n)) break;
         tc_fence_after();
-  #pragma unroll 1
+#pragma unroll 1
         for (int p = 0; p < 2; ++p) {
           float x[16];
           tmem_ld16_wait(rX + 16 * p, x);
@@ -782,13 +782,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // U, and U' over it
         if (!wait_warp(ctl->u_done, n)) break;
         tc_fence_after();
-  #pragma unroll 1
+#pragma unroll 1
         for (int p = 0; p < 2; ++p) {
           float x[16];
           tmem_ld16_wait(rU + 16 * p, x);
           if (run.emit) {
             float hi[8], lo[8];
-  #pragma unroll
+#pragma unroll
             for (int j = 0; j < 8; ++j) {
               uint32_t h, l;
               split_pair(x[2 * j], x[2 * j + 1], h, l);
@@ -797,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st8(rUH + 8 * p, hi);
             tmem_st8(rUH + 32 + 8 * p, lo);
           }
-  #pragma unroll
+#pragma unroll
           for (int j = 0; j < 16; j += 2) {
             const float2 y = f2_mul(make_float2(x[j], x[j + 1]), *reinterpret_cast<const float2 *>(&tb.w[32 * half + 16 * p + j]));
             x[j] = y.x, x[j + 1] = y.y;

@@ -153,6 +153,23 @@ def test_longest_first():
     assert torch.equal(out, o) and torch.equal(fin, f)
 
 
+@pytest.mark.parametrize("out_dtype", [B16, F32])
+@pytest.mark.parametrize("init", [True, False])
+@pytest.mark.parametrize("lens", [[900, 300, 130] + [0] * 40, [0, 64, 0, 1] * 10 + [700], [70] * 30 + [0] * 7 + [1] * 9,
+                                  [1] * 25 + [500, 400]])
+def test_many_sequences_and_heads(lens, init, out_dtype):
+    """Several times more (sequence, head)s than SMs: long ones, some of one token, empty ones in a row."""
+    c = make(lens, H=24, H_k=2, d_k=64, d_v=72, init=init, seed=sum(lens))
+    assert binding.delta_workspace_size(sum(lens), len(lens), 24, 64, 72, B16, out_dtype) == 256
+    out, fin = _check(c, out_dtype=out_dtype)
+    o, f = run(c, out_dtype=out_dtype, workspace=None)
+    assert torch.equal(out, o) and torch.equal(fin, f)
+    if init:
+        state = c["init_state"].clone()
+        o, f = run({**c, "init_state": state}, out_dtype=out_dtype, final_state=state)
+        assert torch.equal(out, o) and torch.equal(fin, f)
+
+
 @pytest.mark.parametrize("T", [200, 2500])
 def test_states(T):
     lens = [T, 0, 60]
