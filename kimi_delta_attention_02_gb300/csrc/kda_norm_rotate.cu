@@ -3,11 +3,12 @@
 // one), a = w cos p and b = -+ w_partner sin p of the token's angles, which all heads share.
 //
 // Reads and writes q and k once at about 7 flops per element: bound by HBM bandwidth (4096 tokens, 192 heads
-// of 128, bf16: 403 MB in 79 us, 5.1 TB/s; the copy rate would be 60 us), by latency for a few tokens (one token:
-// 6 us). The angles of a token are formed once per CTA, in shared memory. A head row takes as many lanes as it has pieces of 8
-// channels (the next power of two), so that a warp works on up to 32 rows at once, and a lane keeps the
-// angles of its channels in registers while it goes through the token's heads, two at a time. A turned
-// channel's partner is in the same lane (neighbours) or comes by a second load, which finds its line in L1.
+// of 128, bf16: 403 MB in 80 us, 5 TB/s; the copy rate would be 60 us), by latency for a few tokens (one token:
+// 6 us). The angles of a token are formed once per CTA, in shared memory. A head row takes as many lanes as it
+// has pieces of 8 channels, so that a warp works on up to 32 rows at once (10007 tokens, 20 heads of 72: 23 us; 31
+// with lanes in powers of two). A lane keeps the factors of its channels in registers while it goes through the
+// token's heads, two at a time. A turned channel's partner is in the same lane (neighbours), in another one,
+// or comes by a second load, which finds its line in L1.
 //
 // Angles. p = position * f can be millions of radians, where fp32 is off by tenths. A turn is a number
 // modulo one: F = f / (2 pi) modulo one as a 64-bit fraction (off by 2^-63 while f is below 2^24), and the
@@ -78,22 +79,29 @@ __device__ __forceinline__ void load4(const void *base, int64_t at, float *x) {
   }
 }
 
-// Rows of whole pieces of 8 channels on 16-byte boundaries, each of which turns as a whole or not at all.
-// kPart: partners are neighbours (0), or lie rot / 2 channels away: whole pieces (8) come from their lane,
-// half pieces (4) by a load. `lanes` threads per row, `group` rows of a token side by side, so
-// kThr / (lanes group) tokens at a time; `pairs` threads form a token's angles.
+// Rows of whole pieces of 8 channels on 16-byte boundaries. kPart: partners are neighbours (0), or lie rot / 2
+// channels away: whole pieces (8) come from their lane, half pieces (4) by a load, others (1) by a load each. With
+// 1 and 2 (neighbours) a piece may turn in part; else it turns as a whole or not at all. `lanes` threads per
+// row, `group` rows of a token side by side; `pairs` threads form a token's angles. (65536 tokens, 18 heads of 64 of
+// which 20 channels turn: 117 us as halves, 70 as neighbours; 155 by the kernel below.)
 template <bool kInBF16, bool kOutBF16, int kPart>
 __global__ void __launch_bounds__(kThr, 3) rotate_kernel(const RotateArgs a, int lanes, int group, int pairs) {
   constexpr int kEi = kInBF16 ? 2 : 4, kEo = kOutBF16 ? 2 : 4;
   constexpr int kU = kInBF16 ? 2 : 1;  // rows at a time, and as many on their way
+  constexpr bool kNear = kPart == 0 || kPart == 2, kSome = kPart == 1 || kPart == 2;
   __shared__ uint64_t s_turn[kRotateMaxD / 2];
   __shared__ __align__(16) float2 s_cs[2][kThr * 4];  // tokens x rot / 2: a row has at most 8 channels per lane
   const int tid = threadIdx.x, lane = tid & 31;
-  const int slot = tid / lanes, tokens = kThr / (lanes * group), token = slot / group;
-  const int c0 = 8 * (tid % lanes), first = slot % group + group * blockIdx.y, stride = group * gridDim.y;
+  const int per_warp = 32 / lanes, slots = kThr / 32 * per_warp;  // (lanes behind a warp's last row take part in shuffles only)
+  const int piece = lane % lanes, slot = lane < per_warp * lanes ? (tid >> 5) * per_warp + lane / lanes : slots;
+  const int tokens = slots / group, token = slot / group;
+  const int c0 = 8 * piece, first = slot % group + group * blockIdx.y, stride = group * gridDim.y;
   const bool turns = c0 < 2 * a.half, upper = c0 >= a.half;
   const int partner = turns ? (upper ? c0 - a.half : c0 + a.half) : c0;  // of a whole piece, and its lane
   const int from_lane = lane + (partner - c0) / 8;
+  int half_way = 1;  // half of the next power of two
+  while (2 * half_way < lanes) half_way *= 2;
+  if (lanes == 1) half_way = 0;
   for (int i = tid; i < a.half; i += kThr) s_turn[i] = turns_per_position(a.inv_freq[i]);
   __syncthreads();
   int buf = 0;
@@ -101,7 +109,7 @@ __global__ void __launch_bounds__(kThr, 3) rotate_kernel(const RotateArgs a, int
   for (int64_t t0 = int64_t(blockIdx.x) * tokens; t0 < a.tokens; t0 += int64_t(gridDim.x) * tokens, buf ^= 1) {
     const int here = a.tokens - t0 < tokens ? int(a.tokens - t0) : tokens;
     const int64_t t = t0 + token;
-    const bool mine = c0 < a.d && token < here;
+    const bool mine = token < here;
     // the first row is on its way while the angles are formed
     const uint8_t *src;
     Piece<kInBF16> next[kU] = {};
@@ -134,11 +142,11 @@ __global__ void __launch_bounds__(kThr, 3) rotate_kernel(const RotateArgs a, int
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int c = c0 + e;
-        const bool up = kPart == 0 ? (e & 1) != 0 : c >= a.half;
-        const int p = kPart == 0 ? c ^ 1 : up ? c - a.half : c + a.half;
+        const bool up = kNear ? (e & 1) != 0 : c >= a.half;
+        const int p = kNear ? c ^ 1 : up ? c - a.half : c + a.half;
         float x = 1.f, y = 0.f;
-        if (mine && turns) {
-          const float2 cs = s_cs[buf][token * a.half + (kPart == 0 ? c >> 1 : up ? p : c)];
+        if (mine && (kSome ? c < 2 * a.half : turns)) {
+          const float2 cs = s_cs[buf][token * a.half + (kNear ? c >> 1 : up ? p : c)];
           x = cs.x, y = up ? cs.y : -cs.y;
           if (w != nullptr) y *= w[p];
         }
@@ -166,19 +174,31 @@ __global__ void __launch_bounds__(kThr, 3) rotate_kernel(const RotateArgs a, int
           for (int e = 0; e < 8; e += 2) s2 = f2_fma(make_float2(x[e], x[e + 1]), make_float2(x[e], x[e + 1]), s2);
           sum[u] = s2.x + s2.y;
         }
+        // to a row's first lane, and from there to all
 #pragma unroll 1
-        for (int off = lanes >> 1; off > 0; off >>= 1) {
+        for (int off = half_way; off > 0; off >>= 1) {
 #pragma unroll
-          for (int u = 0; u < kU; ++u) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], off);
+          for (int u = 0; u < kU; ++u) {
+            const float other = __shfl_down_sync(0xffffffffu, sum[u], off);
+            if (piece + off < lanes) sum[u] += other;
+          }
         }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) sum[u] = __shfl_sync(0xffffffffu, sum[u], lane - piece);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const bool ok = mine && h + u * stride < rows;
           float x[8], xp[8];
           raw[u].get(x);
-          if constexpr (kPart == 0) {
+          if constexpr (kNear) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) xp[e] = x[e ^ 1];
+            for (int e = 0; e < 8; ++e) xp[e] = kSome && c0 + e >= 2 * a.half ? 0.f : x[e ^ 1];
+          } else if constexpr (kPart == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int c = c0 + e;
+              xp[e] = ok && c < 2 * a.half ? load_elem<kInBF16>(row + u * row_in, c < a.half ? c + a.half : c - a.half) : 0.f;
+            }
           } else if constexpr (kPart == 8) {
             Piece<kInBF16> p;
 #pragma unroll
@@ -200,7 +220,7 @@ __global__ void __launch_bounds__(kThr, 3) rotate_kernel(const RotateArgs a, int
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             y[e] = f2_mul(make_float2(x[2 * e], x[2 * e + 1]), ca[e]);
-            // (left out, not multiplied by zero, where nothing turns: the partner may be infinite)
+            // (left out or zero, not multiplied by zero, where nothing turns: the partner may be infinite)
             if (turns) y[e] = f2_fma(make_float2(xp[2 * e], xp[2 * e + 1]), cb[e], y[e]);
             y[e] = f2_mul(y[e], make_float2(r, r));
           }
@@ -295,25 +315,26 @@ cudaError_t launch_norm_rotate(const RotateArgs &a, bool in_bf16, bool out_bf16,
     return p == nullptr || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (a.tokens == 1 || stride * size % 16 == 0));
   };
   const int si = in_bf16 ? 2 : 4, so = out_bf16 ? 2 : 4;
-  if (a.d % 8 == 0 && a.half % 4 == 0 && whole(a.x[0], a.stride[0], si) && whole(a.x[1], a.stride[1], si) &&
+  if (a.d % 8 == 0 && whole(a.x[0], a.stride[0], si) && whole(a.x[1], a.stride[1], si) &&
       whole(a.out[0], a.out_stride[0], so) && whole(a.out[1], a.out_stride[1], so)) {
     using Kern = void (*)(const RotateArgs, int, int, int);
-#define KDA_ROT(ib, ob) {rotate_kernel<ib, ob, 0>, rotate_kernel<ib, ob, 4>, rotate_kernel<ib, ob, 8>}
-    static const Kern kernels[4][3] = {KDA_ROT(false, false), KDA_ROT(false, true), KDA_ROT(true, false), KDA_ROT(true, true)};
+#define KDA_ROT(ib, ob) \
+  {rotate_kernel<ib, ob, 0>, rotate_kernel<ib, ob, 2>, rotate_kernel<ib, ob, 8>, rotate_kernel<ib, ob, 4>, rotate_kernel<ib, ob, 1>}
+    static const Kern kernels[4][5] = {KDA_ROT(false, false), KDA_ROT(false, true), KDA_ROT(true, false), KDA_ROT(true, true)};
 #undef KDA_ROT
-    int lanes = 1, pairs = 1, group = 1;
-    while (8 * lanes < a.d) lanes *= 2;
+    const int lanes = a.d / 8, slots = kThr / 32 * (32 / lanes);
+    int pairs = 1, group = 1;
     while (pairs < a.half) pairs *= 2;
-    const int rows = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1], slots = kThr / lanes;
+    const int rows = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1];
     const int64_t fit = 152 * 3;
     // A lane's factors serve up to twelve rows of a token (us at 1 / 3 / 6 / 12 / 24 rows: 4096 tokens, 192 heads of 128
-    // 82 / 82 / 82 / 79 / 83; 80 heads 59 / 59 / 43 / 40 / 45; 10007 tokens, 20 heads of 72 94 / 39 / 33 / 31 / 31).
-    while (group < slots && group * 12 < rows) group *= 2;
-    const int64_t passes = (a.tokens + slots / group - 1) / (slots / group);
+    // 82 / 82 / 82 / 79 / 83; 80 heads 59 / 59 / 43 / 40 / 45).
+    while (2 * group <= slots && group * 12 < rows) group *= 2;
+    const int64_t tokens = slots / group, passes = (a.tokens + tokens - 1) / tokens;
     // Few tokens: their heads over several CTAs.
     const int64_t most = (rows + group - 1) / group, spare = fit / passes;
     const unsigned parts = unsigned(spare < 1 ? 1 : spare < most ? spare : most);
-    kernels[2 * int(in_bf16) + int(out_bf16)][interleaved ? 0 : a.half % 8 == 0 ? 2 : 1]<<<
+    kernels[2 * int(in_bf16) + int(out_bf16)][interleaved ? (a.half % 4 == 0 ? 0 : 1) : a.half % 8 == 0 ? 2 : a.half % 4 == 0 ? 3 : 4]<<<
         dim3(unsigned(passes < fit ? passes : fit), parts), kThr, 0, stream>>>(a, lanes, group, pairs);
     return cudaGetLastError();
   }

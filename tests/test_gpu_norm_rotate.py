@@ -116,6 +116,22 @@ def test_in_place_in_a_fused_projection(d, rot, interleaved):
     assert torch.equal(rows[:, 7 * d:], was[:, 7 * d:]) and not torch.equal(rows[:, :7 * d], was[:, :7 * d])
 
 
+@pytest.mark.parametrize("dtype,out_dtype", [(B16, B16), (F32, F32), (B16, F32)])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 20), (128, 6), (72, 70), (200, 106), (24, 22), (256, 252), (40, 2)])
+def test_pieces_that_turn_in_part(d, rot, interleaved, dtype, out_dtype):
+    """rot is no multiple of 8, so that a piece of 8 channels turns in part; also in place, and beside an infinity
+    in the first channel that does not turn."""
+    for T, H in ((70, 3), (3, 40)):
+        _check(T, H, 2, d, rot, "rms", interleaved, dtype=dtype, out_dtype=out_dtype)
+    q, k, pos, f, _, w = _inputs(37, 5, 2, d, rot, dtype=dtype, seed=3)
+    q[4, 1, rot] = float("inf")
+    want, _ = binding.norm_rotate(q, k, pos, f, norm=None, interleaved=interleaved)
+    assert want[4, 1, rot] == float("inf") and int((~torch.isfinite(want)).sum()) == 1
+    qo, _ = binding.norm_rotate(q, k, pos, f, norm=None, interleaved=interleaved, q_out=q)
+    assert qo is q and torch.equal(q, want)
+
+
 def test_views_off_16_byte_boundaries():
     flat = torch.randn(4 * 3 * 64 + 3, device="cuda").to(B16)
     pos, f = torch.arange(4, device="cuda"), torch.rand(32, device="cuda")
