@@ -636,8 +636,9 @@ kda_status kda_delta_prefill(const kda_delta_prefill_params *p, void *stream) {
   a.plan = delta_plan(T, p->num_seqs, p->H, p->H_k, p->d_k, p->d_v, in_bf16, p->force_recurrent != 0, p->workspace_bytes);
   a.workspace = static_cast<uint8_t *>(p->workspace);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  const cudaError_t err = a.plan.tensor ? launch_delta_chunked(a, out_bf16, cs)
-                                        : launch_delta_recurrent(a, in_bf16, out_bf16, cs);
+  cudaError_t err = a.plan.few >= 0 ? launch_delta_short(a, in_bf16, out_bf16, cs) : cudaSuccess;
+  if (err == cudaSuccess)
+    err = a.plan.tensor ? launch_delta_chunked(a, out_bf16, cs) : launch_delta_recurrent(a, in_bf16, out_bf16, cs);
   return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 

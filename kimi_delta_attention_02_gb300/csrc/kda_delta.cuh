@@ -16,6 +16,7 @@ namespace kda {
 
 struct DeltaPlan {
   bool tensor = false;   // tensor-core kernel, else the token kernel
+  int32_t few = -1;      // sequences of up to this many tokens are the decode kernel's (-1: none)
   bool order = false;    // longest sequences first, by a list in the workspace
   bool pad = false;      // q, k, v by copies whose head sizes are padded to multiples of 8
   int32_t seg_len = 0;   // tokens between cuts (0: none)
@@ -54,6 +55,7 @@ __host__ __device__ constexpr int delta_up8(int d) { return (d + 7) & ~7; }
 DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool recurrent,
                      size_t workspace_bytes);
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream);
+cudaError_t launch_delta_short(const DeltaArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream);
 cudaError_t launch_delta_chunked(const DeltaArgs &a, bool out_bf16, cudaStream_t stream);
 cudaError_t launch_delta_chain(const DeltaArgs &a, cudaStream_t stream);
 cudaError_t launch_delta_decode(const void *q, const void *k, const void *v, const float *log_decay, bool per_token,

@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     LinearSlot s;
     if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, index, s)) return;
     if ((pass == 3 || map) ? s.first : s.last && !s.first) return;
+    if (s.first && s.last && s.t1 - s.t0 <= a.plan.few) return;  // done by the decode kernel
     const int pk = delta_up8(a.d_k), pv = delta_up8(a.d_v);
     const int64_t dd = int64_t(a.d_k) * a.d_v, ee = int64_t(pk) * pv;
     float *ends = reinterpret_cast<float *>(a.workspace + a.plan.ends);

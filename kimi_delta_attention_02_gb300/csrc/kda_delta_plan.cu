@@ -108,6 +108,11 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, cudaStream_t stream) {
 // copies of q, k and v in the workspace, or without one in the token kernel (4096 tokens, 96 heads of 100: 345 us
 // by copies, 2099 by the token kernel; 32 heads of 68: 209, 835).
 //
+// The shortest sequences go to the decode kernel, which holds no more than a state and is bound by its bytes, where
+// there are more chains than SMs and the mean length says that there may be some: those of up to `few` tokens. us
+// by the token kernel / that one at 1, 4, 8 and 16 tokens, 128 sequences of 64 heads: 128 x 128 754/219, 764/468,
+// 798/808, 1019/1499 (the tensor cores: 667); 64 x 64 250/72, 252/121, 277/195, 336/347 (640 by the tensor cores).
+//
 // A CTA holds one (sequence, head) from end to end, one CTA per SM, so few long sequences leave SMs idle. A
 // sequence cut into m segments runs 2 m - 3 of them side by side in pass 1 and m - 1 in pass 3: two segments'
 // time instead of m, for up to three times the work. Of a single sequence m is that of the least time by
@@ -118,8 +123,9 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, cudaStream_t stream) {
 DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool recurrent,
                      size_t workspace_bytes) {
   DeltaPlan p;
-  const bool few = int64_t(num_seqs) * H <= kLinearSMs;
-  const int64_t least = d_k <= 64 && d_v <= 64 ? (few ? 88 : 44) : few ? 44 : d_v <= 64 ? 24 : d_k <= 64 ? 16 : 6;
+  const bool idle = int64_t(num_seqs) * H <= kLinearSMs;
+  const int64_t least = d_k <= 64 && d_v <= 64 ? (idle ? 88 : 44) : idle ? 44 : d_v <= 64 ? 24 : d_k <= 64 ? 16 : 6;
+  if (!recurrent && !idle && total < 64 * int64_t(num_seqs)) p.few = d_k <= 64 && d_v <= 64 ? 12 : 5;
   p.tensor = in_bf16 && !recurrent && total >= least * num_seqs && int64_t(H) * d_v <= 1 << 25;  // (its output addresses)
   if (!p.tensor) return p;
   const int pk = delta_up8(d_k), pv = delta_up8(d_v);
@@ -128,7 +134,11 @@ DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d
     p.pad_k = qk, p.pad_v = 2 * qk;
     p.bytes = p.ends = p.pad_v + (pv != d_v ? align256(size_t(total) * H * pv * 2) : 0);
     p.pad = p.bytes <= workspace_bytes;
-    if (!p.pad) return DeltaPlan{};
+    if (!p.pad) {
+      DeltaPlan token;
+      token.few = p.few;
+      return token;
+    }
   }
   int64_t len = 0;
   if (num_seqs == 1) {
@@ -157,7 +167,7 @@ DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d
     }
   }
   const size_t list = align256(size_t(num_seqs) * 4);
-  if (num_seqs > 1 && num_seqs <= 8192 && !few && p.bytes + list <= workspace_bytes) {
+  if (num_seqs > 1 && num_seqs <= 8192 && !idle && p.bytes + list <= workspace_bytes) {
     p.order = true;
     p.bytes += list;
   }

@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const Delt
   const int h = blockIdx.x % a.H, n = blockIdx.x / a.H, hk = h / (a.H / a.H_k);
   const int col0 = blockIdx.y * kCols, cw = 32 / kLanes * kNC * w + kNC * cl, col = col0 + cw;
   const int64_t t0 = a.cu[n], t1 = a.cu[n + 1];
+  if (t1 - t0 <= a.plan.few) return;  // done by the decode kernel
 
   // global -> registers -> shared memory, a stage of kTok tokens at a time (as stored: a conversion here
   // would wait for the load). Rows of q and k that are whole 16-byte pieces take 16-byte loads: a load
