@@ -815,6 +815,8 @@ def _heads_of_rows(name, x):
     """The token stride of [T, heads, d] whose heads and channels are contiguous (a part of a fused
     projection's rows, or a whole tensor)."""
     T, H, d = x.shape
+    if x.is_contiguous():
+        return H * d
     if (d > 1 and x.stride(2) != 1) or (H > 1 and x.stride(1) != d):
         raise ValueError(f"{name}: a token's heads and channels must be contiguous")
     return x.stride(0) if T > 1 else H * d
@@ -888,16 +890,22 @@ def norm_rotate(q, k, positions, inv_freq, *, norm="rms", q_weight=None, k_weigh
             if out_dtype is not None and x.dtype != out_dtype:
                 raise TypeError(f"{name} must be {out_dtype}")
             dtype = x.dtype
+    # tokens lie q_row (k_row) elements apart in outputs made here
+    q_row, k_row = H_q * d, H_k * d
     if q_out is None:
         q_out = _empty(q.shape, dtype, q.device, stream)
-    if k is not None and k_out is None:
-        k_out = _empty(k.shape, dtype, k.device, stream)
+    else:
+        q_row = _heads_of_rows("q_out", q_out)
+    if k is not None:
+        if k_out is None:
+            k_out = _empty(k.shape, dtype, k.device, stream)
+        else:
+            k_row = _heads_of_rows("k_out", k_out)
     if k is not None and k_out.dtype != q_out.dtype:
         raise TypeError("q_out and k_out must share one dtype")
     p = NormRotateParams(_NORM_ROTATE_BYTES, _io_dtype(q.dtype), _io_dtype(q_out.dtype), _NORMS[norm], H_q, H_k, d,
                          2 * half, 1 if interleaved else 0, axes, size, eps, T, _heads_of_rows("q", q),
-                         0 if k is None else _heads_of_rows("k", k), _heads_of_rows("q_out", q_out),
-                         0 if k is None else _heads_of_rows("k_out", k_out), q.data_ptr(), _address(k),
+                         0 if k is None else _heads_of_rows("k", k), q_row, k_row, q.data_ptr(), _address(k),
                          _address(q_weight), _address(k_weight), _address(positions), _address(inv_freq),
                          q_out.data_ptr(), _address(k_out), axis_of)
     st = lib().kda_norm_rotate(ctypes.byref(p), _stream_handle(stream))

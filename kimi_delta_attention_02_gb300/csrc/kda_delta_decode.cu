@@ -3,14 +3,14 @@
 // sequences and H heads; and prompts of a few tokens, one token after the other on the state in shared memory.
 //
 // One read and one write of the d_k x d_v fp32 state per (sequence, head) against 1.2 flops per byte:
-// bound by HBM bandwidth (256 sequences, 96 heads of 128: 3.25 GB in 470 to 484 us, the copy rate), and by
-// latency when few states are in flight (one sequence: 6 us, 2 at the copy rate). A new entry needs its whole old
-// column (S'^T k), so a CTA holds all key rows of its value columns, 32 entries per thread: kRows rows of
+// bound by HBM bandwidth (256 sequences, 96 heads of 128: 3.25 GB in 465 to 484 us, the copy rate), and by
+// latency when few states are in flight (one sequence: 6 us, 2 at the copy rate). A new entry needs its whole
+// old column (S'^T k), so a CTA holds all key rows of its value columns, 32 entries per thread: kRows rows of
 // kVec neighbouring columns, every load issued before the first is used. Where rows of the state start on
 // 16-byte boundaries the entries come to shared memory by cp.async (each thread reads back only what it
 // copied), so that they take no registers and six CTAs of 32 KB share an SM (603 us with the entries in
-// registers and two CTAs); single columns are held in registers. The two row sums meet once, by shuffles and through shared memory, and every thread forms its
-// own columns' u.
+// registers and two CTAs); single columns are held in registers. The two row sums meet once, by shuffles and
+// through shared memory, and every thread forms its own columns' u.
 #include "kda_delta.cuh"
 
 namespace kda {

@@ -71,6 +71,14 @@ def test_beside_longer_ones(lens, dtype):
     check(fin, f, bf + bg, "final")
 
 
+@pytest.mark.parametrize("N,H", [(3, 2), (40, 8)])
+@pytest.mark.parametrize("init", [True, False])
+def test_no_tokens_at_all(N, H, init):
+    c = make([0] * N, H=H, d_k=24, d_v=20, dtype=B16, init=init)
+    out, fin = run(c)
+    assert out.shape == (0, H, 20) and torch.equal(fin, c["init_state"] if init else torch.zeros_like(fin))
+
+
 def test_rows_behind_and_nan_stay():
     c = make([2, 1, 4] * 20, H=8, d_k=16, d_v=12, dtype=F32)
     T = c["q"].shape[0]
