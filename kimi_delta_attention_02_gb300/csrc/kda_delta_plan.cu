@@ -127,8 +127,35 @@ DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d
   const int64_t least = d_k <= 64 && d_v <= 64 ? (idle ? 88 : 44) : idle ? 44 : d_v <= 64 ? 24 : d_k <= 64 ? 16 : 6;
   if (!recurrent && !idle && total < 64 * int64_t(num_seqs)) p.few = d_k <= 64 && d_v <= 64 ? 12 : 5;
   p.tensor = in_bf16 && !recurrent && total >= least * num_seqs && int64_t(H) * d_v <= 1 << 25;  // (its output addresses)
-  if (!p.tensor) return p;
   const int pk = delta_up8(d_k), pv = delta_up8(d_v);
+  const auto room = [&](int64_t len) {  // for cuts of this length
+    const int64_t inner = total / len;
+    const size_t ends = align256(size_t(inner) * H * pk * pv * 4), maps = align256(size_t(inner) * H * pk * pk * 4);
+    if (p.bytes + ends + maps > workspace_bytes) return false;
+    p.seg_len = int32_t(len), p.inner = int32_t(inner);
+    p.maps = p.ends + ends;
+    p.bytes += ends + maps;
+    return true;
+  };
+  if (!p.tensor) {
+    // One long sequence in the token kernel, where the cuts save a fifth at least. ns a token by CTAs of 32 columns:
+    // with 38 of them, 76, 152 and more (T = 16384, fp32, heads of 128: 1 head 1545 us in one run, 572 in segments;
+    // 4 heads 1554, 1299; 16 heads 2377, 3808; 8 heads of 64 1557, 705).
+    if (!recurrent && num_seqs == 1) {
+      const auto ns = [&](int64_t ctas) -> int64_t {
+        return ctas <= kLinearSMs / 4 ? 95 : ctas <= kLinearSMs / 2 ? 145 : ctas * 135 / 100 > 236 ? ctas * 135 / 100 : 236;
+      };
+      const int64_t tv = (d_v + 31) / 32, tk = (pk + 31) / 32;
+      int64_t best = total * ns(tv * H) * 4 / 5, len = 0;
+      for (int64_t m = 3; m <= 64 && total >= m * 128; ++m) {
+        const int64_t each = (total + m - 1) / m;
+        const int64_t time = each * (ns(((m - 1) * tv + (m - 2) * tk) * H) + ns((m - 1) * tv * H)) + 30000 + 6000 * m;
+        if (time < best) best = time, len = each;
+      }
+      if (len > 0) room(len);
+    }
+    return p;
+  }
   if (pk != d_k || pv != d_v) {
     const size_t qk = pk != d_k ? align256(size_t(total) * H_k * pk * 2) : 0;
     p.pad_k = qk, p.pad_v = 2 * qk;
@@ -156,15 +183,7 @@ DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d
   // (room for three segments; and cuts that most sequences are too short for would only cost the order of the
   // others: 323 us instead of 280 for prompts of 4096 tokens and less on 32 heads, cut at 4672)
   if (len > 0 && total >= 3 * len - 63 * 3 && 8 * total >= len * num_seqs) {
-    const int64_t inner = total / len;
-    const size_t ends = align256(size_t(inner) * H * pk * pv * 4), maps = align256(size_t(inner) * H * pk * pk * 4);
-    if (p.bytes + ends + maps <= workspace_bytes) {
-      p.seg_len = int32_t(len);
-      p.inner = int32_t(inner);
-      p.maps = p.ends + ends;
-      p.bytes += ends + maps;
-      return p;
-    }
+    if (room(len)) return p;
   }
   const size_t list = align256(size_t(num_seqs) * 4);
   if (num_seqs > 1 && num_seqs <= 8192 && !idle && p.bytes + list <= workspace_bytes) {

@@ -49,17 +49,27 @@ struct Shared {
 };
 
 template <bool kInBF16, bool kOutBF16, int kLanes, int kRows, int kNC>
-__global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const DeltaArgs a) {
+__global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const DeltaArgs a, int pass) {
   constexpr int kDK = kLanes * kRows, kCols = kThr / kLanes * kNC;
   constexpr int kEach = kLanes / 8;  // lanes that end with the same one of a block's eight sums
   extern __shared__ __align__(16) uint8_t smem[];
   Shared<kDK, kCols> &sh = *reinterpret_cast<Shared<kDK, kCols> *>(smem);
   const int tid = threadIdx.x % kThr, lane = tid & 31, w = tid >> 5;
   const int rl = lane % kLanes, cl = lane / kLanes;
-  const int h = blockIdx.x % a.H, n = blockIdx.x / a.H, hk = h / (a.H / a.H_k);
+  const int h = blockIdx.x % a.H, hk = h / (a.H / a.H_k);
   const int col0 = blockIdx.y * kCols, cw = 32 / kLanes * kNC * w + kNC * cl, col = col0 + cw;
-  const int64_t t0 = a.cu[n], t1 = a.cu[n + 1];
-  if (t1 - t0 <= a.plan.few) return;  // done by the decode kernel
+  // the piece: a sequence, or a segment of one (kda_delta.cuh; as in the tensor-core kernel)
+  int index = blockIdx.x / a.H;
+  const bool map = index >= a.plan.inner + a.num_seqs;  // pass 1: the pieces once more, for their M
+  if (map) index -= a.plan.inner + a.num_seqs;
+  LinearSlot s;
+  if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, index, s)) return;
+  if ((pass == 3 || map) ? s.first : s.last && !s.first) return;
+  if (s.first && s.last && s.t1 - s.t0 <= a.plan.few) return;  // done by the decode kernel
+  const int64_t t0 = s.t0, t1 = s.t1;
+  const bool emit = s.first || pass == 3;
+  const int pk = delta_up8(a.d_k), pv = delta_up8(a.d_v), cols = map ? pk : a.d_v;  // (M has zeros behind d_k)
+  if (col0 >= cols) return;
 
   // global -> registers -> shared memory, a stage of kTok tokens at a time (as stored: a conversion here
   // would wait for the load). Rows of q and k that are whole 16-byte pieces take 16-byte loads: a load
@@ -100,7 +110,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const Delt
     for (int i = 0; i < kVals; ++i) {
       const int64_t tt = t + (i * kThr + tid) / kCols;
       const int c = col0 + tid % kCols;
-      rv[i] = i * kThr + tid < kTok * kCols && tt < t1 && c < a.d_v
+      rv[i] = i * kThr + tid < kTok * kCols && tt < t1 && c < a.d_v && !map
                   ? static_cast<const Elem *>(a.v)[(tt * a.H + h) * a.d_v + c] : Elem(0);
     }
     if (tid < kTok) {
@@ -195,13 +205,20 @@ __global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const Delt
 
   // the state: S[c][2 j + p] holds rows 4 kLanes j + 4 rl + 2 p, + 1 of column col + c
   float2 S[kNC][kRows / 2];
-  const int64_t at_state = (int64_t(n) * a.H + h) * a.d_k * a.d_v;
+  const int64_t at_state = (int64_t(s.n) * a.H + h) * a.d_k * a.d_v, place = delta_place(a, s);
+  float *ends = reinterpret_cast<float *>(a.workspace + a.plan.ends);
+  const float *from = a.init_state != nullptr ? a.init_state + at_state : nullptr;
+  float *to = a.final_state != nullptr ? a.final_state + at_state : nullptr;
+  int from_width = a.d_v, to_width = a.d_v;
+  if (!s.first) from = pass == 3 ? ends + ((place - 1) * a.H + h) * (int64_t(pk) * pv) : nullptr, from_width = pv;
+  if (map) to = reinterpret_cast<float *>(a.workspace + a.plan.maps) + (place * a.H + h) * (int64_t(pk) * pk), to_width = pk;
+  else if (!emit || !s.last) to = pass == 3 ? nullptr : ends + (place * a.H + h) * (int64_t(pk) * pv), to_width = pv;
 #pragma unroll
   for (int p = 0; p < kRows / 2; ++p) {
     const int r = 4 * kLanes * (p >> 1) + 4 * rl + 2 * (p & 1);
     auto at = [&](int row, int c) {
-      return a.init_state != nullptr && row < a.d_k && col + c < a.d_v
-                 ? a.init_state[at_state + int64_t(row) * a.d_v + col + c] : 0.f;
+      if (map) return row == col + c && row < a.d_k ? 1.f : 0.f;
+      return from != nullptr && row < a.d_k && col + c < a.d_v ? from[int64_t(row) * from_width + col + c] : 0.f;
     };
 #pragma unroll
     for (int c = 0; c < kNC; ++c) S[c][p] = make_float2(at(r, c), at(r + 1, c));
@@ -260,7 +277,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const Delt
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (i <= e) o = fmaf(B.qk[e][i], u[c][i], o);
-        if (rl >= 4 * kEach && rl % kEach == 0 && i0 + e < len && col + c < a.d_v)
+        if (emit && rl >= 4 * kEach && rl % kEach == 0 && i0 + e < len && col + c < a.d_v)
           store_elem<kOutBF16>(a.out, ((t + i0 + e) * a.H + h) * a.d_v + col + c, a.scale * o);
       }
       const float2 whole = make_float2(B.whole, B.whole);
@@ -290,22 +307,22 @@ __global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const Delt
     if (++b == 3) b = 0;
   }
 
-  if (a.final_state != nullptr) {
+  if (to != nullptr) {
 #pragma unroll
     for (int p = 0; p < kRows / 2; ++p) {
       const int r = 4 * kLanes * (p >> 1) + 4 * rl + 2 * (p & 1);
 #pragma unroll
       for (int c = 0; c < kNC; ++c) {
-        float *dst = a.final_state + at_state + int64_t(r) * a.d_v + col + c;
-        if (col + c < a.d_v && r < a.d_k) dst[0] = S[c][p].x;
-        if (col + c < a.d_v && r + 1 < a.d_k) dst[a.d_v] = S[c][p].y;
+        float *dst = to + int64_t(r) * to_width + col + c;
+        if (col + c < cols && r < a.d_k) dst[0] = S[c][p].x;
+        if (col + c < cols && r + 1 < a.d_k) dst[to_width] = S[c][p].y;
       }
     }
   }
 }
 
 template <bool kInBF16, bool kOutBF16, int kLanes, int kRows, int kNC>
-cudaError_t launch_one(const DeltaArgs &a, cudaStream_t stream) {
+cudaError_t launch_one(const DeltaArgs &a, int pass, int64_t pieces, int cols, cudaStream_t stream) {
   constexpr int kCols = kThr / kLanes * kNC;
   constexpr int smem = int(sizeof(Shared<kLanes * kRows, kCols>));
   const auto kern = delta_recurrent_kernel<kInBF16, kOutBF16, kLanes, kRows, kNC>;
@@ -321,8 +338,8 @@ cudaError_t launch_one(const DeltaArgs &a, cudaStream_t stream) {
       granted.fetch_or(bit, std::memory_order_release);
     }
   }
-  const dim3 grid(unsigned(int64_t(a.num_seqs) * a.H), unsigned((a.d_v + kCols - 1) / kCols));
-  kern<<<grid, 2 * kThr, smem, stream>>>(a);
+  const dim3 grid(unsigned(pieces * a.H), unsigned((cols + kCols - 1) / kCols));
+  kern<<<grid, 2 * kThr, smem, stream>>>(a, pass);
   return cudaGetLastError();
 }
 
@@ -334,18 +351,29 @@ cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool in_bf16, bool out_bf
   // as long again, and one SM's two CTAs twice as long. 1000 tokens in fp32, us by 4 / 16 / 32 columns per
   // CTA: 8 heads of 128 134 / 144 / 205, 16 heads 261 / 146 / 205, 28 heads 388 / 231 / 205, 48 heads 756 / 455 / 315,
   // 96 heads 1432 / 682 / 497; 48 heads of 64 383 / 152 / 122.
-  const int64_t chains = int64_t(a.num_seqs) * a.H;
-  const auto ctas = [&](int cols) { return chains * ((a.d_v + cols - 1) / cols); };
-  const auto run = [&](auto in, auto out) {
-    constexpr bool ib = decltype(in)::value, ob = decltype(out)::value;
-    if (ctas(4) <= 2 * kLinearSMs) return launch_one<ib, ob, 32, 4, 1>(a, stream);
-    const bool wide = a.d_k > 64, two = ctas(16) > kLinearSMs;
-    if (wide) return two ? launch_one<ib, ob, 8, 16, 2>(a, stream) : launch_one<ib, ob, 8, 16, 1>(a, stream);
-    return two ? launch_one<ib, ob, 8, 8, 2>(a, stream) : launch_one<ib, ob, 8, 8, 1>(a, stream);
+  const auto pass = [&](int which) {
+    const bool cut = a.plan.seg_len != 0;
+    const int64_t pieces = int64_t(a.num_seqs) + a.plan.inner + (cut && which == 1 ? a.plan.inner : 0);
+    const int cols = cut && which == 1 && a.d_k > a.d_v ? delta_up8(a.d_k) : a.d_v;
+    const auto ctas = [&](int width) { return pieces * a.H * ((cols + width - 1) / width); };
+    const auto run = [&](auto in, auto out) {
+      constexpr bool ib = decltype(in)::value, ob = decltype(out)::value;
+      if (ctas(4) <= 2 * kLinearSMs) return launch_one<ib, ob, 32, 4, 1>(a, which, pieces, cols, stream);
+      const bool wide = a.d_k > 64, two = ctas(16) > kLinearSMs;
+      if (wide)
+        return two ? launch_one<ib, ob, 8, 16, 2>(a, which, pieces, cols, stream)
+                   : launch_one<ib, ob, 8, 16, 1>(a, which, pieces, cols, stream);
+      return two ? launch_one<ib, ob, 8, 8, 2>(a, which, pieces, cols, stream)
+                 : launch_one<ib, ob, 8, 8, 1>(a, which, pieces, cols, stream);
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    return in_bf16 ? (out_bf16 ? run(yes, yes) : run(yes, no)) : (out_bf16 ? run(no, yes) : run(no, no));
   };
-  const std::true_type yes;
-  const std::false_type no;
-  return in_bf16 ? (out_bf16 ? run(yes, yes) : run(yes, no)) : (out_bf16 ? run(no, yes) : run(no, no));
+  cudaError_t e = pass(1);
+  if (e != cudaSuccess || a.plan.seg_len == 0) return e;
+  e = launch_delta_chain(a, stream);
+  return e == cudaSuccess ? pass(3) : e;
 }
 
 }  // namespace kda

@@ -114,8 +114,14 @@ def test_norm_rotate_head_counts():
 def test_workspace_sizes():
     size = B.delta_workspace_size
     f32, bf16 = torch.float32, torch.bfloat16
-    for T in (1, 63, 5000, 100000):  # the token kernel
+    for T in (1, 63, 380):  # the token kernel
         assert size(T, 1, 8, dtype=f32) == size(T, 1, 8, recurrent=True) == size(T, 1, 8, dtype=f32, d_k=68) == 0
+    assert size(100000, 1, 8, recurrent=True) == size(100000, 1, 8, d_k=68, recurrent=True) == size(100000, 2, 8, dtype=f32) == 0
+    # .. which cuts one long sequence too, where SMs are idle (in its workspace sizes are padded to multiples of 8)
+    n = size(16384, 1, 4, dtype=f32)
+    assert n > 0 and n % (4 * 128 * 128 * 8) == 0 and size(4096, 1, 96, dtype=f32) == 0
+    n = size(16384, 1, 8, dtype=f32, d_k=68, d_v=5)
+    assert n > 0 and n % 256 == 0
     # copies of q and k, of v, or of all, with head sizes padded to multiples of 8; segments behind them
     up = lambda n: (n + 255) // 256 * 256  # noqa: E731
     assert size(100, 1, 8, d_k=68, H_k=2) == 2 * up(100 * 2 * 72 * 2) and size(100, 1, 8, d_v=5) == up(100 * 8 * 8 * 2)

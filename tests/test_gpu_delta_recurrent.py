@@ -123,3 +123,34 @@ def test_rows_behind_the_last_sequence_stay():
     check(out[:50], o, bo, "out")
     assert (out[50:] == 7.0).all()
     assert not np.isnan(f64(out)).any()
+
+
+@pytest.mark.parametrize("T,d_k,d_v,H,H_k", [(3000, 128, 128, 2, 1), (3500, 100, 72, 2, 1), (1500, 33, 7, 2, 2), (2111, 64, 65, 1, 1),
+                                             (4100, 5, 127, 1, 1), (1900, 128, 128, 1, 1)])
+@pytest.mark.parametrize("dtype", [F32, B16])
+def test_one_long_sequence_in_segments(T, d_k, d_v, H, H_k, dtype):
+    """Cut into segments that are joined by their transition maps, with a workspace full of NaN; without one, from
+    end to end. Errors are roundings of 2^-24 with random signs, some four a token, of which a state
+    remembers d_k / beta tokens, 256 or so: 4 sqrt(256) 2^-24 = 4e-6 in the 2-norm, and as much again from the
+    maps; bf16 prompts are on the tensor cores, where ten roundings of pairs make it 2e-5."""
+    c = make([T], H=H, H_k=H_k, d_k=d_k, d_v=d_v, dtype=dtype, decay=0.003, seed=T)
+    assert binding.delta_workspace_size(T, 1, H, d_k, d_v, F32, F32, H_k=H_k) > 0  # (bf16: cut from 1536 tokens on)
+    o, f = reference(c)
+    wide = {x: torch.cat([c[x], torch.full_like(c[x][:20], float("nan"))]) for x in ("q", "k", "v", "log_decay", "beta")}
+    n = binding.delta_workspace_size(T + 20, 1, H, d_k, d_v, dtype, F32, H_k=H_k)
+    ws = torch.full((n // 4,), float("nan"), device="cuda").view(torch.uint8) if n else None
+    out = torch.full((T + 20, H, d_v), 7.0, device="cuda")
+    _, fin = run({**c, **wide}, out=out, workspace=ws)
+    assert (out[T:] == 7).all()
+    tolerance = 1e-5 if dtype == F32 else 2e-5
+    for got, want in ((out[:T], o), (fin, f)):
+        err = np.linalg.norm(f64(got) - want) / np.linalg.norm(want)
+        assert err < tolerance, err
+    if dtype == F32:
+        out, fin = run(c, workspace=None)
+        again, end = run(c, recurrent=True)
+        assert torch.equal(out, again) and torch.equal(fin, end)
+        state = c["init_state"].clone()
+        a, b = run({**c, "init_state": state}, final_state=state)
+        x, y = run(c)
+        assert torch.equal(a, x) and torch.equal(b, y) and not torch.equal(y, end)
