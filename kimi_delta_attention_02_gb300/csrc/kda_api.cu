@@ -595,7 +595,8 @@ size_t kda_delta_prefill_workspace_size(int64_t total_tokens, int32_t num_seqs, 
                                         int32_t force_recurrent) {
   if (check_linear_sizes(total_tokens, num_seqs, H, H_k, d_k, d_v, 1, in_dtype, out_dtype) != KDA_OK) return 0;
   if (total_tokens == 0 || num_seqs == 0) return 0;
-  return delta_plan(total_tokens, num_seqs, H, H_k, d_k, d_v, in_dtype == KDA_BF16, force_recurrent != 0, SIZE_MAX)
+  return delta_plan(total_tokens, num_seqs, H, H_k, d_k, d_v, in_dtype == KDA_BF16, out_dtype == KDA_BF16,
+                    force_recurrent != 0, SIZE_MAX)
       .bytes;
 }
 
@@ -633,7 +634,8 @@ kda_status kda_delta_prefill(const kda_delta_prefill_params *p, void *stream) {
   a.num_seqs = p->num_seqs, a.H = p->H, a.H_k = p->H_k, a.d_k = p->d_k, a.d_v = p->d_v;
   a.per_token = p->decay_per_token, a.total = T, a.scale = p->scale;
   const bool in_bf16 = p->in_dtype == KDA_BF16, out_bf16 = p->out_dtype == KDA_BF16;
-  a.plan = delta_plan(T, p->num_seqs, p->H, p->H_k, p->d_k, p->d_v, in_bf16, p->force_recurrent != 0, p->workspace_bytes);
+  a.plan = delta_plan(T, p->num_seqs, p->H, p->H_k, p->d_k, p->d_v, in_bf16, out_bf16, p->force_recurrent != 0,
+                      p->workspace_bytes);
   a.workspace = static_cast<uint8_t *>(p->workspace);
   const cudaStream_t cs = static_cast<cudaStream_t>(stream);
   cudaError_t err = a.plan.few >= 0 ? launch_delta_short(a, in_bf16, out_bf16, cs) : cudaSuccess;

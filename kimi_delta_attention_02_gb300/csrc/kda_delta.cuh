@@ -52,8 +52,8 @@ __device__ __forceinline__ int64_t delta_place(const DeltaArgs &a, const LinearS
 __host__ __device__ constexpr int delta_up8(int d) { return (d + 7) & ~7; }
 
 // The plan for a call that has this much workspace (SIZE_MAX: what it would like to have).
-DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool recurrent,
-                     size_t workspace_bytes);
+DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool out_bf16,
+                     bool recurrent, size_t workspace_bytes);
 cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream);
 cudaError_t launch_delta_short(const DeltaArgs &a, bool in_bf16, bool out_bf16, cudaStream_t stream);
 cudaError_t launch_delta_chunked(const DeltaArgs &a, bool out_bf16, cudaStream_t stream);

@@ -108,6 +108,11 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, cudaStream_t stream) {
 // copies of q, k and v in the workspace, or without one in the token kernel (4096 tokens, 96 heads of 100: 345 us
 // by copies, 2099 by the token kernel; 32 heads of 68: 209, 835).
 //
+// Few key channels stay in the token kernel, for the precision: the keys of a chunk are far from orthogonal, so
+// that T' V and T'' X are larger than their sum, and their pairs' roundings reach 1.1e-5 of fp32 outputs and 1.0e-5 of
+// states in the 2-norm (d_k = 5 and 6; from 9 on 8.3e-6 of states, from 17 on 8.0e-6 of outputs; 3e-7 by the token
+// kernel). 4096 tokens, 96 heads of 16 x 128: 1259 us there, 240 here.
+//
 // The shortest sequences go to the decode kernel, which holds no more than a state and is bound by its bytes, where
 // there are more chains than SMs and the mean length says that there may be some: those of up to `few` tokens. us
 // by the token kernel / that one at 1, 4, 8 and 16 tokens, 128 sequences of 64 heads: 128 x 128 754/219, 764/468,
@@ -120,13 +125,14 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, cudaStream_t stream) {
 // 65536, 16 heads: m = 10, 1335 us; m = 6: 1378 us; not cut: some 3100). Of several the lengths are not known
 // here, and cuts lie so far apart that pass 1 fills the SMs at most twice. Sequences in more chains than SMs run
 // longest first.
-DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool recurrent,
-                     size_t workspace_bytes) {
+DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool out_bf16,
+                     bool recurrent, size_t workspace_bytes) {
   DeltaPlan p;
   const bool idle = int64_t(num_seqs) * H <= kLinearSMs;
   const int64_t least = d_k <= 64 && d_v <= 64 ? (idle ? 88 : 44) : idle ? 44 : d_v <= 64 ? 24 : d_k <= 64 ? 16 : 6;
   if (!recurrent && !idle && total < 64 * int64_t(num_seqs)) p.few = d_k <= 64 && d_v <= 64 ? 12 : 5;
-  p.tensor = in_bf16 && !recurrent && total >= least * num_seqs && int64_t(H) * d_v <= 1 << 25;  // (its output addresses)
+  p.tensor = in_bf16 && !recurrent && d_k > (out_bf16 ? 8 : 16) && total >= least * num_seqs &&
+             int64_t(H) * d_v <= 1 << 25;  // (its output addresses)
   const int pk = delta_up8(d_k), pv = delta_up8(d_v);
   const auto room = [&](int64_t len) {  // for cuts of this length
     const int64_t inner = total / len;

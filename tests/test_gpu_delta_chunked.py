@@ -55,12 +55,12 @@ def _on_tensor_cores(c, out, fin, **kw):
 
 
 @pytest.mark.parametrize("out_dtype", [B16, F32])
-@pytest.mark.parametrize("d_k,d_v", [(100, 72), (72, 100), (33, 40), (127, 127), (65, 1), (1, 128), (3, 3), (128, 61)])
+@pytest.mark.parametrize("d_k,d_v", [(100, 72), (72, 100), (33, 40), (127, 127), (65, 1), (1, 128), (3, 3), (128, 61), (17, 17)])
 def test_padded_head_sizes(d_k, d_v, out_dtype):
     c = make([150, 0, 140, 1], H=6, H_k=2, d_k=d_k, d_v=d_v, seed=d_k + d_v)
     c = c if d_k > 64 or d_v > 64 else make([150, 140], H=6, H_k=2, d_k=d_k, d_v=d_v, seed=d_k + d_v)
     out, fin = _check(c, scale=0.25, out_dtype=out_dtype)
-    assert d_k == 1 or _on_tensor_cores(c, out, fin, scale=0.25)
+    assert d_k <= (8 if out_dtype == B16 else 16) or _on_tensor_cores(c, out, fin, scale=0.25)
     o, f = run(c, scale=0.25, out_dtype=out_dtype, workspace=None)  # no room for the copies
     assert not _on_tensor_cores(c, o, f, scale=0.25)
 
@@ -79,6 +79,24 @@ def test_padded_segments_and_rows_behind(d_k, d_v):
         o, fin = run({**c, **wide}, out=out, workspace=ws)
         assert (out[2600:] == 7).all()
         _check_against(c, out[:2600].contiguous(), fin)
+
+
+@pytest.mark.parametrize("d_k", [5, 8, 9, 16, 17, 24])
+@pytest.mark.parametrize("d_v", [16, 128])
+def test_few_key_channels_stay_exact(d_k, d_v):
+    """Keys that are far from orthogonal make the terms of a chunk's U larger than U itself. Up to 16 channels
+    the token kernel takes them (2^-24 a rounding, under 1e-6 in the 2-norm as elsewhere); from 17 on the terms
+    are at most some 1 + 64 / d_k times as large in power, and the ten pairs' 2^-18 / sqrt(3), 7e-6 together, stay
+    below 1e-5. With a bf16 output the state alone is fp32, and 9 channels are enough."""
+    c = make([270, 497], H=4, H_k=2, d_k=d_k, d_v=d_v, decay=0.02, seed=d_k)
+    out, fin = run(c, scale=4 * d_k ** -0.5)
+    o, f = reference(c, 4 * d_k ** -0.5)
+    for got, want in ((out, o), (fin, f)):
+        err = np.linalg.norm(f64(got) - want) / np.linalg.norm(want)
+        assert err < (1e-6 if d_k <= 16 else 1e-5), err
+    _, fin = run(c, scale=4 * d_k ** -0.5, out_dtype=B16)
+    err = np.linalg.norm(f64(fin) - f) / np.linalg.norm(f)
+    assert err < (1e-6 if d_k <= 8 else 1e-5), err
 
 
 @pytest.mark.parametrize("out_dtype", [B16, F32])
