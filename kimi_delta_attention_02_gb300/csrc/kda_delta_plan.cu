@@ -145,8 +145,8 @@ DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d
   };
   if (!p.tensor) {
     // One long sequence in the token kernel, where the cuts save a fifth at least. ns a token by CTAs of 32 columns:
-    // with 38 of them, 76, 152 and more (T = 16384, fp32, heads of 128: 1 head 1545 us in one run, 572 in segments;
-    // 4 heads 1554, 1299; 16 heads 2377, 3808; 8 heads of 64 1557, 705).
+    // with 38 of them, 76, 152 and more, in segments (a tenth less in one run). T = 16384, fp32, heads of 128: 1 head
+    // 1405 us in one run, 572 in segments; 4 heads 1405, 1301; 16 heads 2245, 3808; 8 heads of 64 1400, 712.
     if (!recurrent && num_seqs == 1) {
       const auto ns = [&](int64_t ctas) -> int64_t {
         return ctas <= kLinearSMs / 4 ? 95 : ctas <= kLinearSMs / 2 ? 145 : ctas * 135 / 100 > 236 ? ctas * 135 / 100 : 236;

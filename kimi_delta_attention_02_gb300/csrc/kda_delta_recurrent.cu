@@ -48,7 +48,9 @@ struct Shared {
   float g[3][kTok], beta[3][kTok];
 };
 
-template <bool kInBF16, bool kOutBF16, int kLanes, int kRows, int kNC>
+// kCut: pieces of a cut sequence, in passes 1 and 3 (in one kernel with the others, its addresses cost them
+// spills: 4096 tokens, 96 heads of 128 2362 us instead of 1963).
+template <bool kInBF16, bool kOutBF16, int kLanes, int kRows, int kNC, bool kCut>
 __global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const DeltaArgs a, int pass) {
   constexpr int kDK = kLanes * kRows, kCols = kThr / kLanes * kNC;
   constexpr int kEach = kLanes / 8;  // lanes that end with the same one of a block's eight sums
@@ -58,18 +60,23 @@ __global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const Delt
   const int rl = lane % kLanes, cl = lane / kLanes;
   const int h = blockIdx.x % a.H, hk = h / (a.H / a.H_k);
   const int col0 = blockIdx.y * kCols, cw = 32 / kLanes * kNC * w + kNC * cl, col = col0 + cw;
-  // the piece: a sequence, or a segment of one (kda_delta.cuh; as in the tensor-core kernel)
   int index = blockIdx.x / a.H;
-  const bool map = index >= a.plan.inner + a.num_seqs;  // pass 1: the pieces once more, for their M
-  if (map) index -= a.plan.inner + a.num_seqs;
   LinearSlot s;
-  if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, index, s)) return;
-  if ((pass == 3 || map) ? s.first : s.last && !s.first) return;
-  if (s.first && s.last && s.t1 - s.t0 <= a.plan.few) return;  // done by the decode kernel
+  bool map = false, emit = true;
+  if constexpr (kCut) {  // as in the tensor-core kernel
+    map = index >= a.plan.inner + a.num_seqs;  // pass 1: the pieces once more, for their M
+    if (map) index -= a.plan.inner + a.num_seqs;
+    if (!linear_slot(a.cu, a.num_seqs, a.plan.seg_len, a.plan.inner, index, s)) return;
+    if ((pass == 3 || map) ? s.first : s.last && !s.first) return;
+    emit = s.first || pass == 3;
+  } else {
+    s.n = index, s.t0 = a.cu[index], s.t1 = a.cu[index + 1];
+    if (s.t1 - s.t0 <= a.plan.few) return;  // done by the decode kernel
+  }
   const int64_t t0 = s.t0, t1 = s.t1;
-  const bool emit = s.first || pass == 3;
-  const int pk = delta_up8(a.d_k), pv = delta_up8(a.d_v), cols = map ? pk : a.d_v;  // (M has zeros behind d_k)
-  if (col0 >= cols) return;
+  const int pk = delta_up8(a.d_k), cols = map ? pk : a.d_v;  // (M has zeros behind d_k)
+  const int v_cols = map ? 0 : a.d_v, out_cols = emit ? a.d_v : 0;
+  if (kCut && col0 >= cols) return;
 
   // global -> registers -> shared memory, a stage of kTok tokens at a time (as stored: a conversion here
   // would wait for the load). Rows of q and k that are whole 16-byte pieces take 16-byte loads: a load
@@ -110,7 +117,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const Delt
     for (int i = 0; i < kVals; ++i) {
       const int64_t tt = t + (i * kThr + tid) / kCols;
       const int c = col0 + tid % kCols;
-      rv[i] = i * kThr + tid < kTok * kCols && tt < t1 && c < a.d_v && !map
+      rv[i] = i * kThr + tid < kTok * kCols && tt < t1 && c < v_cols
                   ? static_cast<const Elem *>(a.v)[(tt * a.H + h) * a.d_v + c] : Elem(0);
     }
     if (tid < kTok) {
@@ -205,14 +212,18 @@ __global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const Delt
 
   // the state: S[c][2 j + p] holds rows 4 kLanes j + 4 rl + 2 p, + 1 of column col + c
   float2 S[kNC][kRows / 2];
-  const int64_t at_state = (int64_t(s.n) * a.H + h) * a.d_k * a.d_v, place = delta_place(a, s);
-  float *ends = reinterpret_cast<float *>(a.workspace + a.plan.ends);
+  const int64_t at_state = (int64_t(s.n) * a.H + h) * a.d_k * a.d_v;
   const float *from = a.init_state != nullptr ? a.init_state + at_state : nullptr;
   float *to = a.final_state != nullptr ? a.final_state + at_state : nullptr;
   int from_width = a.d_v, to_width = a.d_v;
-  if (!s.first) from = pass == 3 ? ends + ((place - 1) * a.H + h) * (int64_t(pk) * pv) : nullptr, from_width = pv;
-  if (map) to = reinterpret_cast<float *>(a.workspace + a.plan.maps) + (place * a.H + h) * (int64_t(pk) * pk), to_width = pk;
-  else if (!emit || !s.last) to = pass == 3 ? nullptr : ends + (place * a.H + h) * (int64_t(pk) * pv), to_width = pv;
+  if constexpr (kCut) {
+    const int pv = delta_up8(a.d_v);
+    const int64_t place = delta_place(a, s), each = int64_t(pk) * pv;
+    float *ends = reinterpret_cast<float *>(a.workspace + a.plan.ends);
+    if (!s.first) from = pass == 3 ? ends + ((place - 1) * a.H + h) * each : nullptr, from_width = pv;
+    if (map) to = reinterpret_cast<float *>(a.workspace + a.plan.maps) + (place * a.H + h) * (int64_t(pk) * pk), to_width = pk;
+    else if (!emit || !s.last) to = pass == 3 ? nullptr : ends + (place * a.H + h) * each, to_width = pv;
+  }
 #pragma unroll
   for (int p = 0; p < kRows / 2; ++p) {
     const int r = 4 * kLanes * (p >> 1) + 4 * rl + 2 * (p & 1);
@@ -277,7 +288,7 @@ __global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const Delt
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (i <= e) o = fmaf(B.qk[e][i], u[c][i], o);
-        if (emit && rl >= 4 * kEach && rl % kEach == 0 && i0 + e < len && col + c < a.d_v)
+        if (rl >= 4 * kEach && rl % kEach == 0 && i0 + e < len && col + c < out_cols)
           store_elem<kOutBF16>(a.out, ((t + i0 + e) * a.H + h) * a.d_v + col + c, a.scale * o);
       }
       const float2 whole = make_float2(B.whole, B.whole);
@@ -321,11 +332,11 @@ __global__ void __launch_bounds__(2 * kThr, 2) delta_recurrent_kernel(const Delt
   }
 }
 
-template <bool kInBF16, bool kOutBF16, int kLanes, int kRows, int kNC>
-cudaError_t launch_one(const DeltaArgs &a, int pass, int64_t pieces, int cols, cudaStream_t stream) {
+template <bool kInBF16, bool kOutBF16, int kLanes, int kRows, int kNC, bool kCut>
+cudaError_t launch_one_of(const DeltaArgs &a, int pass, int64_t pieces, int cols, cudaStream_t stream) {
   constexpr int kCols = kThr / kLanes * kNC;
   constexpr int smem = int(sizeof(Shared<kLanes * kRows, kCols>));
-  const auto kern = delta_recurrent_kernel<kInBF16, kOutBF16, kLanes, kRows, kNC>;
+  const auto kern = delta_recurrent_kernel<kInBF16, kOutBF16, kLanes, kRows, kNC, kCut>;
   if (smem > 49152) {  // granted once per device (bit d for device d; past 63 at every launch)
     static std::atomic<uint64_t> granted;
     int dev = 0;
@@ -341,6 +352,12 @@ cudaError_t launch_one(const DeltaArgs &a, int pass, int64_t pieces, int cols, c
   const dim3 grid(unsigned(pieces * a.H), unsigned((cols + kCols - 1) / kCols));
   kern<<<grid, 2 * kThr, smem, stream>>>(a, pass);
   return cudaGetLastError();
+}
+
+template <bool kInBF16, bool kOutBF16, int kLanes, int kRows, int kNC>
+cudaError_t launch_one(const DeltaArgs &a, int pass, int64_t pieces, int cols, cudaStream_t stream) {
+  return a.plan.seg_len != 0 ? launch_one_of<kInBF16, kOutBF16, kLanes, kRows, kNC, true>(a, pass, pieces, cols, stream)
+                             : launch_one_of<kInBF16, kOutBF16, kLanes, kRows, kNC, false>(a, pass, pieces, cols, stream);
 }
 
 }  // namespace
