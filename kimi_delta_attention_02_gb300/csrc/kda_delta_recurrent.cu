@@ -371,7 +371,9 @@ cudaError_t launch_delta_recurrent(const DeltaArgs &a, bool in_bf16, bool out_bf
   const auto pass = [&](int which) {
     const bool cut = a.plan.seg_len != 0;
     const int64_t pieces = int64_t(a.num_seqs) + a.plan.inner + (cut && which == 1 ? a.plan.inner : 0);
-    const int cols = cut && which == 1 && a.d_k > a.d_v ? delta_up8(a.d_k) : a.d_v;
+    // (pass 1 writes all of M's columns, those behind d_k too: pass 2 multiplies them by zeros, and what the workspace
+    // held there may be a NaN)
+    const int pk = delta_up8(a.d_k), cols = cut && which == 1 && pk > a.d_v ? pk : a.d_v;
     const auto ctas = [&](int width) { return pieces * a.H * ((cols + width - 1) / width); };
     const auto run = [&](auto in, auto out) {
       constexpr bool ib = decltype(in)::value, ob = decltype(out)::value;
