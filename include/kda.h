@@ -525,13 +525,12 @@ kda_status kda_block_norm(const kda_block_norm_params *params, void *stream);
  * bf16 output; few key channels would lose precision in pairs), their sequences are short (fewer
  * than 6 to 88 tokens on average, by head sizes and the number of sequences and heads; empty
  * sequences count) or H d_v is above 2^25. Its products read the state and what is formed for it
- * as pairs of bf16 (2^-17), so that final states and fp32 outputs are off by some 1e-5 of
- * themselves (in the 2-norm); the masked products q.k are single bf16 when the output is bf16. A
- * log_decay below -88 counts as -88. An infinity or NaN in a channel of v reaches that value
- * channel of every output of its chunk in that (sequence, head), and what follows; one in k, beta
- * or log_decay every channel of the same; one in q its own token's output. fp32 inputs, short
- * sequences, and sequences of up to 5 or 12 tokens beside many others run in fp32 token by token,
- * where they reach only what depends on them.
+ * as pairs of bf16 (2^-17), so that final states and outputs (a bf16 one before it is rounded) are off
+ * by some 1e-5 of themselves (in the 2-norm). A log_decay below -88 counts as -88. An infinity or NaN
+ * in a channel of v reaches that value channel of every output of its chunk in that (sequence, head),
+ * and what follows; one in k, beta or log_decay every channel of the same; one in q its own token's
+ * output. fp32 inputs, short sequences, and sequences of up to 5 or 12 tokens beside many others run in
+ * fp32 token by token, where they reach only what depends on them.
  *
  * Results are accumulated in fp32 and states are fp32.
  */

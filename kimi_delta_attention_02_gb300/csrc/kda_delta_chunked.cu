@@ -15,12 +15,12 @@
 //
 // Roundings. The operands of what reaches the state (S, X, T', T'', U') are pairs of bf16, hi + lo, each
 // pair off by at most 2^-17 of the value, and the products take hi hi + hi lo + lo hi (K, Q and V are bf16
-// as given). The read-out takes S and U as the same kind of pairs; its P is a single bf16 for a bf16 output
-// (2^-9, the size of the output's own rounding), a pair for an fp32 one. A is formed in fp32. Its inverse
+// as given). The read-out takes S, U and P as the same kind of pairs, for bf16 outputs too: where keys are alike, P U
+// is a small sum of large terms, and a single bf16 P (2^-9) put outputs off by up to 0.0065. A is formed in fp32. Its inverse
 // starts from blocks of 8 by forward substitution in fp32, joined to 16 in fp32, and to 32 and 64 by
 // products of blocks in pairs of tf32 (2^-20) on the tensor cores. No power of A is formed, which with keys
-// alike would grow like binomials. At T = 4096, 96 heads of 128: bf16 output off by 0.0023 in the 2-norm (its
-// rounding alone: 0.0017), fp32 output by 7e-6, state by 5e-6.
+// alike would grow like binomials. At T = 4096, 96 heads of 128: bf16 output off by 0.0017 in the 2-norm, its
+// own rounding, fp32 output by 7e-6, state by 5e-6.
 //
 // Decays. G is summed in fp64 and kept as a pair of floats, so that no entry of D loses to long sums.
 // A log-decay below -88 counts as -88 (2^-127), as in linear attention.
@@ -47,9 +47,15 @@ namespace {
 
 constexpr int kC = 64;             // tokens per chunk
 constexpr int kThreads = 768;
-constexpr int kKQ = 3, kTabs = 4;          // buffers
+constexpr int kKQ = 3, kP = 3, kTabs = 4;  // buffers (with two of P, A and P wait for them: 291 us instead of 263)
 constexpr uint32_t kTileKQ = 32768;        // 64 rows of K, then 64 of Q, x 128 channels, two 64-channel blocks
-constexpr uint32_t kTileV = 16384, kTileT = 8192;  // 64 x 64 bf16
+constexpr uint32_t kBlockV = 8192;         // 64 rows of V x 64 channels: two buffers of one block, or one of two
+constexpr uint32_t kTileT = 8192;          // 64 x 64 bf16
+// P's pair in 96 rows. It is lower triangular, so lo takes the place of what would be zero in hi, 32 x 32 at a time:
+//     rows  0 .. 31: hi of P's rows  0 .. 31, columns 0 .. 31 | lo of the same
+//     rows 32 .. 63: hi of P's rows 32 .. 63, columns 0 .. 31 | columns 32 .. 63
+//     rows 64 .. 95: lo of the same
+constexpr uint32_t kTileP = 12288;
 constexpr int kStrideA = 68;       // floats per row of A
 constexpr uint32_t kProbes = 2000000;
 constexpr double kLog2e = 1.4426950408889634, kLn2 = 0.6931471805599453, kMinLog2 = -127.;
@@ -78,15 +84,11 @@ struct Control {
   volatile uint32_t gave_up;
 };
 
-template <bool kOutBF16>
-struct Cfg {
-  static constexpr bool kPair = !kOutBF16;  // P as a pair
-  static constexpr int kV = kPair ? 1 : 2, kP = kPair ? 2 : 3;  // buffers
-  static constexpr uint32_t kTileP = (kPair ? 2 : 1) * kTileT;
-  static constexpr uint32_t oV = kKQ * kTileKQ, oT = oV + kV * kTileV, oP = oT + 4 * kTileT,
-                            oA = oP + kP * kTileP, oTab = oA + 2 * kC * kStrideA * 4,
-                            oCtl = oTab + kTabs * sizeof(Table), bytes = oCtl + sizeof(Control);
-};
+// in shared memory
+constexpr uint32_t kAtV = kKQ * kTileKQ, kAtT = kAtV + 2 * kBlockV, kAtP = kAtT + 4 * kTileT, kAtA = kAtP + kP * kTileP,
+                   kAtTab = kAtA + 2 * kC * kStrideA * 4, kAtCtl = kAtTab + kTabs * sizeof(Table),
+                   kBytes = kAtCtl + sizeof(Control);
+static_assert(kBytes <= 232448, "shared memory of one CTA");
 
 // a run of tokens on one CTA
 struct Run {
@@ -179,12 +181,9 @@ template <bool kOutBF16>
 __global__ void __launch_bounds__(kThreads, 1)
     delta_chunked_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                          const __grid_constant__ CUtensorMap mv, const DeltaArgs a, int pass, uint32_t *err_word) {
-  using F = Cfg<kOutBF16>;
-  constexpr bool kPair = F::kPair;
-  constexpr int kV = F::kV, kP = F::kP;
   extern __shared__ __align__(1024) uint8_t smem[];
-  Table *tab = reinterpret_cast<Table *>(smem + F::oTab);
-  Control *ctl = reinterpret_cast<Control *>(smem + F::oCtl);
+  Table *tab = reinterpret_cast<Table *>(smem + kAtTab);
+  Control *ctl = reinterpret_cast<Control *>(smem + kAtCtl);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % a.H, hk = h / (a.H / a.H_k);
 
@@ -228,10 +227,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int chunks = run.chunks, len = run.len;
   const int nk = (a.d_k + 15) >> 4;       // steps of 16 key channels
   const int kb = (a.d_k + 63) >> 6, vb = (a.d_v + 63) >> 6;  // blocks of 64 channels
+  const int v_last = vb == 1 ? 1 : 0;     // V's buffers less one
 
   if (tid == 0) {
     for (int i = 0; i < kKQ; ++i) mbar_init(&ctl->kq_full[i], 1), mbar_init(&ctl->kq_free[i], 1);
-    for (int i = 0; i < kV; ++i) mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_free[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ctl->v_full[i], 1), mbar_init(&ctl->v_free[i], 1);
     for (int i = 0; i < kP; ++i) mbar_init(&ctl->p_free[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&ctl->gram_done[i], 1), mbar_init(&ctl->t_free[i], 1);
     for (int i = 0; i < kTabs; ++i) mbar_init(&ctl->tab_full[i], 1), mbar_init(&ctl->tab_free[i], run.emit ? 16 : 12);
@@ -282,18 +282,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (++ks == kKQ) ks = 0, ks_turn ^= 1;
           if (run.identity) continue;
           if (!wait(ctl->v_free[vs_], vs_turn)) break;
-          mbar_arrive_expect_tx(&ctl->v_full[vs_], vb * 8192);
+          mbar_arrive_expect_tx(&ctl->v_full[vs_], vb * kBlockV);
 #pragma unroll 1
           for (int b = 0; b < vb; ++b)
-            tma_load_3d(smem + F::oV + vs_ * kTileV + b * 8192, &mv, &ctl->v_full[vs_], 64 * b, h, t);
+            tma_load_3d(smem + kAtV + (vs_ + b) * kBlockV, &mv, &ctl->v_full[vs_], 64 * b, h, t);
           ++vs;
-          if (++vs_ == kV) vs_ = 0, vs_turn ^= 1;
+          if (vs_ == uint32_t(v_last)) vs_ = 0, vs_turn ^= 1;
+          else ++vs_;
         }
         // every load issued has landed before the CTA may end
 #pragma unroll 1
         for (int i = kq > kKQ ? kq - kKQ : 0; i < kq; ++i) wait(ctl->kq_full[i % kKQ], i / kKQ);
 #pragma unroll 1
-        for (int i = vs > kV ? vs - kV : 0; i < vs; ++i) wait(ctl->v_full[i % kV], i / kV);
+        for (int i = vs > v_last ? vs - v_last - 1 : 0; i < vs; ++i) wait(ctl->v_full[i & v_last], i >> v_last);
       }
     } else if (warp == 1) {
       // ---- the chain: X = K S, U = T' V + T'' X, K^T U'
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // forty of them
         const uint32_t none = uint32_t(n) >> 28;
         const uint32_t tS = tmem + none, tX = tS + 128, tU = tS + 192;
-        const uint64_t dT = desc_k(base + none + F::oT), dTW = dT + (2 * kTileT >> 4);  // T', then T'', each hi and lo
+        const uint64_t dT = desc_k(base + none + kAtT), dTW = dT + (2 * kTileT >> 4);  // T', then T'', each hi and lo
         const uint32_t tile = base + stage * kTileKQ;
         const uint64_t dK = desc_k(tile), dKT = desc_mn(tile, 16384);
         uint64_t &kq_full = ctl->kq_full[stage], &kq_free = ctl->kq_free[stage];
@@ -318,17 +319,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (partial && n + 1 == chunks && !wait_warp(ctl->zeroed, 0)) break;
         // T' V, while S is made
         if (!wait_warp(ctl->t_full, n)) break;
-        if (!run.identity && !wait_warp(ctl->v_full[n % kV], n / kV)) break;
+        if (!run.identity && !wait_warp(ctl->v_full[n & v_last], n >> v_last)) break;
         if (n > 0 && !wait_warp(ctl->d_done, n - 1)) break;  // U' of chunk n - 1 is read
         if (!run.identity) {
           tc_fence_after();
-          const uint64_t dV = desc_mn(base + F::oV + n % kV * kTileV, 8192);
+          const uint64_t dV = desc_mn(base + kAtV + (n & v_last) * kBlockV, kBlockV);
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) {
             mma_ss(leader, tU, dV + 128 * ks, dT + 2 * ks, iV, ks > 0);
             mma_ss(leader, tU, dV + 128 * ks, dT + (kTileT >> 4) + 2 * ks, iV, 1);
           }
-          mma_commit(leader, ctl->v_free[n % kV]);
+          mma_commit(leader, ctl->v_free[n & v_last]);
         }
         // Each product begins with the steps whose operands come first: S, X and U' by halves of each thread's
         // columns (steps 0, 1, 4, 5 of S, then 2, 3, 6, 7; steps 0, 2, then 1, 3 of the tokens).
@@ -388,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool leader = elect_lane();
       const uint32_t base = smem_u32(smem);
       constexpr uint32_t i64 = umma_idesc_bf16(128, 64, false, false, false);
+      constexpr uint32_t i32 = umma_idesc_bf16(128, 32, false, false, false);
       const uint64_t dKQ = desc_k(base);
       auto gram = [&](int n) -> bool {  // rows 0 .. 63: K K^T, 64 .. 127: Q K^T
         if (!wait_warp(ctl->kq_full[n % kKQ], n / kKQ)) return false;
@@ -423,14 +425,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ts(leader, tXQ, tS + 16 * ks + 8, b, i64, 1);
         }
         mma_commit(leader, ctl->xq_done);
-        const uint64_t dPn = desc_k(base + F::oP) + n % kP * (F::kTileP >> 4);
+        const uint64_t dPn = desc_k(base + kAtP) + n % kP * (kTileP >> 4);
         if (!wait_warp(ctl->d_done, n)) break;  // (U for the read-out came before)
         tc_fence_after();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
-          mma_ts(leader, tO, tUH + 8 * ks, dPn + 2 * ks, i64, ks > 0);
-          mma_ts(leader, tO, tUH + 32 + 8 * ks, dPn + 2 * ks, i64, 1);
-          if constexpr (kPair) mma_ts(leader, tO, tUH + 8 * ks, dPn + (kTileT >> 4) + 2 * ks, i64, 1);
+          const uint32_t hi = tUH + 8 * ks, lo = hi + 32;
+          if (ks < 2) {  // both halves of the rows; then lo's upper half
+            mma_ts(leader, tO, hi, dPn + 2 * ks, i64, ks > 0);
+            mma_ts(leader, tO, lo, dPn + 2 * ks, i64, 1);
+            mma_ts(leader, tO, hi, dPn + 2 * ks + 4, i32, 1);
+          } else {
+            mma_ts(leader, tO + 32, hi, dPn + 2 * ks + (4096 >> 4), i32, 1);
+            mma_ts(leader, tO + 32, lo, dPn + 2 * ks + (4096 >> 4), i32, 1);
+          }
+          mma_ts(leader, tO + 32, hi, dPn + 2 * ks + (8192 >> 4), i32, 1);
         }
         mma_commit(leader, ctl->o_done);
         mma_commit(leader, ctl->p_free[n % kP]);
@@ -486,21 +495,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     registers_down<72>();
     // ---- A, its inverse and P: warps 4 to 7 of the even chunks, 8 to 11 of the odd ones
     const int w = warp & 3, group = (warp >> 2) - 1, wt = tid & 127;
-    float *const sA = reinterpret_cast<float *>(smem + F::oA) + group * (kC * kStrideA);
+    float *const sA = reinterpret_cast<float *>(smem + kAtA) + group * (kC * kStrideA);
     const uint32_t row = uint32_t(32 * w) << 16;
     const int hb = w & 1, t = 32 * hb + lane;  // this thread's row of K K^T (warps 0, 1) or Q K^T (2, 3)
     auto sync = [&]() { named_bar_sync(1 + group, 128); };
     auto sync_pair = [&]() { named_bar_sync(3 + 2 * group + (w >> 1), 64); };
-    // what lies above the diagonal block of T' and P is zero and stays it (both groups write it)
-    for (int i = wt; i < (4 + kP * (kPair ? 2 : 1)) * 32 * 4; i += 128)
-      *reinterpret_cast<uint4 *>(smem + F::oT + (i >> 7) * kTileT + sw128_chunk((i >> 2) & 31, 4 + (i & 3), 0, kC)) =
+    // what lies above the diagonal blocks of T' and T'' is zero and stays it (both groups write it)
+    for (int i = wt; i < 4 * 32 * 4; i += 128)
+      *reinterpret_cast<uint4 *>(smem + kAtT + (i >> 7) * kTileT + sw128_chunk((i >> 2) & 31, 4 + (i & 3), 0, kC)) =
           make_uint4(0, 0, 0, 0);
     // rows of the last chunk behind the run: another sequence's, whose infinities times zero would not vanish
-    auto clear_rows = [&](uint8_t *tile, uint32_t block, int part) {
+    auto clear_rows = [&](uint8_t *tile, uint32_t block, int blocks, int part) {
 #pragma unroll 1
       for (int i = part * 8 + wt; i < kC * 8; i += 128) {  // 16-byte pieces of a 64-channel block
         *reinterpret_cast<uint4 *>(tile + i * 16) = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(tile + block + i * 16) = make_uint4(0, 0, 0, 0);
+        if (blocks > 1) *reinterpret_cast<uint4 *>(tile + block + i * 16) = make_uint4(0, 0, 0, 0);
       }
       fence_proxy_async_smem();
     };
@@ -510,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool clear = partial && n + 1 == chunks;
       if (clear) {
         ok = wait_warp(ctl->kq_full[n % kKQ], n / kKQ);
-        if (ok) clear_rows(smem + n % kKQ * kTileKQ, 16384, len - n * kC);
+        if (ok) clear_rows(smem + n % kKQ * kTileKQ, 16384, kb, len - n * kC);
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->zeroed);
       }
@@ -524,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int end = w < 2 ? t : run.emit ? t + 1 : 0;
       const float factor = w < 2 ? tb.beta[t] : a.scale;
       const float2 g2 = make_float2(tb.g[t], tb.g[t]), l2 = make_float2(tb.g_lo[t], tb.g_lo[t]);
-      uint8_t *P = smem + F::oP + n % kP * F::kTileP;
+      uint8_t *P = smem + kAtP + n % kP * kTileP;
 #pragma unroll 1
       for (int c = 0; c < 32 * hb + 32; c += 16) {
         float x[16];
@@ -562,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e) split_pair(x[j + 2 * e], x[j + 2 * e + 1], hi[e], lo[e]);
             const uint32_t o = sw128_chunk(t, (c + j) >> 3, 0, kC);
             *reinterpret_cast<uint4 *>(P + o) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if constexpr (kPair) *reinterpret_cast<uint4 *>(P + kTileT + o) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4 *>(P + (hb == 0 ? o ^ 64 : o + 4096)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
         }
       }
@@ -645,14 +654,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // each lower one. Their buffers: the products of chunk n - 1 are done.
       ok = n == 0 || wait_warp(ctl->t_free[(n - 1) & 1], (n - 1) >> 1);
       if (clear && !run.identity) {
-        ok = ok && wait_warp(ctl->v_full[n % kV], n / kV);
-        if (ok) clear_rows(smem + F::oV + n % kV * kTileV, 8192, len - n * kC);
+        ok = ok && wait_warp(ctl->v_full[n & v_last], n >> v_last);
+        if (ok) clear_rows(smem + kAtV + (n & v_last) * kBlockV, kBlockV, vb, len - n * kC);
       }
       if (named_bar_or(1 + group, 128, !ok)) break;
 #pragma unroll 1
       for (int m = 0; m < 3; ++m) {
         const int r = m == 0 ? wt >> 2 : 32 + (((m - 1) * 128 + wt) >> 3), c = 8 * (m == 0 ? wt & 3 : wt & 7);
-        uint8_t *T = smem + F::oT + sw128_chunk(r, c >> 3, 0, kC);
+        uint8_t *T = smem + kAtT + sw128_chunk(r, c >> 3, 0, kC);
         float2 y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -862,8 +871,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <bool kOutBF16>
 cudaError_t launch_pass(const CUtensorMap &mq, const CUtensorMap &mk, const CUtensorMap &mv, const DeltaArgs &a, int pass,
                         cudaStream_t stream) {
-  constexpr uint32_t smem = Cfg<kOutBF16>::bytes;
-  static_assert(smem <= 232448, "shared memory of one CTA");
   const auto kern = delta_chunked_kernel<kOutBF16>;
   // the kernel's shared memory, granted once per device (bit d for device d; past 63 at every launch)
   static std::atomic<uint64_t> granted;
@@ -872,12 +879,12 @@ cudaError_t launch_pass(const CUtensorMap &mq, const CUtensorMap &mk, const CUte
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (bit == 0 || (granted.load(std::memory_order_acquire) & bit) == 0) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kBytes));
     if (e != cudaSuccess) return e;
     granted.fetch_or(bit, std::memory_order_release);
   }
   const unsigned pieces = unsigned(a.plan.inner + a.num_seqs) + (pass == 1 && a.plan.seg_len != 0 ? unsigned(a.plan.inner) : 0u);
-  kern<<<pieces * unsigned(a.H), kThreads, smem, stream>>>(mq, mk, mv, a, pass, device_error_word());
+  kern<<<pieces * unsigned(a.H), kThreads, kBytes, stream>>>(mq, mk, mv, a, pass, device_error_word());
   return cudaGetLastError();
 }
 
