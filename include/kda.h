@@ -612,7 +612,8 @@ size_t kda_delta_prefill_workspace_size(int64_t total_tokens, int32_t num_seqs, 
  * rot_dim even and <= d, 1 <= num_axes <= 4, 1 <= H_q <= 65535, H_k <= 65535. eps finite and >= 0; a row
  * of zeros with eps = 0 gives NaN, as the formula does. Squares are summed in fp32, so rows that are
  * normalised hold values below 1e17 (beyond, the sum may overflow and the row becomes 0), and with eps =
- * 0 some above 1e-18. An angle is exact to 2^-32 of a turn while |inv_freq| is below 2^24; the result is
+ * 0 some above 1e-18. An angle is exact to 2^-32 of a turn at every position while |inv_freq| is below
+ * 2^24, and its sine and cosine are those of what fp32 holds of it, within 2^-28 of a turn; the result is
  * rounded once. An infinite or NaN inv_freq gives NaN for its pair.
  */
 typedef enum { KDA_NORM_NONE = 0, KDA_NORM_RMS = 1, KDA_NORM_L2 = 2 } kda_norm_form;

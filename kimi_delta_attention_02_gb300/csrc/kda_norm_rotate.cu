@@ -11,10 +11,10 @@
 // or comes by a second load, which finds its line in L1.
 //
 // Angles. p = position * f can be millions of radians, where fp32 is off by tenths. A turn is a number
-// modulo one: F = f / (2 pi) modulo one as a 64-bit fraction (off by 2^-63 while f is below 2^24), and the
-// wrapping 64-bit product position * F is the angle's fraction of a turn whatever the position, negative
-// ones among them (off by position 2^-63). Its top 32 bits, as a signed number of half turns, go to
-// sincospi: off by 2^-32 of a turn.
+// modulo one: F = f / (2 pi) modulo one as a 128-bit fraction (off by 2^-104 while f is below 2^24), and the
+// upper 64 bits of the wrapping product |position| F are the angle's fraction of a turn, off by 2^-41 at the
+// furthest of 64-bit positions. The nearest quarter turn is taken off in integers, so that what fp32 holds of
+// the rest, at most an eighth, is off by 2^-28 of a turn (all of a turn's fraction in 24 bits by 2^-26).
 #include "kda_common.cuh"
 #include "kda_norm_rotate.h"
 
@@ -23,24 +23,36 @@ namespace {
 
 constexpr int kThr = 256;
 
-// The angle of pair i at token t as (cos, sin); `turns` is the pair's F.
-__device__ __forceinline__ uint64_t turns_per_position(float inv_freq) {
-  // |f| = m 2^-s with a whole m, times 1 / (2 pi) as 128 bits behind the point; all in integers
+using Turns = unsigned __int128;  // the fraction of a turn, behind the point
+
+__device__ __forceinline__ Turns turns_per_position(float inv_freq) {
+  // |f| = m 2^-s with a whole m, times 1 / (2 pi) with 128 bits behind the point; all in integers
   const uint32_t bits = __float_as_uint(inv_freq) & 0x7fffffffu, exponent = bits >> 23;
   const uint64_t m = (bits & 0x7fffffu) | (exponent != 0 ? 0x800000u : 0u);
   const int s = 150 - int(exponent != 0 ? exponent : 1);
   constexpr uint64_t k1 = 0x28be60db9391054aull, k0 = 0x7f09d5f47d4d3770ull;  // 1 / (2 pi)
-  const uint64_t low = m * k1 + __umul64hi(m, k0), high = __umul64hi(m, k1) + (low < m * k1);  // m / (2 pi) 2^64
-  uint64_t f = s <= 0 ? (s > -64 ? low << -s : 0) : s < 64 ? (low >> s) | (high << (64 - s)) : s < 128 ? high >> (s - 64) : 0;
-  return inv_freq < 0.f ? uint64_t(0) - f : f;
+  const Turns upper = Turns(m) * k1 + __umul64hi(m, k0);
+  const Turns low = (upper << 64) | (m * k0), high = upper >> 64;  // m / (2 pi) 2^128
+  const Turns f = s <= 0 ? (s > -128 ? low << -s : 0) : s < 128 ? (low >> s) | (high << (128 - s)) : high >> (s - 128);
+  return inv_freq < 0.f ? 0 - f : f;
 }
-__device__ __forceinline__ float2 angle(const RotateArgs &a, int i, int64_t t, uint64_t turns) {
+// The angle of pair i at token t as (cos, sin); `turns` is the pair's F.
+__device__ __forceinline__ float2 angle(const RotateArgs &a, int i, int64_t t, Turns turns) {
   const int64_t at = a.axis[i] * a.tokens + t;
   const int64_t pos = a.pos64 ? static_cast<const int64_t *>(a.positions)[at]
                               : int64_t(static_cast<const int32_t *>(a.positions)[at]);
-  const int32_t turn = int32_t((uint64_t(pos) * turns) >> 32);
+  const uint64_t far = pos < 0 ? uint64_t(0) - uint64_t(pos) : uint64_t(pos);
+  uint64_t turn = far * uint64_t(turns >> 64) + __umul64hi(far, uint64_t(turns));
+  if (pos < 0) turn = uint64_t(0) - turn;
+  const uint32_t quarter = uint32_t((turn + (uint64_t(1) << 61)) >> 62);  // the nearest; 4 is 0
+  const int32_t rest = int32_t(int64_t(turn - (uint64_t(quarter) << 62)) >> 30);  // in 2^-34 of a turn
   float s, c;
-  sincospif(float(turn) * 0x1p-31f, &s, &c);
+  sincospif(float(rest) * 0x1p-33f, &s, &c);
+  if (quarter & 1) {
+    const float x = c;
+    c = -s, s = x;
+  }
+  if (quarter & 2) c = -c, s = -s;
   if (!isfinite(a.inv_freq[i])) s = c = __int_as_float(0x7fc00000);
   return make_float2(c, s);
 }
@@ -89,7 +101,7 @@ __global__ void __launch_bounds__(kThr, 3) rotate_kernel(const RotateArgs a, int
   constexpr int kEi = kInBF16 ? 2 : 4, kEo = kOutBF16 ? 2 : 4;
   constexpr int kU = kInBF16 ? 2 : 1;  // rows at a time, and as many on their way
   constexpr bool kNear = kPart == 0 || kPart == 2, kSome = kPart == 1 || kPart == 2;
-  __shared__ uint64_t s_turn[kRotateMaxD / 2];
+  __shared__ Turns s_turn[kRotateMaxD / 2];
   __shared__ __align__(16) float2 s_cs[2][kThr * 4];  // tokens x rot / 2: a row has at most 8 channels per lane
   const int tid = threadIdx.x, lane = tid & 31;
   const int per_warp = 32 / lanes, slots = kThr / 32 * per_warp;  // (lanes behind a warp's last row take part in shuffles only)
@@ -248,7 +260,7 @@ __global__ void __launch_bounds__(kThr, 3) rotate_kernel(const RotateArgs a, int
 template <bool kInBF16, bool kOutBF16, int kPer>
 __global__ void __launch_bounds__(kThr) rotate_any_kernel(const RotateArgs a, int interleaved) {
   const int lane = threadIdx.x & 31;
-  uint64_t turns[kPer];
+  Turns turns[kPer];
   int ch[kPer], ph[kPer];  // the pair's channels, or the row's end
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
