@@ -518,19 +518,21 @@ kda_status kda_block_norm(const kda_block_norm_params *params, void *stream);
  *                sequences of unlike lengths start longest first, and bf16 head sizes that are no
  *                multiple of 8 are padded for the tensor-core kernel; with less, every (sequence,
  *                head) runs from end to end in the order given, and such head sizes run the
- *                token-recurrent kernel. It may not be shared by calls that run at
- *                the same time (two captured graphs that may replay together need one each).
+ *                token-recurrent kernel. force_recurrent cuts nothing and asks for none. It may not
+ *                be shared by calls that run at the same time (two captured graphs that may replay
+ *                together need one each).
  *
  * bf16 prompts run a tensor-core kernel in chunks of 64 tokens, unless d_k is at most 16 (8 with a
- * bf16 output; few key channels would lose precision in pairs), their sequences are short (fewer
- * than 6 to 88 tokens on average, by head sizes and the number of sequences and heads; empty
- * sequences count) or H d_v is above 2^25. Its products read the state and what is formed for it
- * as pairs of bf16 (2^-17), so that final states and outputs (a bf16 one before it is rounded) are off
- * by some 1e-5 of themselves (in the 2-norm). A log_decay below -88 counts as -88. An infinity or NaN
- * in a channel of v reaches that value channel of every output of its chunk in that (sequence, head),
- * and what follows; one in k, beta or log_decay every channel of the same; one in q its own token's
- * output. fp32 inputs, short sequences, and sequences of up to 5 or 12 tokens beside many others run in
- * fp32 token by token, where they reach only what depends on them.
+ * bf16 output; few random keys are less orthogonal and lose more in pairs), their sequences are short
+ * (fewer than 6 to 88 tokens on average, by head sizes and the number of sequences and heads; empty
+ * sequences count) or H d_v is above 2^25. Its products read the state and what is formed for it as
+ * pairs of bf16 (2^-17), so that final states and outputs (a bf16 one before it is rounded) are off by
+ * some 1e-5 of themselves in the 2-norm where keys are random, by up to 2e-5 (states) and 3e-5
+ * (outputs) where they share a direction; with force_recurrent by 4e-7. A log_decay below -88 counts
+ * as -88. An infinity or NaN in a channel of v reaches that value channel of every output of its chunk
+ * in that (sequence, head), and what follows; one in k, beta or log_decay every channel of the same;
+ * one in q its own token's output. fp32 inputs, short sequences, and sequences of up to 5 or 12 tokens
+ * beside many others run in fp32 token by token, where they reach only what depends on them.
  *
  * Results are accumulated in fp32 and states are fp32.
  */

@@ -30,10 +30,10 @@
 // every other chunk each, one to two chunks ahead; 12-15 write the output; 16-23 keep the state (a value
 // channel and half of the key rows per thread) and form the chain's operands.
 //
-// What bounds it: the chain's latency. A chunk takes 3.9 us (T = 4096, 96 heads of 128: 250 us for 64 of them,
-// against 63 us to move the bytes and 2.41 ms of the token kernel), of which the three products take 0.8 us
+// What bounds it: the chain's latency. A chunk takes 4.1 us (T = 4096, 96 heads of 128: 262 us for 64 of them,
+// against 63 us to move the bytes and 2.0 ms of the token kernel), of which the three products take 0.8 us
 // and the hand-overs between MMA and warps (six, 0.15 to 0.2 us each) and the splitting of X, U' and S the
-// rest, in competition with warps 4 to 11 for the issue slots: 203 us with those idle. (4.6 us a chunk with all
+// rest, in competition with warps 4 to 11 for the issue slots: 203 us of 256 with those idle. (4.7 us a chunk with all
 // SMs busy: the roles' 85 KB of code share an instruction cache.) Hence two halves per
 // hand-over, so that a product starts on the first half, and V's product and the read-out off the chain.
 #include <atomic>

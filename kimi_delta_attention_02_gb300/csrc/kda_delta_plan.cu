@@ -101,28 +101,29 @@ cudaError_t launch_delta_chain(const DeltaArgs &a, cudaStream_t stream) {
 
 // The tensor-core kernel takes a chunk of 64 tokens' time for the shortest sequence, so calls of short ones go
 // to the token kernel: below `least` tokens a sequence on average. us by the token kernel / this one at 8, 16,
-// 32, 64 and 100 tokens; 16 sequences of 64 heads: 128 x 128 103/91, 134/91, 200/93, 329/96; 64 x 128 68/84, 82/84,
-// 125/84; 128 x 64 54/88, 68/88, 105/90, 173/92; 64 x 64, where a warp holds a whole state, 35/82, 43/83,
-// 66/84, 107/83. Fewer chains than SMs (3 sequences of 8 heads): 128 x 128 9/15, 11/15, 13/15, 19/15; 64 x 64
-// 6/13, 7/13, 9/13, 12/13, 16/17. TMA needs rows of whole 16-byte pieces, so other head sizes run on padded
-// copies of q, k and v in the workspace, or without one in the token kernel (4096 tokens, 96 heads of 100: 345 us
-// by copies, 2099 by the token kernel; 32 heads of 68: 209, 835).
+// 32, 64 and 100 tokens; 16 sequences of 64 heads: 128 x 128 103/93, 132/93, 198/94, 326/97; 64 x 128 70/86, 86/86,
+// 133/88; 128 x 64 54/90, 70/90, 106/92, 172/93; 64 x 64, where a warp holds a whole state, 36/84, 43/84,
+// 66/85, 111/86. Fewer chains than SMs (3 sequences of 8 heads): 128 x 128 9/15, 11/15, 13/15, 19/15; 64 x 64
+// 7/14, 7/14, 9/14, 13/13, 17/17. TMA needs rows of whole 16-byte pieces, so other head sizes run on padded
+// copies of q, k and v in the workspace, or without one in the token kernel (4096 tokens, 96 heads of 100: 348 us
+// by copies, 2087 by the token kernel; 32 heads of 68: 215, 828).
 //
-// Few key channels stay in the token kernel, for the precision: the keys of a chunk are far from orthogonal, so
+// Few key channels stay in the token kernel, for the precision: random keys of a chunk are far from orthogonal, so
 // that T' V and T'' X are larger than their sum, and their pairs' roundings reach 1.1e-5 of fp32 outputs and 1.0e-5 of
-// states in the 2-norm (d_k = 5 and 6; from 9 on 8.3e-6 of states, from 17 on 8.0e-6 of outputs; 3e-7 by the token
-// kernel). 4096 tokens, 96 heads of 16 x 128: 1259 us there, 240 here.
+// states in the 2-norm (d_k = 5 and 6; from 9 on 8.3e-6 of states, from 17 on 9.1e-6 of outputs; 3e-7 by the token
+// kernel). 4096 tokens, 96 heads of 16 x 128: 1197 us there, 237 here. It is a rule for random keys: ones that share a
+// direction are no more orthogonal in 128 channels than in few, and come to 3e-5 of outputs and 2e-5 of states at any d_k.
 //
 // The shortest sequences go to the decode kernel, which holds no more than a state and is bound by its bytes, where
 // there are more chains than SMs and the mean length says that there may be some: those of up to `few` tokens. us
 // by the token kernel / that one at 1, 4, 8 and 16 tokens, 128 sequences of 64 heads: 128 x 128 754/219, 764/468,
-// 798/808, 1019/1499 (the tensor cores: 667); 64 x 64 250/72, 252/121, 277/195, 336/347 (640 by the tensor cores).
+// 798/808, 1019/1499 (the tensor cores: 651); 64 x 64 250/72, 252/121, 277/195, 336/347 (597 by the tensor cores).
 //
 // A CTA holds one (sequence, head) from end to end, one CTA per SM, so few long sequences leave SMs idle. A
 // sequence cut into m segments runs 2 m - 3 of them side by side in pass 1 and m - 1 in pass 3: two segments'
 // time instead of m, for up to three times the work. Of a single sequence m is that of the least time by
 // waves of CTAs: a chunk of 64 tokens takes some 4 us, a step of pass 2 five, a pass ten to begin and end (T =
-// 65536, 16 heads: m = 10, 1335 us; m = 6: 1378 us; not cut: some 3100). Of several the lengths are not known
+// 65536, 16 heads: m = 10, 1268 us; m = 6: 1354 us; not cut: 3870). Of several the lengths are not known
 // here, and cuts lie so far apart that pass 1 fills the SMs at most twice. Sequences in more chains than SMs run
 // longest first.
 DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d_v, bool in_bf16, bool out_bf16,
@@ -187,7 +188,7 @@ DeltaPlan delta_plan(int64_t total, int num_seqs, int H, int H_k, int d_k, int d
   len = (len + 63) / 64 * 64;
   if (len > 0 && len < 512) len = 512;
   // (room for three segments; and cuts that most sequences are too short for would only cost the order of the
-  // others: 323 us instead of 280 for prompts of 4096 tokens and less on 32 heads, cut at 4672)
+  // others: 301 us instead of 273 for prompts of 4096 tokens and less on 32 heads, cut at 4672)
   if (len > 0 && total >= 3 * len - 63 * 3 && 8 * total >= len * num_seqs) {
     if (room(len)) return p;
   }

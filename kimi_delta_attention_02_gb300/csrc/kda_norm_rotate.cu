@@ -3,7 +3,7 @@
 // one), a = w cos p and b = -+ w_partner sin p of the token's angles, which all heads share.
 //
 // Reads and writes q and k once at about 7 flops per element: bound by HBM bandwidth (4096 tokens, 192 heads
-// of 128, bf16: 403 MB in 80 us, 5 TB/s; the copy rate would be 60 us), by latency for a few tokens (one token:
+// of 128, bf16: 403 MB in 82 us, 4.9 TB/s; the copy rate would be 60 us), by latency for a few tokens (one token:
 // 6 us). The angles of a token are formed once per CTA, in shared memory. A head row takes as many lanes as it
 // has pieces of 8 channels, so that a warp works on up to 32 rows at once (10007 tokens, 20 heads of 72: 23 us; 31
 // with lanes in powers of two). A lane keeps the factors of its channels in registers while it goes through the
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kThr, 3) rotate_kernel(const RotateArgs a, int
 // and step (kPer of them: the pairs that turn, then neighbours of those that do not), element by element. A
 // warp keeps a token's factors in registers while it goes through its share of the token's heads (blockIdx.y).
 // Bound by its 2-byte accesses: the sizes above take 189 us here, and 10007 tokens of 20 heads of 72 take 45 us
-// (31 us by whole pieces), so rows that allow it go there.
+// (23 us by whole pieces), so rows that allow it go there.
 template <bool kInBF16, bool kOutBF16, int kPer>
 __global__ void __launch_bounds__(kThr) rotate_any_kernel(const RotateArgs a, int interleaved) {
   const int lane = threadIdx.x & 31;
